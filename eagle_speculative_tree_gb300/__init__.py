@@ -24,9 +24,10 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_E4M3 = 0, 1, 2
 KERNEL_AUTO, KERNEL_SIMT, KERNEL_TC, KERNEL_TC_PAIR, KERNEL_TC_2SM, KERNEL_TC_STREAM = 0, 1, 2, 3, 4, 5
 ACCEPT_AUTO, ACCEPT_ALL_ROWS, ACCEPT_PATH_ONLY = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ABSENT = -2                     # parent entry of a padding slot after a smaller tree
 STATUS_BITS = {1: "BAD_PARENT", 2: "BAD_PAGE", 4: "BAD_LENGTH", 8: "BAD_TOKEN", 16: "TIMEOUT", 32: "INTERNAL",
                64: "BAD_PATH"}
@@ -41,6 +42,18 @@ class AttnShape(ctypes.Structure):
 class AttnPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "kernel", "num_splits", "split_tokens", "rows_per_block", "row_blocks", "merge")]
+
+
+class ChunkShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_tokens", "num_q_heads", "num_kv_heads", "head_dim", "page_size",
+        "max_pages_per_seq", "num_pool_pages", "dtype", "kv_dtype", "kernel")]
+
+
+class AppendOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q_norm", "k_norm", "inv_freq", "positions")] + \
+        [(n, ctypes.c_float) for n in ("norm_eps", "rope_scale")] + \
+        [(n, ctypes.c_int32) for n in ("rot_dim", "layout")]
 
 
 _vp, _i32p, _f32p = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p
@@ -70,6 +83,21 @@ _lib.tree_rerank.argtypes = [_vp] * 3 + [ctypes.c_int32] * 3 + [_vp] * 3 + [ctyp
 _lib.tree_rerank.restype = ctypes.c_int
 _lib.tree_rerank_pool.argtypes = [_vp] * 4 + [ctypes.c_int32] * 4 + [_vp] * 3 + [ctypes.c_size_t, _vp]
 _lib.tree_rerank_pool.restype = ctypes.c_int
+_lib.treespec_append_workspace_bytes.argtypes = []
+_lib.treespec_append_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_chunk_append.argtypes = [_vp, ctypes.c_int64] * 3 + [_vp] * 8 + \
+    [ctypes.POINTER(ChunkShape), ctypes.POINTER(AppendOptions), _vp, ctypes.c_size_t, _vp]
+_lib.tree_chunk_append.restype = ctypes.c_int
+_lib.treespec_chunk_attn_workspace_bytes.argtypes = [ctypes.POINTER(ChunkShape)]
+_lib.treespec_chunk_attn_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_chunk_attn.argtypes = [_vp] * 9 + [ctypes.POINTER(ChunkShape), _vp, ctypes.c_size_t, _vp]
+_lib.tree_chunk_attn.restype = ctypes.c_int
+_lib.treespec_attn_e4m3_workspace_bytes.argtypes = [ctypes.POINTER(AttnShape)]
+_lib.treespec_attn_e4m3_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_attn_verify_e4m3.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnShape), _vp, ctypes.c_size_t, _vp]
+_lib.tree_attn_verify_e4m3.restype = ctypes.c_int
+_lib.tree_kv_commit_e4m3.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnShape), _vp, ctypes.c_size_t, _vp]
+_lib.tree_kv_commit_e4m3.restype = ctypes.c_int
 _lib.treespec_read_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.treespec_read_status.restype = ctypes.c_int
 _lib.treespec_error_string.argtypes = [ctypes.c_int]
@@ -364,6 +392,276 @@ def tree_rerank(node_parent, node_token, node_score, num_nodes: int, tree_parent
                                      pool.shape[1], B, M, num_nodes, _ptr(tree_parents), _ptr(draft_tokens),
                                      _ptr(workspace), workspace.numel(), _stream_handle(stream, dev)))
     return tree_parents, draft_tokens
+
+
+# ------------------------------------------------- chunks of new tokens, 8-bit cache
+
+class _on_device:
+    """The library launches on the current device: make it the tensors' own for a call."""
+
+    def __init__(self, device):
+        here = torch.cuda.current_device()
+        self._guard = None if device.index is None or device.index == here else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _fresh(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that a call makes for itself, out of the memory of the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace_for(workspace, need: int, device, stream) -> torch.Tensor:
+    if workspace is None:
+        return _fresh((need,), torch.uint8, device, stream)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace
+
+
+def _need_shape(t: torch.Tensor, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_pools(q_dtype, k_pages, v_pages, k_scales, v_scales, device) -> int:
+    """Checks a pair of page pools and their scales; returns the pools' DTYPE_*."""
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    want = torch.float8_e4m3fn if e4m3 else q_dtype
+    _need(k_pages, "k_pages", want, device)
+    _need(v_pages, "v_pages", want, device)
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must have shape [pages][16][kv heads][head_dim]")
+    _need_shape(v_pages, "v_pages", k_pages.shape)
+    if e4m3:
+        P, ps, Hkv, _ = k_pages.shape
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if t is None:
+                raise ValueError(f"{name} is needed with float8_e4m3fn pools")
+            _need(t, name, torch.float32, device)
+            _need_shape(t, name, (P, Hkv, ps))
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("scales belong to float8_e4m3fn pools only")
+    return DTYPE_E4M3 if e4m3 else DTYPE_BF16 if q_dtype == torch.bfloat16 else DTYPE_F32
+
+
+@dataclass
+class ChunkProblem:
+    batch: int
+    num_tokens: int
+    num_q_heads: int
+    num_kv_heads: int
+    head_dim: int
+    page_size: int
+    max_pages_per_seq: int
+    num_pool_pages: int
+    dtype: int
+    kv_dtype: int
+    kernel: int = KERNEL_AUTO
+
+    def c_shape(self) -> ChunkShape:
+        return ChunkShape(self.batch, self.num_tokens, self.num_q_heads, self.num_kv_heads, self.head_dim,
+                          self.page_size, self.max_pages_per_seq, self.num_pool_pages, self.dtype, self.kv_dtype,
+                          self.kernel)
+
+
+def chunk_problem(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, chunk_offsets: torch.Tensor, *,
+                  kernel: int = KERNEL_AUTO) -> ChunkProblem:
+    """Sizes of a tree_chunk_attn / tree_chunk_append call: q [T][Hq][D], page_table [B][max_pages]."""
+    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or chunk_offsets.dim() != 1:
+        raise ValueError("q is [tokens][heads][head_dim], k_pages [pages][16][kv heads][head_dim], "
+                         "page_table [batch][pages], chunk_offsets [batch + 1]")
+    T, Hq, D = q.shape
+    P, ps, Hkv, D2 = k_pages.shape
+    if D2 != D:
+        raise ValueError("head_dim of q and k_pages differ")
+    B = page_table.shape[0]
+    _need_shape(chunk_offsets, "chunk_offsets", (B + 1,))
+    dt = DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F32
+    kv = DTYPE_E4M3 if k_pages.dtype == torch.float8_e4m3fn else dt
+    return ChunkProblem(B, T, Hq, Hkv, D, ps, page_table.shape[1], P, dt, kv, kernel)
+
+
+def append_workspace_bytes() -> int:
+    return int(_lib.treespec_append_workspace_bytes())
+
+
+def tree_chunk_append(q, k, v, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, q_out=None, *,
+                      positions=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6, inv_freq=None,
+                      rope: int = ROPE_HALF, rope_scale: float = 1.0, k_scales=None, v_scales=None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Norm, rotary positions and the write of new tokens into the page pools; see
+    include/treespec.h for the operation.
+
+    q [T][Hq][D], k / v [T][Hkv][D] (float32 or bfloat16; views whose heads are contiguous,
+    such as slices of one projection's output), k_pages / v_pages [P][16][Hkv][D] in the
+    same type or float8_e4m3fn with k_scales / v_scales [P][Hkv][16] float32, page_table
+    [B][max_pages], prefix_lens [B], chunk_offsets [B + 1], positions [T] (int32),
+    q_norm / k_norm [D] and inv_freq [rot_dim / 2] float32 (None: no norm, no rotation).
+    Returns q_out [T][Hq][D] (q itself may be given); the pools are written in place.  Rows
+    that are left out stay as they are in `q_out` (and hold nothing of use in a new one)."""
+    dev, dt = q.device, q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("q must be float32 or bfloat16")
+    prob = chunk_problem(q, k_pages, page_table, chunk_offsets)
+    T, Hq, D, Hkv = prob.num_tokens, prob.num_q_heads, prob.head_dim, prob.num_kv_heads
+    for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        if not t.is_cuda or t.device != dev or t.dtype != dt:
+            raise ValueError(f"{name} must be {dt} on {dev}")
+        _need_shape(t, name, (T, H, D))
+        if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
+    ints = [("page_table", page_table), ("prefix_lens", prefix_lens), ("chunk_offsets", chunk_offsets)]
+    if positions is not None:
+        ints.append(("positions", positions))
+        _need_shape(positions, "positions", (T,))
+    for name, t in ints:
+        _need(t, name, torch.int32, dev)
+    _need_shape(prefix_lens, "prefix_lens", (prob.batch,))
+    for name, t, n in (("q_norm", q_norm, D), ("k_norm", k_norm, D), ("inv_freq", inv_freq, None)):
+        if t is not None:
+            _need(t, name, torch.float32, dev)
+            _need_shape(t, name, (t.numel() if n is None else n,))
+    # one token has no distance to the next: its rows count as packed
+    strides = [t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v)]
+    if q_out is None:
+        q_out = _fresh((T, Hq, D), dt, dev, stream)
+    _need(q_out, "q_out", dt, dev)
+    _need_shape(q_out, "q_out", (T, Hq, D))
+    workspace = _workspace_for(workspace, append_workspace_bytes(), dev, stream)
+    opt = AppendOptions(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), _ptr(positions), float(norm_eps), float(rope_scale),
+                        0 if inv_freq is None else 2 * inv_freq.numel(), int(rope))
+    with _on_device(dev):
+        _check(_lib.tree_chunk_append(
+            _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
+            _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens), _ptr(chunk_offsets),
+            ctypes.byref(prob.c_shape()), ctypes.byref(opt), _ptr(workspace), workspace.nbytes,
+            _stream_handle(stream, dev)))
+    return q_out
+
+
+def chunk_attn_workspace_bytes(prob: ChunkProblem) -> int:
+    n = _lib.treespec_chunk_attn_workspace_bytes(ctypes.byref(prob.c_shape()))
+    if n == 0:
+        raise ValueError(f"unsupported chunk attention shape {prob}")
+    return int(n)
+
+
+def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, out=None, *, k_scales=None,
+                    v_scales=None, kernel: int = KERNEL_AUTO, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Causal attention of packed new tokens over the paged cache that holds them already;
+    see include/treespec.h for the operation.
+
+    q [T][Hq][D] (float32 or bfloat16), k_pages / v_pages [P][16][Hkv][D] in the same type
+    or float8_e4m3fn with k_scales / v_scales [P][Hkv][16] float32, page_table [B][max_pages],
+    prefix_lens [B], chunk_offsets [B + 1] int32.  Returns out [T][Hq][D] in q's dtype; rows
+    that belong to no sequence are left as they are in `out` (and hold nothing of use in a
+    new one)."""
+    dev, dt = q.device, q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("q must be float32 or bfloat16")
+    _need(q, "q", dt, dev)
+    prob = chunk_problem(q, k_pages, page_table, chunk_offsets, kernel=kernel)
+    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
+    for name, t in (("page_table", page_table), ("prefix_lens", prefix_lens), ("chunk_offsets", chunk_offsets)):
+        _need(t, name, torch.int32, dev)
+    _need_shape(prefix_lens, "prefix_lens", (prob.batch,))
+    if out is None:
+        out = _fresh(q.shape, dt, dev, stream)
+    _need(out, "out", dt, dev)
+    _need_shape(out, "out", q.shape)
+    workspace = _workspace_for(workspace, chunk_attn_workspace_bytes(prob), dev, stream)
+    with _on_device(dev):
+        _check(_lib.tree_chunk_attn(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens),
+            _ptr(chunk_offsets), _ptr(out), ctypes.byref(prob.c_shape()), _ptr(workspace), workspace.nbytes,
+            _stream_handle(stream, dev)))
+    return out
+
+
+def attn_e4m3_workspace_bytes(prob: AttnProblem) -> int:
+    n = _lib.treespec_attn_e4m3_workspace_bytes(ctypes.byref(prob.c_shape()))
+    if n == 0:
+        raise ValueError(f"unsupported attention shape {prob}")
+    return int(n)
+
+
+def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out=None, *,
+                          kernel: int = KERNEL_AUTO, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Tree-attention verification over float8_e4m3fn pools; see include/treespec.h.
+
+    q [B][N][Hq][D] (float32 or bfloat16), k_pages / v_pages [P][16][Hkv][D] float8_e4m3fn,
+    k_scales / v_scales [P][Hkv][16] float32, page_table [B][max_pages], prefix_lens [B],
+    tree_parents [B][N] int32.  Returns out [B][N][Hq][D] in q's dtype."""
+    dev, dt = q.device, q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError("q must be float32 or bfloat16")
+    _need(q, "q", dt, dev)
+    if q.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q is [batch][nodes][heads][head_dim], page_table [batch][pages]")
+    if k_pages.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"k_pages must be {torch.float8_e4m3fn}, got {k_pages.dtype}")
+    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
+    prob = attn_problem(q, k_pages, page_table, kernel=kernel)
+    for name, t, shape in (("page_table", page_table, (prob.batch, prob.max_pages_per_seq)),
+                           ("prefix_lens", prefix_lens, (prob.batch,)),
+                           ("tree_parents", tree_parents, (prob.batch, prob.num_nodes))):
+        _need(t, name, torch.int32, dev)
+        _need_shape(t, name, shape)
+    if out is None:
+        out = _fresh(q.shape, dt, dev, stream)
+    _need(out, "out", dt, dev)
+    _need_shape(out, "out", q.shape)
+    workspace = _workspace_for(workspace, attn_e4m3_workspace_bytes(prob), dev, stream)
+    with _on_device(dev):
+        _check(_lib.tree_attn_verify_e4m3(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens),
+            _ptr(tree_parents), _ptr(out), ctypes.byref(prob.c_shape()), _ptr(workspace), workspace.nbytes,
+            _stream_handle(stream, dev)))
+    return out
+
+
+def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, accept_path, accept_len,
+                        new_prefix_lens=None, *, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Move the accepted path's codes and scales next to each prefix, in place; see
+    include/treespec.h.  Pools and scales as for tree_attn_verify_e4m3, the rest as for
+    tree_kv_commit.  Returns new_prefix_lens [B] int32."""
+    dev = k_pages.device
+    if k_pages.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"k_pages must be {torch.float8_e4m3fn}, got {k_pages.dtype}")
+    _need_pools(torch.bfloat16, k_pages, v_pages, k_scales, v_scales, dev)
+    if accept_path.dim() != 2 or page_table.dim() != 2:
+        raise ValueError("accept_path is [batch][nodes], page_table [batch][pages]")
+    B, N = accept_path.shape
+    P, ps, Hkv, D = k_pages.shape
+    for name, t, shape in (("page_table", page_table, (B, page_table.shape[1])), ("prefix_lens", prefix_lens, (B,)),
+                           ("accept_path", accept_path, (B, N)), ("accept_len", accept_len, (B,))):
+        _need(t, name, torch.int32, dev)
+        _need_shape(t, name, shape)
+    shape = AttnShape(B, N, Hkv, Hkv, D, ps, page_table.shape[1], P, DTYPE_BF16, KERNEL_AUTO, 0)
+    if new_prefix_lens is None:
+        new_prefix_lens = _fresh((B,), torch.int32, dev, stream)
+    _need(new_prefix_lens, "new_prefix_lens", torch.int32, dev)
+    _need_shape(new_prefix_lens, "new_prefix_lens", (B,))
+    workspace = _workspace_for(workspace, commit_workspace_bytes(), dev, stream)
+    with _on_device(dev):
+        _check(_lib.tree_kv_commit_e4m3(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
+                                        _ptr(prefix_lens), _ptr(accept_path), _ptr(accept_len), _ptr(new_prefix_lens),
+                                        ctypes.byref(shape), _ptr(workspace), workspace.nbytes,
+                                        _stream_handle(stream, dev)))
+    return new_prefix_lens
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -400,11 +400,12 @@ extern "C" int tree_accept(const float* target_logits, const int32_t* draft_toke
 
 extern "C" size_t treespec_commit_workspace_bytes(void) { return kWsAlign; }
 
-extern "C" int tree_kv_commit(void* k_pages, void* v_pages, const int32_t* page_table,
-                              const int32_t* prefix_lens, const int32_t* accept_path,
-                              const int32_t* accept_len, int32_t* new_prefix_lens,
-                              const treespec_attn_shape* shape, void* workspace, size_t workspace_bytes,
-                              treespec_stream_t stream) {
+namespace {
+// tree_kv_commit (k_scales NULL) and tree_kv_commit_e4m3
+int commit(void* k_pages, void* v_pages, float* k_scales, float* v_scales, const int32_t* page_table,
+           const int32_t* prefix_lens, const int32_t* accept_path, const int32_t* accept_len,
+           int32_t* new_prefix_lens, const treespec_attn_shape* shape, void* workspace, size_t workspace_bytes,
+           treespec_stream_t stream) {
     int rc = check_attn_shape(shape);
     if (rc != TREESPEC_OK) return rc;
     if (!k_pages || !v_pages || !page_table || !prefix_lens || !accept_path || !accept_len || !new_prefix_lens)
@@ -432,12 +433,338 @@ extern "C" int tree_kv_commit(void* k_pages, void* v_pages, const int32_t* page_
     p.ps = s.page_size;
     p.max_pages = s.max_pages_per_seq;
     p.num_pool_pages = s.num_pool_pages;
-    p.elem = s.dtype == TREESPEC_DTYPE_BF16 ? 2 : 4;
+    p.elem = k_scales ? 1 : s.dtype == TREESPEC_DTYPE_BF16 ? 2 : 4;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
     if (launch_kv_commit(p, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
     g_launches++;
     return TREESPEC_OK;
+}
+}  // namespace
+
+extern "C" int tree_kv_commit(void* k_pages, void* v_pages, const int32_t* page_table,
+                              const int32_t* prefix_lens, const int32_t* accept_path,
+                              const int32_t* accept_len, int32_t* new_prefix_lens,
+                              const treespec_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                              treespec_stream_t stream) {
+    return commit(k_pages, v_pages, nullptr, nullptr, page_table, prefix_lens, accept_path, accept_len,
+                  new_prefix_lens, shape, workspace, workspace_bytes, stream);
+}
+
+extern "C" int tree_kv_commit_e4m3(void* k_pages, void* v_pages, float* k_scales, float* v_scales,
+                                   const int32_t* page_table, const int32_t* prefix_lens,
+                                   const int32_t* accept_path, const int32_t* accept_len, int32_t* new_prefix_lens,
+                                   const treespec_attn_shape* shape, void* workspace, size_t workspace_bytes,
+                                   treespec_stream_t stream) {
+    if (!k_scales || !v_scales) return TREESPEC_ERR_NULL_POINTER;
+    if (!aligned16(k_scales) || !aligned16(v_scales)) return TREESPEC_ERR_ALIGNMENT;
+    return commit(k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, accept_path, accept_len,
+                  new_prefix_lens, shape, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------------ chunks, 8-bit cache
+
+namespace {
+
+int check_chunk_shape(const treespec_chunk_shape* s, bool attn) {
+    if (!s) return TREESPEC_ERR_NULL_POINTER;
+    if (s->dtype != TREESPEC_DTYPE_F32 && s->dtype != TREESPEC_DTYPE_BF16) return TREESPEC_ERR_DTYPE;
+    if (s->kv_dtype != s->dtype && s->kv_dtype != TREESPEC_DTYPE_E4M3) return TREESPEC_ERR_DTYPE;
+    if (s->batch < 1 || s->batch > 65535 || s->num_tokens < 1) return TREESPEC_ERR_SHAPE;
+    if (s->num_kv_heads < 1 || s->num_q_heads < 1 || s->num_q_heads % s->num_kv_heads) return TREESPEC_ERR_SHAPE;
+    if (s->num_q_heads > 65535 || s->num_q_heads / s->num_kv_heads > 128) return TREESPEC_ERR_SHAPE;
+    if ((long long)s->num_tokens * s->num_q_heads >= (1ll << 31)) return TREESPEC_ERR_SHAPE;
+    if (s->head_dim != 64 && s->head_dim != 128) return TREESPEC_ERR_SHAPE;
+    if (s->page_size != kPage) return TREESPEC_ERR_SHAPE;
+    if (s->max_pages_per_seq < 1 || s->num_pool_pages < 1) return TREESPEC_ERR_SHAPE;
+    if ((long long)s->max_pages_per_seq * s->page_size > (1ll << 30)) return TREESPEC_ERR_SHAPE;
+    if (s->kernel != TREESPEC_KERNEL_AUTO && !(attn && s->kernel == TREESPEC_KERNEL_SIMT)) return TREESPEC_ERR_SHAPE;
+    return TREESPEC_OK;
+}
+
+struct ChunkPlan {
+    int kernel, num_splits, split_tokens, rows_block, ctas;
+};
+
+// rows: query rows per kv head of the whole batch.  The lengths are on the device, so the
+// plan goes by the page table's width and the mean rows of a sequence.
+ChunkPlan chunk_plan(long long batch, long long rows, int Hkv, int max_pages, int sms) {
+    ChunkPlan c{};
+    c.kernel = TREESPEC_KERNEL_SIMT;
+    const long long mean = (rows + batch - 1) / batch;
+    c.rows_block = mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+    const long long units = ((rows + c.rows_block - 1) / c.rows_block) * Hkv;
+    const long long tokens = (long long)max_pages * kPage;
+    // two CTAs per SM where the row blocks alone do not give them, no split below 256 tokens
+    long long splits = units >= 2ll * sms ? 1 : 2ll * sms / units;
+    splits = std::max(1ll, std::min(splits, tokens / 256));
+    splits = std::min(splits, 256ll);
+    long long chunk = (tokens + splits - 1) / splits;
+    chunk = (chunk + 127) / 128 * 128;
+    c.split_tokens = int(chunk);
+    c.num_splits = int((tokens + chunk - 1) / chunk);
+    return c;
+}
+
+ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long long tree_rows, long long batch) {
+    ChunkLayout L{};
+    size_t off = 0;
+    L.status = off;
+    off += kWsAlign;
+    L.anc = off;
+    off = align_up(off + size_t(tree_rows) * kAncWords * 8, kWsAlign);
+    L.lens = off;
+    off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
+    L.nn = off;
+    off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
+    const size_t parts = c.num_splits > 1 ? size_t(c.num_splits) * T * Hq : 0;
+    L.ml = off;
+    off = align_up(off + parts * 2 * 4, kWsAlign);
+    L.acc = off;
+    off = align_up(off + parts * D * 4, kWsAlign);
+    L.total = off;
+    return L;
+}
+
+ChunkPlan plan_of(const treespec_chunk_shape& s) {
+    return chunk_plan(s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads,
+                      s.max_pages_per_seq, sm_count_or_default());
+}
+ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c) {
+    return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch);
+}
+
+int check_e4m3_verify_shape(const treespec_attn_shape* s) {
+    if (!s) return TREESPEC_ERR_NULL_POINTER;
+    treespec_attn_shape t = *s;
+    if (t.kernel != TREESPEC_KERNEL_AUTO && t.kernel != TREESPEC_KERNEL_SIMT) return TREESPEC_ERR_SHAPE;
+    t.kernel = TREESPEC_KERNEL_SIMT;                     // the limits of the tensor-core kernels are checked by the plan
+    const int rc = check_attn_shape(&t);
+    if (rc != TREESPEC_OK) return rc;
+    if (t.num_q_heads / t.num_kv_heads > 128) return TREESPEC_ERR_SHAPE;
+    if ((long long)t.batch * t.num_nodes * t.num_q_heads >= (1ll << 31)) return TREESPEC_ERR_SHAPE;
+    return TREESPEC_OK;
+}
+ChunkPlan plan_of(const treespec_attn_shape& s) {
+    return chunk_plan(s.batch, (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads,
+                      s.max_pages_per_seq, sm_count_or_default());
+}
+ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c) {
+    const long long rows = (long long)s.batch * s.num_nodes;
+    return chunk_layout(c, rows, s.num_q_heads, s.head_dim, rows, s.batch);
+}
+
+// What the two attention calls share once their arguments are checked.
+int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsigned char* ws, int dtype, int kv_dtype,
+              cudaStream_t st) {
+    p.status = reinterpret_cast<uint32_t*>(ws + lay.status);
+    p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
+    p.part_acc = reinterpret_cast<float*>(ws + lay.acc);
+    p.G = p.Hq / p.Hkv;
+    p.num_splits = c.num_splits;
+    p.split_tokens = c.split_tokens;
+    p.rows_block = c.rows_block;
+    p.ctas = c.ctas;
+    p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.D)));
+    p.wait_ns = g_wait_ns.load();
+    cudaError_t e = launch_chunk_simt(p, dtype, kv_dtype, st);
+    if (e != cudaSuccess) return launch_failed(e);
+    g_launches++;
+    if (c.num_splits > 1) {
+        e = launch_chunk_merge(p, dtype, st);
+        if (e != cudaSuccess) return launch_failed(e);
+        g_launches++;
+    }
+    return TREESPEC_OK;
+}
+
+}  // namespace
+
+extern "C" size_t treespec_append_workspace_bytes(void) { return kWsAlign; }
+
+extern "C" int tree_chunk_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, void* q_out, void* k_pages, void* v_pages, float* k_scales,
+                                 float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                 const int32_t* chunk_offsets, const treespec_chunk_shape* shape,
+                                 const treespec_append_options* options, void* workspace, size_t workspace_bytes,
+                                 treespec_stream_t stream) {
+    int rc = check_chunk_shape(shape, false);
+    if (rc != TREESPEC_OK) return rc;
+    if (!options || !q || !k || !v || !q_out || !k_pages || !v_pages || !page_table || !prefix_lens || !chunk_offsets)
+        return TREESPEC_ERR_NULL_POINTER;
+    const treespec_chunk_shape& s = *shape;
+    const treespec_append_options& o = *options;
+    const bool q8 = s.kv_dtype == TREESPEC_DTYPE_E4M3;
+    if (q8 && (!k_scales || !v_scales)) return TREESPEC_ERR_NULL_POINTER;
+    if (o.rot_dim < 0 || o.rot_dim > s.head_dim || o.rot_dim % 16) return TREESPEC_ERR_SHAPE;
+    if (o.layout != TREESPEC_ROPE_HALF && o.layout != TREESPEC_ROPE_INTERLEAVED) return TREESPEC_ERR_SHAPE;
+    if (o.rot_dim > 0 && !o.inv_freq) return TREESPEC_ERR_NULL_POINTER;
+    if ((o.q_norm || o.k_norm) && !(o.norm_eps >= 0.f)) return TREESPEC_ERR_SHAPE;
+    if (!std::isfinite(o.rope_scale)) return TREESPEC_ERR_SHAPE;
+    const long long e = s.dtype == TREESPEC_DTYPE_BF16 ? 2 : 4;
+    const long long D = s.head_dim;
+    if (q_stride < s.num_q_heads * D || k_stride < s.num_kv_heads * D || v_stride < s.num_kv_heads * D)
+        return TREESPEC_ERR_SHAPE;
+    if (q == q_out && q_stride != s.num_q_heads * D) return TREESPEC_ERR_SHAPE;
+    if (q_stride * e % 16 || k_stride * e % 16 || v_stride * e % 16) return TREESPEC_ERR_ALIGNMENT;
+    const void* all[] = {q, k, v, q_out, k_pages, v_pages, o.q_norm, o.k_norm};
+    for (const void* x : all)
+        if (!aligned16(x)) return TREESPEC_ERR_ALIGNMENT;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign) ||
+        workspace_bytes < treespec_append_workspace_bytes())
+        return TREESPEC_ERR_WORKSPACE;
+    rc = check_device();
+    if (rc != TREESPEC_OK) return rc;
+    AppendParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out = q_out;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.page_table = page_table;
+    p.prefix_lens = prefix_lens;
+    p.offsets = chunk_offsets;
+    p.positions = o.positions;
+    p.q_norm = o.q_norm;
+    p.k_norm = o.k_norm;
+    p.inv_freq = o.inv_freq;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.B = s.batch;
+    p.T = s.num_tokens;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.D = s.head_dim;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    p.rot = o.rot_dim;
+    p.layout = o.layout;
+    p.eps = o.norm_eps;
+    p.rope_scale = o.rope_scale;
+    p.sms = sm_count_or_default();
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    const cudaError_t err = launch_chunk_append(p, s.dtype, s.kv_dtype, st);
+    if (err != cudaSuccess) return launch_failed(err);
+    g_launches++;
+    return TREESPEC_OK;
+}
+
+extern "C" size_t treespec_chunk_attn_workspace_bytes(const treespec_chunk_shape* shape) {
+    if (check_chunk_shape(shape, true) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape)).total;
+}
+
+extern "C" int tree_chunk_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                               const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                               const int32_t* chunk_offsets, void* out, const treespec_chunk_shape* shape,
+                               void* workspace, size_t workspace_bytes, treespec_stream_t stream) {
+    int rc = check_chunk_shape(shape, true);
+    if (rc != TREESPEC_OK) return rc;
+    if (!q || !k_pages || !v_pages || !page_table || !prefix_lens || !chunk_offsets || !out)
+        return TREESPEC_ERR_NULL_POINTER;
+    const treespec_chunk_shape& s = *shape;
+    const bool q8 = s.kv_dtype == TREESPEC_DTYPE_E4M3;
+    if (q8 && (!k_scales || !v_scales)) return TREESPEC_ERR_NULL_POINTER;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        (q8 && (!aligned16(k_scales) || !aligned16(v_scales))))
+        return TREESPEC_ERR_ALIGNMENT;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
+    rc = check_device();
+    if (rc != TREESPEC_OK) return rc;
+    const ChunkPlan plan = plan_of(s);
+    const ChunkLayout lay = layout_of(s, plan);
+    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
+    ChunkParams p{};
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.k_scales = q8 ? k_scales : nullptr;
+    p.v_scales = q8 ? v_scales : nullptr;
+    p.page_table = page_table;
+    p.prefix_lens = prefix_lens;
+    p.offsets = chunk_offsets;
+    p.out = out;
+    p.B = s.batch;
+    p.T = s.num_tokens;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.D = s.head_dim;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(ws + lay.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    return run_chunk(p, plan, lay, ws, s.dtype, s.kv_dtype, st);
+}
+
+extern "C" size_t treespec_attn_e4m3_workspace_bytes(const treespec_attn_shape* shape) {
+    if (check_e4m3_verify_shape(shape) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape)).total;
+}
+
+extern "C" int tree_attn_verify_e4m3(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                     const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                     const int32_t* tree_parents, void* out, const treespec_attn_shape* shape,
+                                     void* workspace, size_t workspace_bytes, treespec_stream_t stream) {
+    int rc = check_e4m3_verify_shape(shape);
+    if (rc != TREESPEC_OK) return rc;
+    if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !prefix_lens || !tree_parents || !out)
+        return TREESPEC_ERR_NULL_POINTER;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(k_scales) ||
+        !aligned16(v_scales))
+        return TREESPEC_ERR_ALIGNMENT;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
+    rc = check_device();
+    if (rc != TREESPEC_OK) return rc;
+    const treespec_attn_shape& s = *shape;
+    const ChunkPlan plan = plan_of(s);
+    const ChunkLayout lay = layout_of(s, plan);
+    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    ChunkParams p{};
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.page_table = page_table;
+    p.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
+    p.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
+    p.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
+    p.out = out;
+    p.B = s.batch;
+    p.T = s.batch * s.num_nodes;
+    p.N = s.num_nodes;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.D = s.head_dim;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    AttnParams a{};                                      // what the tree prologue reads and writes
+    a.parents = tree_parents;
+    a.prefix_lens = prefix_lens;
+    a.status = reinterpret_cast<uint32_t*>(ws + lay.status);
+    a.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
+    a.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
+    a.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
+    a.B = s.batch;
+    a.N = s.num_nodes;
+    a.max_pages = s.max_pages_per_seq;
+    a.ps = kPage;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    const cudaError_t e = launch_tree_prologue(a, st);
+    if (e != cudaSuccess) return launch_failed(e);
+    g_launches++;
+    return run_chunk(p, plan, lay, ws, s.dtype, TREESPEC_DTYPE_E4M3, st);
 }
 
 extern "C" size_t treespec_draft_workspace_bytes(int32_t batch, int32_t frontier, int32_t topk) {

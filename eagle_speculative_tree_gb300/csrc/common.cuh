@@ -161,9 +161,112 @@ struct CommitParams {
     const int32_t* len;
     int32_t* new_lens;
     uint32_t* status;
+    float* k_scales;   // [P][Hkv][16] of 8-bit pools, else NULL
+    float* v_scales;
     int B, N, Hkv, D, ps, max_pages, num_pool_pages, elem;   // elem: bytes per element
 };
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
+
+// Appending new tokens (tree_chunk_append)
+struct AppendParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    long long q_stride, k_stride, v_stride;   // elements from one token to the next
+    void* q_out;
+    void* k_pages;
+    void* v_pages;
+    float* k_scales;
+    float* v_scales;
+    const int32_t* page_table;
+    const int32_t* prefix_lens;
+    const int32_t* offsets;
+    const int32_t* positions;                 // or NULL: logical positions
+    const float* q_norm;
+    const float* k_norm;
+    const float* inv_freq;
+    uint32_t* status;
+    int B, T, Hq, Hkv, D, max_pages, num_pool_pages, rot, layout;
+    float eps, rope_scale;
+    int sms;
+};
+cudaError_t launch_chunk_append(const AppendParams& p, int dtype, int kv_dtype, cudaStream_t s);
+
+// Attention of packed chunks, or of a batch of trees over 8-bit pools
+constexpr int kPage = 16;                     // tokens per page
+constexpr int kChunkMaxBatch = 1024;          // persistent tensor-core form: sequences per call
+constexpr int kChunkMaxCtas = 1024;           // persistent tensor-core form: CTAs
+struct ChunkLayout {
+    size_t status, anc, lens, nn, ml, acc, total;
+};
+struct ChunkParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* k_scales;
+    const float* v_scales;
+    const int32_t* page_table;
+    const int32_t* prefix_lens;
+    const int32_t* offsets;                   // [B + 1]; NULL: a batch of trees
+    const uint64_t* anc;                      // trees: ancestor sets, checked lengths and node counts
+    const int32_t* lens;                      //        of the prologue
+    const int32_t* nn;
+    void* out;
+    uint32_t* status;
+    float* part_ml;                           // SIMT: [splits][T][Hq][2], acc [splits][T][Hq][D]
+    float* part_acc;                          // persistent: [2 CTAs][256][2] and [2 CTAs][256][D]
+    int32_t* counters;                        // persistent: [CTAs] arrivals at a cut unit, behind the status word
+    int B, T, N, Hq, Hkv, G, D, max_pages, num_pool_pages;
+    int num_splits, split_tokens, rows_block; // SIMT
+    int ctas;                                 // persistent
+    float scale_log2;
+    uint64_t wait_ns;
+};
+cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int dtype, cudaStream_t s);
+
+// Rows of a sequence's new tokens: the first row, the rows, those of them that hold a
+// token (a padded tree's other rows are zeros), and the prefix length (-1: the sequence is
+// invalid and its rows are zeros).  Offsets that decrease or leave [0, T] give no rows.
+struct SeqRows {
+    int row0, n, live, S;
+};
+__device__ __forceinline__ SeqRows seq_rows(const ChunkParams& p, int b) {
+    SeqRows r;
+    if (!p.offsets) {
+        r.row0 = b * p.N;
+        r.n = p.N;
+        r.S = p.lens[b];
+        r.live = p.nn[b];
+        return r;
+    }
+    const int o0 = p.offsets[b], o1 = p.offsets[b + 1];
+    const bool ok = o0 >= 0 && o1 >= o0 && o1 <= p.T;
+    r.row0 = ok ? o0 : 0;
+    r.n = r.live = ok ? o1 - o0 : 0;
+    const int S = p.prefix_lens[b];
+    r.S = S >= 0 && (long long)S + r.n <= (long long)p.max_pages * kPage ? S : -1;
+    return r;
+}
+// Whether sequence b's lengths are what the call allows (trees: the prologue checks them).
+__device__ __forceinline__ bool seq_ok(const ChunkParams& p, int b) {
+    if (!p.offsets) return true;
+    const int o0 = p.offsets[b], o1 = p.offsets[b + 1], S = p.prefix_lens[b];
+    return o0 >= 0 && o1 >= o0 && o1 <= p.T && S >= 0 && (long long)S + (o1 - o0) <= (long long)p.max_pages * kPage;
+}
+
+// two e4m3 codes -> two floats (exact; NaN codes give NaN)
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    return h;
+}
+// two floats -> two e4m3 codes, to nearest even; `lo` in the low byte
+__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(hi), "f"(lo));
+    return c;
+}
 
 // Draft-tree construction (tree_draft_step, tree_rerank)
 constexpr int kMaxTopk = 16;          // branching per step

@@ -5,7 +5,8 @@
 // checks the page ids of the rows it moves.  The CTA then reads all
 // source rows of K into shared memory, waits, writes them to their destinations, and
 // does the same for V -- so a destination that is also a later source is never
-// overwritten before it is read.  Rows move as 16-byte words.
+// overwritten before it is read.  Rows move as 16-byte words.  Over 8-bit pools
+// (tree_kv_commit_e4m3) a row is D bytes and its two scales move the same way.
 #include "common.cuh"
 
 namespace treespec {
@@ -19,6 +20,7 @@ constexpr int kMaxStageBytes = (kMaxNodes - 1) * kMaxRowWords * 16;
 
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitParams p) {
     extern __shared__ uint4 buf[];                        // [N - 1][words]: the accepted rows of one kv head
+    __shared__ float sbuf[2][kMaxNodes];                  // 8-bit pools: their K and V scales
     __shared__ int s_ok, s_len, s_S, s_badpage;
     const int b = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
     const int* path = p.path + size_t(b) * p.N;
@@ -83,6 +85,14 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitP
             *row_word(base, S + 1 + k, w) = buf[k * words + w];
         }
         __syncthreads();
+    }
+    if (p.k_scales) {                                     // [P][Hkv][16]
+        auto scale = [&](int t, int pos) -> float* {
+            return (t ? p.v_scales : p.k_scales) + (size_t(ptab[pos / p.ps]) * p.Hkv + h) * p.ps + pos % p.ps;
+        };
+        for (int e = tid; e < 2 * n; e += kCommitThreads) sbuf[e / n][e % n] = *scale(e / n, S + path[e % n]);
+        __syncthreads();
+        for (int e = tid; e < 2 * n; e += kCommitThreads) *scale(e / n, S + 1 + e % n) = sbuf[e / n][e % n];
     }
     if (tid == 0 && h == 0) p.new_lens[b] = S + 1 + n;
 }

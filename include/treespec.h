@@ -53,6 +53,8 @@ typedef struct CUstream_st *treespec_stream_t;   /* a cudaStream_t */
 enum treespec_dtype {
     TREESPEC_DTYPE_F32 = 0,    /* IEEE float32 storage and arithmetic */
     TREESPEC_DTYPE_BF16 = 1,   /* bfloat16 storage, float32 accumulation */
+    TREESPEC_DTYPE_E4M3 = 2,   /* page pools of the *_e4m3 and tree_chunk_* calls only: 8-bit floats (4 exponent,
+                                  3 mantissa bits) with a float32 scale per token and kv head */
 };
 
 /* Parent entry of a padding slot after a tree smaller than the batch's N. */
@@ -94,7 +96,8 @@ enum treespec_error {
 enum treespec_status_bits {
     TREESPEC_STATUS_BAD_PARENT = 1u << 0,  /* parents[0] != -1, parents[i] not in [0, i), or a node after padding */
     TREESPEC_STATUS_BAD_PAGE = 1u << 1,    /* a page id outside [0, num_pool_pages) */
-    TREESPEC_STATUS_BAD_LENGTH = 1u << 2,  /* prefix_len < 0 or prefix_len + N > pages * page_size */
+    TREESPEC_STATUS_BAD_LENGTH = 1u << 2,  /* prefix_len < 0 or prefix_len + N > pages * page_size; tree_chunk_*: chunk
+                                              offsets that decrease or leave [0, num_tokens] */
     TREESPEC_STATUS_BAD_TOKEN = 1u << 3,   /* a draft token outside [0, vocab) */
     TREESPEC_STATUS_TIMEOUT = 1u << 4,     /* a bounded wait inside a kernel ran out */
     TREESPEC_STATUS_INTERNAL = 1u << 5,    /* a launch-configuration invariant failed (work skipped) */
@@ -366,6 +369,138 @@ int tree_rerank_pool(const int32_t *node_parent, const int32_t *node_token, cons
                      int32_t batch, int32_t max_nodes, int32_t num_nodes,
                      int32_t *tree_parents, int32_t *draft_tokens,
                      void *workspace, size_t workspace_bytes, treespec_stream_t stream);
+
+/* ------------------------------------------------- chunks of new tokens, 8-bit cache */
+
+/*
+ * The calls below take the new tokens of a batch packed: row t of q / k / v is a token,
+ * and sequence b owns rows chunk_offsets[b] .. chunk_offsets[b+1]-1 (n_b of them, which
+ * may be none), the i-th of them at logical position prefix_lens[b] + i of the sequence.
+ * chunk_offsets has batch + 1 entries that do not decrease and lie in [0, num_tokens];
+ * rows before the first and behind the last sequence belong to none and are left alone.
+ * Offsets out of order or range set BAD_LENGTH: a sequence with such offsets has no rows,
+ * and those of others may be left out too; nothing outside the call's buffers is touched.
+ *
+ * 8-bit pools (TREESPEC_DTYPE_E4M3): k_pages / v_pages [P][16][Hkv][D] hold e4m3 codes
+ * (1 byte each), k_scales / v_scales [P][Hkv][16] a float32 for each token and kv head;
+ * an element stands for code * scale.  A page's 16 scales of one kv head are 64
+ * contiguous bytes, so that a reader of one head touches no other head's.
+ */
+typedef struct {
+    int32_t batch;              /* B, 1..65535 (TREESPEC_KERNEL_TC_STREAM: at most 1024) */
+    int32_t num_tokens;         /* T >= 1, rows of q, k, v, out */
+    int32_t num_q_heads;        /* Hq */
+    int32_t num_kv_heads;       /* Hkv, Hq % Hkv == 0, Hq / Hkv <= 128 */
+    int32_t head_dim;           /* D: 64 or 128 */
+    int32_t page_size;          /* 16 */
+    int32_t max_pages_per_seq;  /* row length of page_table */
+    int32_t num_pool_pages;     /* P */
+    int32_t dtype;              /* F32 or BF16: q, k, v, q_out, out */
+    int32_t kv_dtype;           /* the pools: the same as dtype, or TREESPEC_DTYPE_E4M3 */
+    int32_t kernel;             /* tree_chunk_attn: AUTO, SIMT or TC_STREAM (bf16 q); tree_chunk_append: 0 */
+} treespec_chunk_shape;
+
+enum treespec_rope_layout {
+    TREESPEC_ROPE_HALF = 0,         /* element j turns with element j + rot_dim / 2 */
+    TREESPEC_ROPE_INTERLEAVED = 1,  /* element 2j turns with element 2j + 1 */
+};
+
+typedef struct {
+    const float *q_norm;        /* [D] device, weight of the queries' norm; NULL: no norm */
+    const float *k_norm;        /* [D] device, weight of the keys' norm; NULL: no norm */
+    const float *inv_freq;      /* [rot_dim / 2] device, radians per position; NULL only if rot_dim == 0 */
+    const int32_t *positions;   /* [T] device, rotary position of each row, negative for a padding row; NULL:
+                                   the logical positions */
+    float norm_eps;             /* >= 0 */
+    float rope_scale;           /* factor on cosines and sines (1 for plain rotary positions) */
+    int32_t rot_dim;            /* leading elements of a head that turn: a multiple of 16, 0..D */
+    int32_t layout;             /* enum treespec_rope_layout */
+} treespec_append_options;
+
+/* Workspace bytes tree_chunk_append needs (its status word). */
+size_t treespec_append_workspace_bytes(void);
+
+/*
+ * tree_chunk_append -- what stands between the projections of the new tokens and the
+ * attention over the cache: the norm of every query and key head, the rotary positions,
+ * and the write of K and V into the page pools (quantised where the pools are 8-bit).
+ * It places what tree_attn_verify and tree_chunk_attn read: for a draft tree, give each
+ * sequence N rows (chunk_offsets[b] = b * N), positions[b*N + i] = S + depth of node i,
+ * and a negative position for the padding slots.
+ *
+ * Per head x of q and k (in float32, rounded once when it is stored):
+ *     y   = x * (mean(x^2) + norm_eps)^(-1/2) * weight            (with a norm weight)
+ *     z   = y with each pair (a, b), frequency j, turned by the angle w = position *
+ *           inv_freq[j]:  (a cos w - b sin w, b cos w + a sin w) * rope_scale
+ * q goes to q_out [T][Hq][D]; k and v (v as it is) go to logical position S + i of their
+ * sequence.  Frequencies scaled for long contexts are given by inv_freq and rope_scale.
+ * The angle is reduced in 64-bit fixed point, so it keeps its accuracy at any position
+ * (below 2^31) for inv_freq below 2^24.
+ * 8-bit pools: scale = max(max |x| / 448, 2^-100) over the head, code = x / scale rounded
+ * to nearest even; a head with a NaN or an infinity reads back as NaN.
+ *
+ *   q [T][Hq][D], k, v [T][Hkv][D] in shape->dtype: heads contiguous, tokens q_stride /
+ *      k_stride / v_stride elements apart (views of one projection's output work); rows
+ *      16-byte aligned.  q_out is contiguous and may be q itself (q_stride == Hq * D);
+ *      no other overlap is allowed.
+ *   k_pages, v_pages in shape->kv_dtype, written in place; k_scales, v_scales NULL unless
+ *      8-bit.
+ * A row with a negative position is padding: nothing of it is read or written.  A row
+ * whose slot lies outside its page table (BAD_LENGTH) or whose page lies outside the pool
+ * (BAD_PAGE) is left out in the same way.  Two sequences whose new tokens share a slot
+ * are the caller's mistake; one of them is kept.
+ */
+int tree_chunk_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                      int64_t v_stride, void *q_out, void *k_pages, void *v_pages, float *k_scales, float *v_scales,
+                      const int32_t *page_table, const int32_t *prefix_lens, const int32_t *chunk_offsets,
+                      const treespec_chunk_shape *shape, const treespec_append_options *options,
+                      void *workspace, size_t workspace_bytes, treespec_stream_t stream);
+
+/* Workspace bytes tree_chunk_attn needs for `shape` (0 if the shape is invalid). */
+size_t treespec_chunk_attn_workspace_bytes(const treespec_chunk_shape *shape);
+
+/*
+ * tree_chunk_attn -- causal attention of each sequence's new tokens over its paged cache:
+ * a whole prompt (prefix length 0), a chunk of a longer one, or single decoded tokens, in
+ * one batch of any mixture.  The new tokens' own K/V are in the pages already
+ * (tree_chunk_append).  For row t, the i-th of sequence b, and query head hq:
+ *     out[t][hq] = softmax_u( q[t][hq] . K[u][hq / G] / sqrt(D) ) applied to V[u][hq / G],
+ *                  over the logical tokens u = 0 .. prefix_lens[b] + i.
+ *   q, out [T][Hq][D] contiguous, in shape->dtype; pools and scales as above.
+ * Tokens that a row may not see, and slots behind a sequence's last token, do not reach
+ * the row's result, whatever they hold (NaN and infinities included).
+ * The rows of a sequence with prefix_len < 0 or prefix_len + n_b > max_pages * 16 are
+ * zeros (BAD_LENGTH).  A page id outside the pool sets BAD_PAGE; its tokens count as zeros.
+ * All tensors 16-byte aligned.  Results do not depend on timing: the same call gives the
+ * same bits.
+ */
+int tree_chunk_attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                    const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                    const int32_t *chunk_offsets, void *out, const treespec_chunk_shape *shape,
+                    void *workspace, size_t workspace_bytes, treespec_stream_t stream);
+
+/* Workspace bytes tree_attn_verify_e4m3 needs for `shape` (0 if the shape is invalid). */
+size_t treespec_attn_e4m3_workspace_bytes(const treespec_attn_shape *shape);
+
+/*
+ * tree_attn_verify_e4m3 -- tree_attn_verify over 8-bit pools.  shape->dtype is that of q
+ * and out; shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q, batch <= 1024), num_splits
+ * is not used.  Everything else is as for tree_attn_verify.
+ */
+int tree_attn_verify_e4m3(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                          const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                          const int32_t *tree_parents, void *out, const treespec_attn_shape *shape,
+                          void *workspace, size_t workspace_bytes, treespec_stream_t stream);
+
+/*
+ * tree_kv_commit_e4m3 -- tree_kv_commit over 8-bit pools: codes and scales of the accepted
+ * nodes move.  shape->dtype is F32 or BF16 (that of the queries) and is not used.
+ * Workspace: treespec_commit_workspace_bytes().
+ */
+int tree_kv_commit_e4m3(void *k_pages, void *v_pages, float *k_scales, float *v_scales,
+                        const int32_t *page_table, const int32_t *prefix_lens, const int32_t *accept_path,
+                        const int32_t *accept_len, int32_t *new_prefix_lens, const treespec_attn_shape *shape,
+                        void *workspace, size_t workspace_bytes, treespec_stream_t stream);
 
 /* ------------------------------------------------------------------------- helpers */
 

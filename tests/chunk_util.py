@@ -1,0 +1,110 @@
+"""Problems and error bounds of the chunk and 8-bit cache tests."""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import numpy as np
+import torch
+
+from oracle import chunk as och
+
+U_BF16 = 2.0 ** -8            # a rounding to bf16 is off by at most this share of the value
+U_F32 = 2.0 ** -24
+U_F16 = 2.0 ** -11
+U_E4M3 = 2.0 ** -4
+
+
+@dataclass
+class Problem:
+    """Inputs of one batch on the device, and their float64 values."""
+    prefix: list
+    new: list
+    q: torch.Tensor              # [T][Hq][D]
+    k_pages: torch.Tensor
+    v_pages: torch.Tensor
+    k_scales: torch.Tensor | None
+    v_scales: torch.Tensor | None
+    page_table: torch.Tensor
+    prefix_lens: torch.Tensor
+    chunk_offsets: torch.Tensor
+
+    def pools64(self):
+        if self.k_scales is None:
+            return self.k_pages.double().cpu().numpy(), self.v_pages.double().cpu().numpy()
+        return tuple(och.dequantise(p.view(torch.uint8).cpu().numpy(), s.cpu().numpy())
+                     for p, s in ((self.k_pages, self.k_scales), (self.v_pages, self.v_scales)))
+
+    def scales(self):
+        return {} if self.k_scales is None else {"k_scales": self.k_scales, "v_scales": self.v_scales}
+
+
+def make(device, prefix, new, hq, hkv, dim, dtype, e4m3=False, seed=0, spare=3, lead=0, tail=0, rows=None,
+         extra_pages=0):
+    """Random pools and queries.  Slots past a sequence's last token and the spare pages hold
+    NaN.  `lead` / `tail`: rows of q before the first and behind the last sequence."""
+    rng = np.random.default_rng([seed, 77])
+    B = len(prefix)
+    rows = rows or new
+    need = [(p + n + 15) // 16 for p, n in zip(prefix, rows)]
+    pool = sum(need) + spare
+    order = rng.permutation(pool).astype(np.int32)
+    table = np.full((B, max(max(need), 1) + extra_pages), pool + 5, dtype=np.int32)   # unused entries: no page
+    used = np.zeros((pool, 16), dtype=bool)
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = order[at:at + need[b]]
+        at += need[b]
+        t = np.arange(prefix[b] + new[b])
+        used[table[b][t // 16], t % 16] = True
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    T = lead + sum(rows) + tail
+    q = torch.from_numpy(rng.standard_normal((T, hq, dim)).astype(np.float32)).to(device).to(dt)
+    pools, scales = [], []
+    for _ in range(2):
+        x = rng.standard_normal((pool, 16, hkv, dim)) * np.exp(rng.normal(size=(pool, 16, hkv, 1)) * 0.5 * e4m3)
+        if e4m3:
+            codes, sc = och.quantise(x)
+            codes[~used] = 0x7f
+            sc = sc.transpose(0, 2, 1).astype(np.float32)
+            sc[~used[:, None, :].repeat(hkv, 1)] = np.nan
+            pools.append(torch.from_numpy(codes).to(device).view(torch.float8_e4m3fn))
+            scales.append(torch.from_numpy(np.ascontiguousarray(sc)).to(device))
+        else:
+            x[~used] = np.nan
+            pools.append(torch.from_numpy(x.astype(np.float32)).to(device).to(dt))
+            scales.append(None)
+    ints = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).to(device)  # noqa: E731
+    offsets = lead + np.concatenate(([0], np.cumsum(rows)))
+    return Problem(list(prefix), list(new), q, pools[0], pools[1], scales[0], scales[1], ints(table), ints(prefix),
+                   ints(offsets))
+
+
+def attention_bound(ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores):
+    """How far a kernel's rows may be from the float64 ones: [.., H, D].
+
+    A score is a sum of `dim` products in 32 bits (tensor cores may truncate: 2^-23 a step)
+    and two scalings: it is off by ds <= (dim + 8) 2^-23 reach; over 8-bit K the tensor cores
+    take the query in fp16, after scaling its row below 2: 2^-11 reach more would be a normal
+    rounding of each element (bf16 values are exact above 2^-14 of the row's largest, below
+    it the error is 2^-25 of that: counted as 2^-11 reach for float32 queries only).  Every
+    weight is then off by exp(2 ds) - 1, by 2^-21 of exp2 and the running rescales, and by
+    half a step of the type that P is rounded to before it meets V (bf16, or fp16 over 8-bit
+    V); a sum of `tokens` terms in 32 bits adds tokens 2^-23.  The result is rounded once."""
+    ds = (dim + 8) * 2.0 ** -23 * reach[..., None]
+    if tensor_cores and e4m3:
+        ds = ds + 2.0 ** -20 * reach[..., None]
+    w = np.expm1(2 * ds) + 2.0 ** -21 + tokens * 2.0 ** -23
+    if tensor_cores:
+        w = w + (U_F16 if e4m3 else U_BF16)
+    out = U_BF16 if dtype == "bf16" else U_F32
+    return w * spread * 1.0001 + out * (np.abs(ref) + w * spread) + 1e-30
+
+
+def check_attention(got, ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores):
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(ref)), "NaN in other places than the definition's"
+    live = ~np.isnan(ref)
+    bound = attention_bound(ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores)
+    err = np.abs(g - ref)
+    bad = live & ~(err <= bound)
+    assert not bad.any(), f"{bad.sum()} of {live.sum()} elements out of bounds, worst {np.nanmax(err / bound):.3g} times"
