@@ -480,7 +480,13 @@ int check_chunk_shape(const treespec_chunk_shape* s, bool attn) {
     if (s->page_size != kPage) return TREESPEC_ERR_SHAPE;
     if (s->max_pages_per_seq < 1 || s->num_pool_pages < 1) return TREESPEC_ERR_SHAPE;
     if ((long long)s->max_pages_per_seq * s->page_size > (1ll << 30)) return TREESPEC_ERR_SHAPE;
-    if (s->kernel != TREESPEC_KERNEL_AUTO && !(attn && s->kernel == TREESPEC_KERNEL_SIMT)) return TREESPEC_ERR_SHAPE;
+    if (s->kernel != TREESPEC_KERNEL_AUTO &&
+        !(attn && (s->kernel == TREESPEC_KERNEL_SIMT || s->kernel == TREESPEC_KERNEL_TC_STREAM)))
+        return TREESPEC_ERR_SHAPE;
+    if (s->kernel == TREESPEC_KERNEL_TC_STREAM) {
+        if (s->dtype != TREESPEC_DTYPE_BF16) return TREESPEC_ERR_DTYPE;
+        if (!chunk_tc_supported(s->dtype, s->batch, (long long)s->num_pool_pages * kPage)) return TREESPEC_ERR_SHAPE;
+    }
     return TREESPEC_OK;
 }
 
@@ -490,8 +496,15 @@ struct ChunkPlan {
 
 // rows: query rows per kv head of the whole batch.  The lengths are on the device, so the
 // plan goes by the page table's width and the mean rows of a sequence.
-ChunkPlan chunk_plan(long long batch, long long rows, int Hkv, int max_pages, int sms) {
+ChunkPlan chunk_plan(int kernel, int dtype, long long batch, long long rows, int Hkv, int max_pages, int pool_pages,
+                     int sms) {
     ChunkPlan c{};
+    if (kernel != TREESPEC_KERNEL_SIMT && chunk_tc_supported(dtype, int(batch), (long long)pool_pages * kPage)) {
+        c.kernel = TREESPEC_KERNEL_TC_STREAM;
+        c.num_splits = 1;
+        c.ctas = std::min(sms, kChunkMaxCtas);
+        return c;
+    }
     c.kernel = TREESPEC_KERNEL_SIMT;
     const long long mean = (rows + batch - 1) / batch;
     c.rows_block = mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
@@ -511,15 +524,18 @@ ChunkPlan chunk_plan(long long batch, long long rows, int Hkv, int max_pages, in
 ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long long tree_rows, long long batch) {
     ChunkLayout L{};
     size_t off = 0;
-    L.status = off;
+    L.status = off;                                      // and the persistent kernel's counters behind it
     off += kWsAlign;
+    off = align_up(off + size_t(c.ctas) * 8 * 4, kWsAlign);
+    L.cleared = off;
     L.anc = off;
     off = align_up(off + size_t(tree_rows) * kAncWords * 8, kWsAlign);
     L.lens = off;
     off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
     L.nn = off;
     off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
-    const size_t parts = c.num_splits > 1 ? size_t(c.num_splits) * T * Hq : 0;
+    // SIMT: a row of each split; persistent: two slots of two tiles per CTA
+    const size_t parts = c.ctas ? size_t(2) * c.ctas * 256 : c.num_splits > 1 ? size_t(c.num_splits) * T * Hq : 0;
     L.ml = off;
     off = align_up(off + parts * 2 * 4, kWsAlign);
     L.acc = off;
@@ -529,8 +545,8 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
 }
 
 ChunkPlan plan_of(const treespec_chunk_shape& s) {
-    return chunk_plan(s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads,
-                      s.max_pages_per_seq, sm_count_or_default());
+    return chunk_plan(s.kernel, s.dtype, s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads),
+                      s.num_kv_heads, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
 }
 ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c) {
     return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch);
@@ -539,7 +555,12 @@ ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c) {
 int check_e4m3_verify_shape(const treespec_attn_shape* s) {
     if (!s) return TREESPEC_ERR_NULL_POINTER;
     treespec_attn_shape t = *s;
-    if (t.kernel != TREESPEC_KERNEL_AUTO && t.kernel != TREESPEC_KERNEL_SIMT) return TREESPEC_ERR_SHAPE;
+    if (t.kernel != TREESPEC_KERNEL_AUTO && t.kernel != TREESPEC_KERNEL_SIMT && t.kernel != TREESPEC_KERNEL_TC_STREAM)
+        return TREESPEC_ERR_SHAPE;
+    if (t.kernel == TREESPEC_KERNEL_TC_STREAM) {
+        if (t.dtype != TREESPEC_DTYPE_BF16) return TREESPEC_ERR_DTYPE;
+        if (!chunk_tc_supported(t.dtype, t.batch, (long long)t.num_pool_pages * kPage)) return TREESPEC_ERR_SHAPE;
+    }
     t.kernel = TREESPEC_KERNEL_SIMT;                     // the limits of the tensor-core kernels are checked by the plan
     const int rc = check_attn_shape(&t);
     if (rc != TREESPEC_OK) return rc;
@@ -548,8 +569,8 @@ int check_e4m3_verify_shape(const treespec_attn_shape* s) {
     return TREESPEC_OK;
 }
 ChunkPlan plan_of(const treespec_attn_shape& s) {
-    return chunk_plan(s.batch, (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads,
-                      s.max_pages_per_seq, sm_count_or_default());
+    return chunk_plan(s.kernel, s.dtype, s.batch, (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads),
+                      s.num_kv_heads, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
 }
 ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c) {
     const long long rows = (long long)s.batch * s.num_nodes;
@@ -560,8 +581,10 @@ ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c) {
 int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsigned char* ws, int dtype, int kv_dtype,
               cudaStream_t st) {
     p.status = reinterpret_cast<uint32_t*>(ws + lay.status);
+    p.counters = reinterpret_cast<int32_t*>(ws + lay.status + kWsAlign);
     p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
     p.part_acc = reinterpret_cast<float*>(ws + lay.acc);
+    p.ps = kPage;
     p.G = p.Hq / p.Hkv;
     p.num_splits = c.num_splits;
     p.split_tokens = c.split_tokens;
@@ -569,7 +592,8 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsign
     p.ctas = c.ctas;
     p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.D)));
     p.wait_ns = g_wait_ns.load();
-    cudaError_t e = launch_chunk_simt(p, dtype, kv_dtype, st);
+    cudaError_t e = c.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_chunk_tc(p, kv_dtype, st)
+                                                          : launch_chunk_simt(p, dtype, kv_dtype, st);
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;
     if (c.num_splits > 1) {
@@ -701,7 +725,7 @@ extern "C" int tree_chunk_attn(const void* q, const void* k_pages, const void* v
     p.num_pool_pages = s.num_pool_pages;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws + lay.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
     return run_chunk(p, plan, lay, ws, s.dtype, s.kv_dtype, st);
 }
 
@@ -760,7 +784,7 @@ extern "C" int tree_attn_verify_e4m3(const void* q, const void* k_pages, const v
     a.max_pages = s.max_pages_per_seq;
     a.ps = kPage;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
     const cudaError_t e = launch_tree_prologue(a, st);
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;

@@ -456,11 +456,11 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // 3-D view of a page pool [P][16][Hkv][128] bf16 as (head dim, kv head, pool token),
 // copied in boxes of 64 head-dim columns x 1 head x 16 tokens (one page) with
 // 128-byte swizzle.
-bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens) {
+bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens, int D) {
     auto fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(Hkv), cuuint64_t(pool_tokens)};
-    cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(Hkv) * kD * 2};
+    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hkv), cuuint64_t(pool_tokens)};
+    cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(Hkv) * D * 2};
     cuuint32_t box[3] = {64, 1, 16};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,

@@ -1,4 +1,5 @@
-// Pieces shared by the tensor-core attention kernels (attn_tc.cu, attn_tc_pair.cu): the
+// Pieces shared by the tensor-core attention kernels (attn_tc.cu, attn_tc_pair.cu, and in
+// part chunk_tc.cu, which also has heads of 64 elements): the
 // TMA page producer, the tree mask of a 128-token tile, one tile of the online softmax,
 // the rescale of O in tensor memory and the epilogue that writes a row block's result.
 //
@@ -41,8 +42,8 @@ struct ProducerArgs {
     int pg0, npg, dp0, ndp;
 };
 
-template <int TILE>
-__device__ __forceinline__ bool produce_pages(const AttnParams& p, const ProducerArgs& a, int b, int h, int t0,
+template <int TILE, int DIM = kD, class Params>
+__device__ __forceinline__ bool produce_pages(const Params& p, const ProducerArgs& a, int b, int h, int t0,
                                               int t1, int L, int ntiles, int& g, volatile uint32_t* abort_flag) {
     constexpr int kPPT = TILE / 16;                    // pages per tile
     constexpr int kTPB = 32 / kPPT;                    // tiles per warp-wide page-id load
@@ -98,7 +99,7 @@ __device__ __forceinline__ bool produce_pages(const AttnParams& p, const Produce
                     const int pos = q0 + rr;
                     uint4 val = make_uint4(0, 0, 0, 0);
                     if (pgid >= 0 && pos < t1) {
-                        const size_t off = ((size_t(pgid) * p.ps + (pos & 15)) * p.Hkv + h) * kD + (a.dp0 * 8 + cc) * 8;
+                        const size_t off = ((size_t(pgid) * p.ps + (pos & 15)) * p.Hkv + h) * DIM + (a.dp0 * 8 + cc) * 8;
                         val = __ldg(reinterpret_cast<const uint4*>(a.src + off));
                     }
                     *reinterpret_cast<uint4*>(dst + (cc >> 3) * a.panel_bytes + sw128_offset(pg * 16 + rr, cc & 7)) = val;

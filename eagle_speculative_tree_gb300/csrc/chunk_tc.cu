@@ -1,0 +1,1135 @@
+// Attention of packed chunks (tree_chunk_attn), and of trees over 8-bit pools, on the
+// 5th-generation tensor cores: bf16 queries, head dim 64 or 128, K/V bf16 or e4m3.
+//
+// A unit is 2 floor(128 / G) consecutive new tokens of one sequence and one kv head: their
+// rows (token x query head of the group) fill two 128-row query tiles, the second of which
+// is idle where the unit's tokens fit the first.  A unit runs over the sequence's logical
+// tokens, from 0 to the last that one of its rows may see, in KV tiles of 64.
+//
+// One CTA per SM.  The units, ordered (sequence, kv head, rows), and within them their KV
+// tiles are cut into equal contiguous ranges, one per CTA, so single decoded tokens over a
+// long cache, prompts and any mixture load every SM alike, whatever the lengths; they are
+// on the device and the host does not know them.  A unit costs kKappa tiles beyond its own
+// (its epilogue and the restart of the pipeline).  A unit cut between CTAs leaves a partial
+// (m, l, O) of each piece in the CTAs' slots; of the warps that hold the same 32 rows the
+// one that finishes last joins them, in the order of the pieces, so the result does not
+// depend on which one that is and nobody waits for another CTA.
+//
+// Within a CTA, as in the two-tile tree kernel: S_t(j) = Q_t K(j)^T in 64 tensor-memory
+// columns, double-buffered, P_t(j) written over it as bf16, O_t += P_t(j) V(j); one warp
+// issues the MMAs of each query tile, one warpgroup runs each tile's softmax with a row per
+// thread, and O is rescaled only when a row's running maximum grows by more than 2^8.
+//   bf16 K/V: warps 8 and 9 fill the K and V rings by TMA, a page of 16 tokens at a time.
+//   e4m3 K/V: four more warps copy codes into shared memory with cp.async (each thread the
+//   64 bytes it will convert, several tiles ahead), widen them exactly to bf16 operands, and
+//   leave the tile's scales beside them: K's multiplies a column of S inside the exponent's
+//   fused multiply-add, V's multiplies P before it is rounded.
+//
+// Rows are spread over the four warps of a tile (row r in lane r / 4 of warp r % 4), so that
+// the few rows of a decoded token share the epilogue's work.
+//
+// A value that a row may not see must not reach it.  S is masked by selection, but P V
+// multiplies a masked token's V by zero, and 0 x NaN is NaN.  A row whose O comes out
+// non-finite is therefore recomputed from the visible tokens alone, on CUDA cores: rare and
+// slow, and no cost to the others but a test in the epilogue.
+//
+// Every mbarrier wait is bounded; on expiry the CTA records TREESPEC_STATUS_TIMEOUT, drains
+// its own copies and MMAs, frees its tensor memory and exits.
+#include <type_traits>
+
+#include "attn_tc_parts.cuh"
+
+namespace treespec {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kM = 128;              // rows of a query tile = TMEM lanes
+constexpr int kNQ = 2;               // query tiles
+constexpr int kBN = 64;              // tokens per KV tile
+constexpr int kKappa = 7;            // a unit's fixed cost, in tiles
+constexpr int kRaw = 5;              // e4m3: tiles of codes in flight
+constexpr int kScaleRing = 4;        // e4m3: tiles of scales (a slot is rewritten three tiles later at the earliest)
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;        // S buffer b of tile t: [128 t + 64 b, 128 t + 64 b + 64)
+constexpr uint32_t kColO = 256;      // O_t: [256 + 128 t, 256 + 128 t + D)
+constexpr int kWarpK = 8, kWarpV = 9, kWarpMma = 10, kWarpConv = 12;
+
+template <int D, bool E4M3>
+struct Cfg {
+    static constexpr int kNP = D / 64;                    // 64-element panels of a row
+    static constexpr int kNS = E4M3 ? 2 : D == 128 ? 4 : 6;   // stages of the K ring, and of the V ring
+    static constexpr int kThreads = E4M3 ? 512 : 384;
+    static constexpr int kQPanel = kM * 128;
+    static constexpr int kQTile = kNP * kQPanel;
+    static constexpr int kPanel = kBN * 128;
+    static constexpr int kTile = kNP * kPanel;
+    static constexpr int kRawTile = E4M3 ? 2 * kBN * D : 0;   // K and V codes of a tile
+    // registers: two softmax warpgroups, the producer / issuer one, the converting one; the
+    // sum is what the launch allocates (384 x 168 or 512 x 128)
+    static constexpr uint32_t kRegsSoftmax = 200;
+    static constexpr uint32_t kRegsOther = E4M3 ? 40 : 56;
+    static constexpr uint32_t kRegsConv = 72;
+    static_assert(E4M3 ? 128 * (2 * kRegsSoftmax + kRegsOther + kRegsConv) <= 512 * 128
+                       : 128 * (2 * kRegsSoftmax + kRegsOther) <= 384 * 168,
+                  "register split exceeds the launch allocation");
+    struct Bars {
+        uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS];
+        uint64_t q_full[kNQ], s_full[kNQ][2], p_full[kNQ][2], pv_done[kNQ][2], o_full[kNQ], o_free[kNQ], drain[kNQ];
+        uint64_t sc_full[kScaleRing];                     // e4m3: a tile's scales are in shared memory
+    };
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kNQ * kQTile;
+    static constexpr int kOffV = kOffK + kNS * kTile;
+    static constexpr int kOffRaw = kOffV + kNS * kTile;
+    static constexpr int kOffScale = kOffRaw + kRaw * kRawTile;
+    static constexpr int kOffBar = kOffScale + (E4M3 ? kScaleRing * 2 * kBN * 4 : 0);
+    static constexpr int kOffMisc = kOffBar + int(sizeof(Bars));
+    static constexpr int kOffEnds = kOffMisc + 16;        // the two ends of the CTA's range
+    static constexpr int kOffWarp = kOffEnds + 2 * 16;    // scratch of the scan
+    static constexpr int kOffTiles = kOffWarp + 16 * 16;  // [kChunkMaxBatch + 1] tiles before a sequence, one kv head
+    static constexpr int kOffUnits = kOffTiles + (kChunkMaxBatch + 1) * 8;   // and units
+    static constexpr int kSmemBytes = kOffUnits + (kChunkMaxBatch + 1) * 4;
+    static_assert(kSmemBytes <= 232448, "shared memory budget");
+    static_assert(kOffBar % 8 == 0 && kOffTiles % 8 == 0, "alignment");
+};
+
+// ------------------------------------------------------------------ units and the cut
+
+// sum over i = 0 .. n - 1 of floor((a i + b) / m); all terms and the sum within 32 bits / 64 bits
+__device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
+    long long ans = 0;
+    while (n) {
+        if (a >= m) {
+            ans += (long long)(n) * (n - 1) / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += (long long)n * (b / m);
+            b %= m;
+        }
+        const uint32_t y = a * n + b;                      // < 64 (n + 1): n is below 2^24
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const uint32_t t = m;
+        m = a;
+        a = t;
+    }
+    return ans;
+}
+
+// The units of one sequence and one kv head.
+struct SeqUnits {
+    int S, live, np;                  // prefix, rows' tokens, units
+    int tpu;                          // tokens per unit
+    bool tree;
+    // KV tiles of unit pr
+    __device__ __forceinline__ int tiles(int pr) const {
+        return (S + (tree ? live : min(live, (pr + 1) * tpu)) + kBN - 1) / kBN;
+    }
+    // KV tiles of units 0 .. pr - 1
+    __device__ __forceinline__ long long tiles_before(int pr) const {
+        if (pr <= 0) return 0;
+        if (tree) return (long long)pr * tiles(0);
+        const int full = min(pr, live / tpu);              // units whose tokens are all there
+        const int A = S + kBN - 1 + tpu;                   // sum of floor((A + k tpu) / 64), k = 0 .. full - 1
+        const int a1 = tpu / kBN, r = tpu % kBN;
+        long long s = (long long)full * (A / kBN) + (long long)full * (full - 1) / 2 * a1;
+        if (r) s += floor_sum(uint32_t(full), kBN, uint32_t(r), uint32_t(A % kBN));
+        return pr > full ? s + tiles(pr - 1) : s;
+    }
+};
+__device__ __forceinline__ SeqUnits seq_units(const ChunkParams& p, const SeqRows& r) {
+    SeqUnits u;
+    u.tree = !p.offsets;
+    u.tpu = 2 * (kM / p.G);
+    u.S = r.S;
+    u.live = r.S < 0 ? 0 : r.live;
+    u.np = (u.live + u.tpu - 1) / u.tpu;
+    return u;
+}
+
+// Positions of the cut: unit (b, h, pr) begins at Hkv (tiles[b] + k units[b]) + h (tiles and
+// k units of the sequence) + (tiles and k units before pr), and its tile j lies k + j after
+// that.
+struct Cut {
+    const long long* tiles;           // [B + 1], shared memory
+    const int* units;
+    long long total;
+    int B, Hkv, k, parts;
+    __device__ __forceinline__ long long before(int b) const { return Hkv * (tiles[b] + (long long)k * units[b]); }
+    __device__ __forceinline__ long long bound(int c) const { return total * c / parts; }    // total x CTAs < 2^63
+    // the part that holds position x: the last c with bound(c) <= x
+    __device__ __forceinline__ int owner(long long x) const { return int(((x + 1) * parts - 1) / total); }
+};
+struct End {                          // tile j of unit (b, h, pr)
+    int b, h, pr, j;
+};
+
+// The tile at or after position x of the cut, by one warp.  x < total.
+__device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long long x) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = q.B;                                  // the last b with before(b) <= x
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q.before(mid) <= x) lo = mid;
+        else hi = mid;
+    }
+    End e;
+    e.b = lo;
+    const SeqUnits u = seq_units(p, seq_rows(p, lo));
+    const long long head = (q.before(lo + 1) - q.before(lo)) / q.Hkv;
+    long long y = x - q.before(lo);
+    e.h = int(y / head);
+    y -= e.h * head;
+    int at = 0, n = u.np;                                  // the last unit that begins at or before y, 32 ways
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int i = lane * step;
+        const bool le = i < n && u.tiles_before(at + i) + (long long)q.k * (at + i) <= y;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int last = 31 - __clz(m);                    // lane 0 always holds
+        at += last * step;
+        n = min(step, n - last * step);
+    }
+    e.pr = at;
+    y -= u.tiles_before(at) + (long long)q.k * at;
+    e.j = int(max(0ll, y - q.k));
+    return e;
+}
+
+// One contiguous range of KV tiles of one unit.
+struct Seg {
+    int b, h, pr;
+    int S, live, L;        // prefix, rows' tokens and logical tokens of the sequence
+    int row0;              // q row of the unit's first token
+    int i0, tokens;        // the unit's tokens: i0 .. i0 + tokens - 1 of the sequence's new ones
+    int j0, ntiles, n;     // tiles j0 .. j0 + ntiles - 1 of n
+    int t0, t1;            // their logical tokens
+    int nq;                // query tiles in use
+    __device__ __forceinline__ bool whole() const { return ntiles == n; }
+};
+
+// The segments of a CTA's range, in order.  Every role walks them by itself.
+struct Walk {
+    const ChunkParams* p;
+    End e, end;            // next segment's first tile; the first tile behind the range
+    SeqUnits u;
+    SeqRows rows;
+    __device__ __forceinline__ void load() {
+        rows = seq_rows(*p, e.b);
+        u = seq_units(*p, rows);
+    }
+    __device__ __forceinline__ void start(const ChunkParams& pp, const End& a, const End& z) {
+        p = &pp;
+        e = a;
+        end = z;
+        load();
+    }
+    __device__ __forceinline__ bool next(Seg& s) {
+        if (e.b > end.b) return false;
+        const bool last = e.b == end.b && e.h == end.h && e.pr == end.pr;
+        if (last && e.j >= end.j) return false;
+        s.b = e.b;
+        s.h = e.h;
+        s.pr = e.pr;
+        s.S = u.S;
+        s.live = u.live;
+        s.L = u.S + u.live;
+        s.i0 = e.pr * u.tpu;
+        s.tokens = min(u.tpu, u.live - s.i0);
+        s.row0 = rows.row0 + s.i0;
+        s.nq = s.tokens > u.tpu / 2 ? 2 : 1;
+        s.n = u.tiles(e.pr);
+        s.j0 = e.j;
+        s.ntiles = (last ? min(end.j, s.n) : s.n) - e.j;
+        const int vis = u.S + (u.tree ? u.live : s.i0 + s.tokens);
+        s.t0 = s.j0 * kBN;
+        s.t1 = min(vis, (s.j0 + s.ntiles) * kBN);
+        e.j = 0;
+        if (last) {
+            e.b = end.b + 1;                               // done
+        } else if (++e.pr >= u.np) {
+            e.pr = 0;
+            if (++e.h >= p->Hkv) {
+                e.h = 0;
+                do {
+                    ++e.b;
+                    if (e.b >= p->B || e.b > end.b) { e.b = end.b + 1; break; }
+                    load();
+                } while (u.np == 0);
+            }
+        }
+        return true;
+    }
+};
+
+// ------------------------------------------------------------------ rows
+
+// A thread's query row of a segment.
+struct Row {
+    int i, hq;             // token of the sequence's new ones, query head
+    size_t at;             // element offset of the row in q and out
+    bool ok;
+};
+__device__ __forceinline__ Row row_of(const ChunkParams& p, const Seg& s, int t, int r, int D) {
+    const int tpq = kM / p.G;
+    Row o;
+    const int it = r / p.G, g = r - it * p.G;
+    o.ok = it < tpq && t * tpq + it < s.tokens;
+    const int i = o.ok ? t * tpq + it : 0;
+    o.i = s.i0 + i;
+    o.hq = s.h * p.G + (o.ok ? g : 0);
+    o.at = (size_t(s.row0 + i) * p.Hq + o.hq) * D;
+    return o;
+}
+// What a row may see: the prefix and, of the new tokens, 0 .. i (a chunk) or its ancestors.
+struct Sight {
+    int end;               // chunks: first logical token it may not see
+    uint64_t a0, a1;       // trees
+};
+__device__ __forceinline__ Sight sight_of(const ChunkParams& p, const Seg& s, const Row& r) {
+    Sight v{0, 0, 0};
+    if (!r.ok) return v;
+    if (p.offsets) {
+        v.end = s.S + r.i + 1;
+    } else {
+        const uint64_t* a = p.anc + (size_t(s.b) * p.N + r.i) * kAncWords;
+        v.a0 = a[0];
+        v.a1 = a[1];
+    }
+    return v;
+}
+
+// A row's exact attention over the segment's visible tokens, by one warp on CUDA cores:
+// (m, l) and O in lane-wise slices of D / 32 elements.  Nothing of a token that the row does
+// not see is read.
+template <int D, bool E4M3>
+__device__ __noinline__ void slow_row(const ChunkParams& p, const Seg& s, const Row& r, const Sight& v, float (&o)[4],
+                                      float& m_out, float& l_out) {
+    constexpr int DS = D / 32;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < DS; ++e) o[e] = 0.f;
+    const int* ptab = p.page_table + size_t(s.b) * p.max_pages;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) + r.at;
+    for (int base = s.t0; base < s.t1; base += 32) {
+        const int pos = base + lane;
+        bool ok = pos < s.t1;
+        if (ok && pos >= s.S) {
+            const int j = pos - s.S;
+            ok = p.offsets ? pos < v.end : ((j < 64 ? v.a0 >> j : v.a1 >> (j - 64)) & 1ull) != 0;
+        }
+        long long slot = -1;                               // a page outside the pool holds zeros
+        if (ok) {
+            const int page = ptab[pos >> 4];
+            if (page >= 0 && page < p.num_pool_pages) slot = (long long)page * kPage + (pos & 15);
+        }
+        float x = 0.f, vs = 1.f;
+        if (slot >= 0) {
+            if constexpr (E4M3) {
+                const unsigned char* k = static_cast<const unsigned char*>(p.k) + (slot * p.Hkv + s.h) * D;
+                for (int d = 0; d < D; d += 2) {
+                    const uint32_t h2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(k + d));
+                    const uint32_t q2 = *reinterpret_cast<const uint32_t*>(q + d);
+                    float a, b;
+                    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+                        : "=f"(a), "=f"(b) : "r"(h2));
+                    x = fmaf(bf16_lo(q2), a, x);
+                    x = fmaf(bf16_hi(q2), b, x);
+                }
+                const size_t sc = ((slot >> 4) * p.Hkv + s.h) * kPage + (slot & 15);
+                x *= p.k_scales[sc];
+                vs = p.v_scales[sc];
+            } else {
+                const uint16_t* k = static_cast<const uint16_t*>(p.k) + (slot * p.Hkv + s.h) * D;
+                for (int d = 0; d < D; d += 2) {
+                    const uint32_t k2 = *reinterpret_cast<const uint32_t*>(k + d);
+                    const uint32_t q2 = *reinterpret_cast<const uint32_t*>(q + d);
+                    x = fmaf(bf16_lo(q2), bf16_lo(k2), x);
+                    x = fmaf(bf16_hi(q2), bf16_hi(k2), x);
+                }
+            }
+        }
+        x *= p.scale_log2;
+        const float mt = warp_max(ok ? x : -INFINITY);
+        const float mn = fmaxf(m, mt);
+        const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
+        const float pr = ok ? exp2f(x - mn) : 0.f;
+        l = l * alpha + warp_sum(pr);
+        m = mn;
+#pragma unroll
+        for (int e = 0; e < DS; ++e) o[e] *= alpha;
+        const unsigned who = __ballot_sync(0xffffffffu, slot >= 0);
+        for (unsigned w = who; w; w &= w - 1) {
+            const int t = __ffs(w) - 1;
+            const long long st = __shfl_sync(0xffffffffu, slot, t);
+            const float pt = __shfl_sync(0xffffffffu, pr, t), vt = __shfl_sync(0xffffffffu, vs, t);
+            const size_t at = (st * p.Hkv + s.h) * D + lane * DS;
+#pragma unroll
+            for (int e = 0; e < DS; ++e) {
+                float y;
+                if constexpr (E4M3) {
+                    const uint32_t h2 = e4m3x2_to_f16x2(static_cast<const unsigned char*>(p.v)[at + e]);
+                    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(y) : "r"(h2));
+                    y *= vt;
+                } else {
+                    y = bf16_to_f32(static_cast<const uint16_t*>(p.v)[at + e]);
+                }
+                o[e] = fmaf(pt, y, o[e]);
+            }
+        }
+    }
+    m_out = m;
+    l_out = l;
+}
+
+// One warp's 32 rows of a cut unit: partial k of the unit is in slot `first` (k = 0) or
+// 2 (c0 + k).  M = max m_k, out = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M).  `valid`: the
+// lanes that hold rows.
+template <int D>
+__device__ __forceinline__ void join_pieces(const ChunkParams& p, int c0, int pieces, int t, int quarter, size_t my_at,
+                                            unsigned valid) {
+    constexpr int DS = D / 32;
+    const int lane = threadIdx.x & 31;
+    auto slot = [&](int k) { return size_t(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * kNQ + t; };
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    const int mine = quarter * 32 + lane;
+    float M = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(ml + slot(k) * kM + mine).x);
+    auto weight = [&](float2 x) {                          // a piece without a visible token has l = 0
+        return x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
+    };
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+        const float2 x = __ldcg(ml + slot(k) * kM + mine);
+        l += x.y * weight(x);
+    }
+    const float inv = 1.f / l;
+    // 8 rows at a time, a row's columns across the lanes
+    for (unsigned left = valid; left;) {
+        int row[8];
+        bool on[8];
+        float acc[8][DS];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            on[i] = left != 0;
+            row[i] = on[i] ? __ffs(left) - 1 : 0;
+            left &= left - 1;
+#pragma unroll
+            for (int e = 0; e < DS; ++e) acc[i][e] = 0.f;
+        }
+#pragma unroll 2
+        for (int k = 0; k < pieces; ++k) {
+            const size_t s0 = slot(k) * kM;
+            const float w = weight(__ldcg(ml + s0 + mine));
+            float x[8][DS];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float* src = p.part_acc + (s0 + quarter * 32 + row[i]) * D + lane * DS;
+                if constexpr (DS == 4) {
+                    const float4 y = on[i] ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0, 0, 0, 0);
+                    x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
+                } else {
+                    const float2 y = on[i] ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0, 0);
+                    x[i][0] = y.x; x[i][1] = y.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, row[i]);
+                if (wi != 0.f)                             // an empty piece's O may hold anything
+#pragma unroll
+                    for (int e = 0; e < DS; ++e) acc[i][e] = fmaf(x[i][e], wi, acc[i][e]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = __shfl_sync(0xffffffffu, inv, row[i]);
+            const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)my_at, row[i]);
+            if (!on[i]) continue;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) + lane * (DS / 2);
+            if constexpr (DS == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[i][0] * f, acc[i][1] * f),
+                                                            pack_bf16x2(acc[i][2] * f, acc[i][3] * f));
+            else
+                *dst = pack_bf16x2(acc[i][0] * f, acc[i][1] * f);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ e4m3 -> operands
+
+// Two e4m3 codes -> packed bf16, exact: every e4m3 value, NaN among them, is a bf16 value.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c) {
+    uint32_t h = e4m3x2_to_f16x2(c), r;
+    asm("{\n\t.reg .f16 lo, hi;\n\t.reg .f32 a, b;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 a, lo;\n\tcvt.f32.f16 b, hi;\n\t"
+        "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
+        : "=r"(r) : "r"(h));
+    return r;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
+    chunk_tc_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    using C = Cfg<D, E4M3>;
+    using Bars = typename C::Bars;
+    constexpr int kNS = C::kNS;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Bars* bars = reinterpret_cast<Bars*>(sm + C::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(sm + C::kOffMisc + 4);
+    End* ends = reinterpret_cast<End*>(sm + C::kOffEnds);
+    long long* tiles_s = reinterpret_cast<long long*>(sm + C::kOffTiles);
+    int* units_s = reinterpret_cast<int*>(sm + C::kOffUnits);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    grid_dep_wait();                                       // trees: the prologue's results
+    if (smem_u32(sm) & 1023u) {                            // never expected; refuse rather than misread tiles
+        if (tid == 0) atomicOr(p.status, TREESPEC_STATUS_INTERNAL);
+        return;
+    }
+
+    // ---- the sequences' tiles and units, and this CTA's range
+    {
+        long long* wt = reinterpret_cast<long long*>(sm + C::kOffWarp);   // [16 warps] {tiles, units}
+        const int per = (p.B + C::kThreads - 1) / C::kThreads;
+        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        long long nt = 0;
+        int nu = 0;
+        bool bad = false;
+        for (int b = b0; b < b1; ++b) {
+            const SeqUnits u = seq_units(p, seq_rows(p, b));
+            bad |= !seq_ok(p, b);
+            tiles_s[b] = nt;                               // relative to the thread's first
+            units_s[b] = nu;
+            nt += u.np == 1 ? u.tiles(0) : u.tiles_before(u.np);
+            nu += u.np;
+        }
+        if (bad && blockIdx.x == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
+        long long it = nt;
+        int iu = nu;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, it, o);
+            const int y = __shfl_up_sync(0xffffffffu, iu, o);
+            if (lane >= o) {
+                it += x;
+                iu += y;
+            }
+        }
+        if (lane == 31) {
+            wt[2 * warp] = it;
+            wt[2 * warp + 1] = iu;
+        }
+        __syncthreads();
+        long long bt = it - nt;
+        int bu = iu - nu;
+        for (int w = 0; w < warp; ++w) {
+            bt += wt[2 * w];
+            bu += int(wt[2 * w + 1]);
+        }
+        for (int b = b0; b < b1; ++b) {
+            tiles_s[b] += bt;
+            units_s[b] += bu;
+        }
+        if (tid == C::kThreads - 1) {
+            tiles_s[p.B] = bt + nt;
+            units_s[p.B] = bu + nu;
+        }
+        __syncthreads();
+    }
+    Cut cut;
+    cut.tiles = tiles_s;
+    cut.units = units_s;
+    cut.B = p.B;
+    cut.Hkv = p.Hkv;
+    {
+        // the fixed cost counts where the ranges are long against it
+        const long long w0 = p.Hkv * tiles_s[p.B], w1 = w0 + (long long)kKappa * p.Hkv * units_s[p.B];
+        cut.k = w1 >= (long long)(kKappa + 2) * gridDim.x ? kKappa : 0;
+        cut.total = cut.k ? w1 : w0;
+        cut.parts = int(max(1ll, min((long long)gridDim.x, cut.total)));
+    }
+    // rows without a token (a padded tree's, and those of an invalid sequence) are zeros
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const SeqRows r = seq_rows(p, b);
+        const int from = r.S < 0 ? 0 : r.live;
+        const size_t words = size_t(r.n - from) * p.Hq * (D / 8);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + size_t(r.row0 + from) * p.Hq * D);
+        for (size_t e = tid; e < words; e += C::kThreads) dst[e] = make_uint4(0, 0, 0, 0);
+    }
+    const int me = blockIdx.x;
+    if (cut.total == 0 || me >= cut.parts) return;
+    if (warp < 2) {                                        // warp 0 the begin, warp 1 the end of the range
+        const int c = me + warp;
+        End e;
+        if (c >= cut.parts) e = End{p.B, 0, 0, 0};
+        else e = locate(p, cut, cut.bound(c));
+        if (lane == 0) ends[warp] = e;
+    }
+
+    if (tid == 0) {
+        for (int s = 0; s < kNS; ++s) {
+            mbar_init(&bars->k_full[s], E4M3 ? 128 : 1);
+            mbar_init(&bars->k_empty[s], kNQ);
+            mbar_init(&bars->v_full[s], E4M3 ? 128 : 1);
+            mbar_init(&bars->v_empty[s], kNQ);
+        }
+        for (int t = 0; t < kNQ; ++t) {
+            mbar_init(&bars->q_full[t], kM);
+            for (int bf = 0; bf < 2; ++bf) {
+                mbar_init(&bars->s_full[t][bf], 1);
+                mbar_init(&bars->p_full[t][bf], kM);
+                mbar_init(&bars->pv_done[t][bf], 1);
+            }
+            mbar_init(&bars->o_full[t], 1);
+            mbar_init(&bars->o_free[t], kM);
+            mbar_init(&bars->drain[t], 1);
+        }
+        for (int s = 0; s < kScaleRing; ++s) mbar_init(&bars->sc_full[s], kBN);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_slot;
+    const uint32_t sbase = smem_u32(sm);
+    Walk walk;
+    walk.start(p, ends[0], ends[1]);
+    Seg sg;
+
+    if (E4M3 && warp >= kWarpConv) {
+        // ------------------------------------------------------------ e4m3 -> bf16 operands
+        // Thread i converts half of the 16-byte words of row i / 2: words i % 2 + 2 k.  Its copies
+        // run kRaw tiles ahead in its own words of the raw ring, so only it waits for them.
+        regs_lower<C::kRegsConv>();
+        constexpr int KW = D / 32;                         // 16-byte words per thread and operand
+        const int i = tid - kWarpConv * 32, rowi = i >> 1, half = i & 1;
+        uint4* raw = reinterpret_cast<uint4*>(sm + C::kOffRaw);           // [kRaw][K, V][KW][128]
+        float* scales = reinterpret_cast<float*>(sm + C::kOffScale);      // [kScaleRing][K, V][64]
+        Walk ahead = walk;
+        Seg sa;
+        int ja = 0;
+        bool have = ahead.next(sa);
+        float sc_k[kRaw], sc_v[kRaw];                      // this row's scales, loaded with the copies
+        auto copy = [&](int slot, float& k_scale, float& v_scale) {
+            if (have) {
+                const int pos = sa.t0 + ja * kBN + rowi;
+                long long at = -1;
+                if (pos < sa.t1) {
+                    const int page = __ldg(p.page_table + size_t(sa.b) * p.max_pages + (pos >> 4));
+                    if (page >= 0 && page < p.num_pool_pages) at = (long long)page * kPage + (pos & 15);
+                    else atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
+                }
+                const size_t off = at < 0 ? 0 : size_t(at * p.Hkv + sa.h) * D + half * 16;
+                uint4* dst = raw + size_t(slot) * 2 * KW * 128 + i;
+#pragma unroll
+                for (int k = 0; k < KW; ++k) {
+                    cp_async_16_zfill(dst + k * 128, static_cast<const unsigned char*>(p.k) + off + k * 32, at < 0 ? 0 : 16);
+                    cp_async_16_zfill(dst + (KW + k) * 128, static_cast<const unsigned char*>(p.v) + off + k * 32,
+                                      at < 0 ? 0 : 16);
+                }
+                const size_t sc = at < 0 ? 0 : (size_t(at >> 4) * p.Hkv + sa.h) * kPage + (at & 15);
+                k_scale = at < 0 ? 0.f : __ldg(p.k_scales + sc);
+                v_scale = at < 0 ? 0.f : __ldg(p.v_scales + sc);
+                if (++ja == sa.ntiles) {
+                    ja = 0;
+                    have = ahead.next(sa);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        // one operand's words of a tile into its stage
+        auto widen = [&](const uint4* src, unsigned char* stage) {
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                const uint4 w = src[k * 128];
+                const int word = half + 2 * k;             // 16 elements: panel word / 4, chunks 2 (word % 4) and the next
+                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[2 * e] = e4m3x2_to_bf16x2(uint16_t(in[e]));
+                    o[2 * e + 1] = e4m3x2_to_bf16x2(uint16_t(in[e] >> 16));
+                }
+                unsigned char* dst = stage + (word >> 2) * C::kPanel;
+                const int ch = (word & 3) * 2;
+                *reinterpret_cast<uint4*>(dst + sw128_offset(rowi, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(dst + sw128_offset(rowi, ch + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        };
+#pragma unroll
+        for (int s = 0; s < kRaw; ++s) copy(s, sc_k[s], sc_v[s]);
+        bool ok = true;
+        int g = 0, slot = 0;
+        while (ok && walk.next(sg)) {
+            for (int j = 0; j < sg.ntiles; ++j, ++g) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
+                const int st = g % kNS;
+                const uint4* src = raw + size_t(slot) * 2 * KW * 128 + i;
+                // the scale slot was read three tiles ago at the latest: V's stage of the tile
+                // before last has been freed by MMAs that came after those reads
+                float* sc = scales + (g % kScaleRing) * 2 * kBN;
+                if (half == 0) {
+                    sc[rowi] = sc_k[0] * p.scale_log2;
+                    sc[kBN + rowi] = sc_v[0];
+                    mbar_arrive(&bars->sc_full[g % kScaleRing]);
+                }
+                if (g >= kNS) ok = mbar_wait_bounded(&bars->k_empty[st], ((g / kNS) - 1) & 1, p.wait_ns);
+                if (!ok || *abort_flag) { ok = false; break; }
+                widen(src, sm + C::kOffK + st * C::kTile);
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->k_full[st]);
+                if (g >= kNS) ok = mbar_wait_bounded(&bars->v_empty[st], ((g / kNS) - 1) & 1, p.wait_ns);
+                if (!ok || *abort_flag) { ok = false; break; }
+                widen(src + KW * 128, sm + C::kOffV + st * C::kTile);
+                fence_proxy_async_smem();
+                mbar_arrive(&bars->v_full[st]);
+#pragma unroll
+                for (int s = 0; s + 1 < kRaw; ++s) {
+                    sc_k[s] = sc_k[s + 1];
+                    sc_v[s] = sc_v[s + 1];
+                }
+                copy(slot, sc_k[kRaw - 1], sc_v[kRaw - 1]);
+                slot = slot + 1 == kRaw ? 0 : slot + 1;
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (!ok) {
+            *abort_flag = 1;
+            atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+        }
+    } else if (warp >= kWarpK) {
+        regs_lower<C::kRegsOther>();
+        if (warp == kWarpK || warp == kWarpV) {
+            if constexpr (!E4M3) {
+                // -------------------------------------------------------- TMA producers
+                const bool is_v = warp == kWarpV;
+                tcparts::ProducerArgs a;
+                a.map = is_v ? &tmv : &tmk;
+                a.src = static_cast<const uint16_t*>(is_v ? p.v : p.k);
+                a.ring = sm + (is_v ? C::kOffV : C::kOffK);
+                a.full = is_v ? bars->v_full : bars->k_full;
+                a.empty = is_v ? bars->v_empty : bars->k_empty;
+                a.nst = kNS;
+                a.stage_bytes = C::kTile;
+                a.panel_bytes = C::kPanel;
+                a.pg0 = 0;
+                a.npg = kBN / 16;
+                a.dp0 = 0;
+                a.ndp = C::kNP;
+                int armed = 0;
+                while (walk.next(sg))
+                    if (!tcparts::produce_pages<kBN, D>(p, a, sg.b, sg.h, sg.t0, sg.t1, sg.L, sg.ntiles, armed, abort_flag))
+                        break;
+                tcparts::drain_copies(a, armed);
+            }
+        } else {
+            // ------------------------------------------------------------ MMA issuers
+            // Warp 10 + t issues every MMA of tile t; one elected lane issues each group and its
+            // commits.  g counts the KV tiles over the CTA's life (ring stages), a those that this
+            // query tile takes part in (S buffers), k its segments (Q, O).  A tile that sits a
+            // segment out only hands the stages back.
+            const int t = warp - kWarpMma;
+            auto ready = [&](uint64_t* x, uint32_t px) -> bool {
+                const uint64_t t0 = global_ns();
+                for (;;) {
+                    if (__all_sync(0xffffffffu, mbar_test_wait(x, px))) return true;
+                    if (*abort_flag || global_ns() - t0 > p.wait_ns) return false;
+                }
+            };
+            constexpr uint32_t kIdS = idesc_bf16_f32(128, kBN, false);
+            constexpr uint32_t kIdO = idesc_bf16_f32(128, D, true);
+            const uint32_t dS = tbase + kColS + uint32_t(t) * 128u;
+            const uint32_t dO = tbase + kColO + uint32_t(t) * 128u;
+            const uint64_t dq = smem_desc(sbase + C::kOffQ + t * C::kQTile, 16, 1024);
+            const uint64_t dk = smem_desc(sbase + C::kOffK, 16, 1024);
+            const uint64_t dv = smem_desc(sbase + C::kOffV, C::kPanel, 1024);
+            bool ok = true;
+            int g = 0, a = 0, k = 0;
+            while (ok && walk.next(sg)) {
+                const int ntiles = sg.ntiles;
+                if (t >= sg.nq) {
+                    for (int j = 0; ok && j < ntiles; ++j) {
+                        const int st = (g + j) % kNS;
+                        const uint32_t ph = ((g + j) / kNS) & 1;
+                        ok = ready(&bars->k_full[st], ph);
+                        if (ok && lane == 0) mbar_arrive(&bars->k_empty[st]);
+                        ok = ok && ready(&bars->v_full[st], ph);
+                        if (ok && lane == 0) mbar_arrive(&bars->v_empty[st]);
+                    }
+                    g += ntiles;
+                    continue;
+                }
+                ok = ready(&bars->q_full[t], k & 1);
+                for (int j = 0; ok && j <= ntiles; ++j) {
+                    if (j < ntiles) {
+                        // S_t = Q_t K^T, once K has landed and the P V that read this buffer is done
+                        const int st = (g + j) % kNS, aj = a + j, bf = aj & 1;
+                        ok = ready(&bars->k_full[st], ((g + j) / kNS) & 1) &&
+                             (aj < 2 || ready(&bars->pv_done[t][bf], ((aj >> 1) - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kb = dk + uint64_t((st * C::kTile) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint64_t qoff = uint64_t(((kk >> 2) * C::kQPanel + (kk & 3) * 32) >> 4);
+                                const uint64_t koff = uint64_t(((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4);
+                                mma_bf16_ss(dS + bf * 64u, dq + qoff, kb + koff, kIdS, kk > 0);
+                            }
+                            mma_commit(&bars->k_empty[st]);
+                            mma_commit(&bars->s_full[t][bf]);
+                        }
+                        __syncwarp();
+                    }
+                    if (j > 0) {
+                        // O_t += P_t V; a segment's first one overwrites O, once the last segment's O is read
+                        const int jp = j - 1, ap = a + jp, st = (g + jp) % kNS, bf = ap & 1;
+                        ok = ready(&bars->p_full[t][bf], (ap >> 1) & 1) && ready(&bars->v_full[st], ((g + jp) / kNS) & 1) &&
+                             (jp > 0 || k == 0 || ready(&bars->o_free[t], (k - 1) & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vb = dv + uint64_t((st * C::kTile) >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < kBN / 16; ++kk)
+                                mma_bf16_ts(dO, dS + bf * 64u + kk * 8, vb + uint64_t((kk * 2048) >> 4), kIdO,
+                                            (jp > 0 || kk > 0));
+                            mma_commit(&bars->v_empty[st]);
+                            mma_commit(&bars->pv_done[t][bf]);
+                            if (jp == ntiles - 1) mma_commit(&bars->o_full[t]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                g += ntiles;
+                a += ntiles;
+                ++k;
+            }
+            if (!ok && lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+            }
+            if (elect_one()) mma_commit(&bars->drain[t]);  // the pipe completes MMAs in issue order
+            __syncwarp();
+            mbar_wait_bounded(&bars->drain[t], 0, kDefaultWaitNs);
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax warps
+        regs_raise<C::kRegsSoftmax>();
+        const int t = warp >> 2, quarter = warp & 3;
+        const int tlane = quarter * 32 + lane;             // TMEM lane, and row of Q's image
+        const int r = lane * 4 + quarter;                  // row of the tile
+        const uint32_t tl = tbase + (uint32_t(quarter * 32) << 16);
+        const uint32_t scol0 = tl + kColS + uint32_t(t) * 128u;
+        const uint32_t ocol = tl + kColO + uint32_t(t) * 128u;
+        const float sc = p.scale_log2;
+        bool alive = true;
+        uint32_t v[kBN];
+        // the next segment this tile takes part in; *skipped counts the KV tiles passed over
+        auto next_seg = [&](Seg& s, int& skipped) -> bool {
+            skipped = 0;
+            while (walk.next(s)) {
+                if (t < s.nq) return true;
+                skipped += s.ntiles;
+            }
+            return false;
+        };
+        auto issue_q = [&](const Seg& s) {
+            const Row ro = row_of(p, s, t, r, D);
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + ro.at);
+            unsigned char* qt = sm + C::kOffQ + t * C::kQTile;
+#pragma unroll
+            for (int ch = 0; ch < D / 8; ++ch)
+                cp_async_16_zfill(qt + (ch >> 3) * C::kQPanel + sw128_offset(tlane, ch & 7), ro.ok ? src + ch : p.q,
+                                  ro.ok ? 16 : 0);
+        };
+        auto finish_q = [&]() {
+            cp_async_wait_all_groups();
+            fence_proxy_async_smem();
+            mbar_arrive(&bars->q_full[t]);
+        };
+        Seg s, nxt;
+        int skip, g = 0, a = 0, k = 0;                     // as the MMA issuer counts them
+        bool have = next_seg(s, skip);
+        g += skip;
+        if (have) {
+            issue_q(s);
+            finish_q();
+        }
+        while (have) {
+            const Row ro = row_of(p, s, t, r, D);
+            const Sight si = sight_of(p, s, ro);
+            const bool warp_rows = __any_sync(0xffffffffu, ro.ok);
+            float m_used = -INFINITY, l = 0.f;
+            bool more = false;
+            int skip2 = 0;
+            for (int j = 0; j < s.ntiles; ++j) {
+                const int aj = a + j, bf = aj & 1;
+                const uint32_t scol = scol0 + bf * 64u;
+                const int base = s.t0 + j * kBN;
+                uint32_t mw[2];
+                if (p.offsets) {
+                    const int nv = min(min(si.end, s.t1) - base, kBN);    // visible columns: the first nv
+                    mw[0] = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                    mw[1] = nv >= 64 ? 0xffffffffu : nv <= 32 ? 0u : (1u << (nv - 32)) - 1u;
+                } else {
+                    tcparts::tile_mask<kBN>(mw, base, s.S, s.t1, si.a0, si.a1, ro.ok);
+                }
+                const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xffffffffu || !ro.ok);
+                if (!mbar_wait_spin(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns)) { alive = false; break; }
+                tc_fence_after();
+                if (j == s.ntiles - 1) {                   // Q is read no more: the next segment's may come
+                    more = next_seg(nxt, skip2);
+                    if (more) issue_q(nxt);
+                }
+                bool resc = false;
+                float alpha = 1.f, ts;
+                if (warp_rows) {
+                    auto load_s = [&]() {
+#pragma unroll
+                        for (int c = 0; c < kBN / 32; ++c) tmem_ld32(scol + c * 32, v + c * 32);
+                        tmem_wait_ld();
+                    };
+                    load_s();
+                    if constexpr (!E4M3) {
+                        if (__all_sync(0xffffffffu, tcparts::softmax_tile_fast<kBN>(v, mw, full, sc, m_used, ts))) {
+                            l += ts;
+                        } else {
+                            load_s();
+                            tcparts::softmax_tile<kBN>(v, mw, full, sc, m_used, l, resc, alpha);
+                        }
+                    } else {
+                        const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) +
+                                           ((g + j) % kScaleRing) * 2 * kBN;
+                        if (!mbar_wait_bounded(&bars->sc_full[(g + j) % kScaleRing], ((g + j) / kScaleRing) & 1, p.wait_ns)) {
+                            alive = false;
+                            break;
+                        }
+                        // P = 2^(s ks - m), P vs leaves as bf16 (its one rounding); the sum is over P.
+                        // Masked columns are replaced after the products: a scale that the row does not
+                        // see may hold anything.
+                        auto columns = [&](auto masked, float m, float& sum) {
+                            float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+                            for (int c = 0; c < kBN / 4; ++c) {
+                                const float4 ks = reinterpret_cast<const float4*>(scl)[c];
+                                const float4 vs = reinterpret_cast<const float4*>(scl + kBN)[c];
+                                const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, vv[4] = {vs.x, vs.y, vs.z, vs.w};
+                                float x[4], y[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    x[e] = fmaf(__uint_as_float(v[4 * c + e]), kk[e], -m);
+                                    y[e] = vv[e];
+                                    if constexpr (decltype(masked)::value) {
+                                        const bool seen = (mw[c >> 3] >> ((4 * c + e) & 31)) & 1u;
+                                        x[e] = seen ? x[e] : -INFINITY;
+                                        y[e] = seen ? y[e] : 0.f;
+                                    }
+                                    x[e] = ex2(x[e]);
+                                }
+                                add_f32x2(a0, a1, x[0], x[1]);
+                                add_f32x2(a2, a3, x[2], x[3]);
+                                v[2 * c] = pack_bf16x2(x[0] * y[0], x[1] * y[1]);
+                                v[2 * c + 1] = pack_bf16x2(x[2] * y[2], x[3] * y[3]);
+                            }
+                            sum = (a0 + a1) + (a2 + a3);
+                        };
+                        auto pass = [&](float m, float& sum) {
+                            if (full) columns(std::false_type{}, m, sum);
+                            else columns(std::true_type{}, m, sum);
+                        };
+                        bool fine;
+                        if (m_used == -INFINITY) {
+                            fine = (mw[0] | mw[1]) == 0u;
+                            ts = 0.f;
+                            if (fine) {
+#pragma unroll
+                                for (int c = 0; c < kBN / 2; ++c) v[c] = 0u;
+                            }
+                        } else {
+                            pass(m_used, ts);
+                            fine = ts <= 256.f;
+                        }
+                        if (__all_sync(0xffffffffu, fine)) {
+                            l += ts;
+                        } else {
+                            load_s();
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int c = 0; c < kBN; ++c)
+                                if ((mw[c >> 5] >> (c & 31)) & 1u) mt = fmaxf(mt, __uint_as_float(v[c]) * scl[c]);
+                            if (mt > m_used + 8.f) {
+                                alpha = ex2(m_used - mt);
+                                resc = m_used != -INFINITY;
+                                l *= alpha;
+                                m_used = mt;
+                            }
+                            pass(m_used == -INFINITY ? 0.f : m_used, ts);
+                            l += ts;
+                        }
+                    }
+                    tmem_st32(scol, v);                    // P over the first 32 columns of the buffer
+                    tmem_wait_st();
+                }
+                if (__any_sync(0xffffffffu, resc)) {
+                    // O may be rescaled once P V of the tile before is in it; never at a segment's first tile
+                    if (!mbar_wait_bounded(&bars->pv_done[t][bf ^ 1], ((aj - 1) >> 1) & 1, p.wait_ns)) { alive = false; break; }
+                    tc_fence_after();
+                    const float f = resc ? alpha : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32(ocol + c * 32, o);
+                        tmem_wait_st();
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->p_full[t][bf]);
+            }
+            if (!alive) break;
+            if (more) finish_q();
+            if (!mbar_wait_bounded(&bars->o_full[t], k & 1, p.wait_ns)) { alive = false; break; }
+            tc_fence_after();
+            // ---- epilogue: the rows, or this piece of them
+            const bool whole = s.whole();
+            const bool head = s.j0 == 0;
+            const size_t slot = size_t(2 * me + (head ? 1 : 0)) * kNQ + t;
+            const size_t prow = slot * kM + tlane;
+            if (warp_rows) {
+                const float inv = 1.f / l;
+                float odd = 0.f;                           // stays 0 unless some element is not finite
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(ocol + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
+                    if (ro.ok && whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ro.at + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w4[4];
+#pragma unroll
+                            for (int k2 = 0; k2 < 4; ++k2)
+                                w4[k2] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k2]) * inv,
+                                                     __uint_as_float(o[8 * e + 2 * k2 + 1]) * inv);
+                            dst[e] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        }
+                    } else if (ro.ok) {
+                        float4* dst = reinterpret_cast<float4*>(p.part_acc + prow * D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                    }
+                }
+                if (!whole && ro.ok) __stcg(reinterpret_cast<float2*>(p.part_ml) + prow, make_float2(m_used, l));
+                for (unsigned w = __ballot_sync(0xffffffffu, ro.ok && !(odd == 0.f)); w; w &= w - 1) {
+                    const int x = __ffs(w) - 1;            // one row at a time, by the whole warp
+                    const Row rx = row_of(p, s, t, x * 4 + quarter, D);
+                    float o4[4], mx, lx;
+                    slow_row<D, E4M3>(p, s, rx, sight_of(p, s, rx), o4, mx, lx);
+                    const size_t px = slot * kM + quarter * 32 + x;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const int d = lane * (D / 32) + e;
+                        if (whole) static_cast<uint16_t*>(p.out)[rx.at + d] = f32_to_bf16_rne(o4[e] / lx);
+                        else __stcg(p.part_acc + px * D + d, o4[e]);
+                    }
+                    if (!whole && lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + px, make_float2(mx, lx));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars->o_free[t]);
+            if (!whole && warp_rows) {
+                // the last of the warps that hold these rows joins the unit's pieces
+                const SeqUnits u = seq_units(p, seq_rows(p, s.b));
+                const long long ub = cut.before(s.b) + s.h * ((cut.before(s.b + 1) - cut.before(s.b)) / cut.Hkv) +
+                                     u.tiles_before(s.pr) + (long long)cut.k * s.pr + cut.k;
+                const int c0 = cut.owner(ub), pieces = cut.owner(ub + s.n - 1) - c0 + 1;
+                __threadfence();
+                __syncwarp();
+                int n = 0;
+                if (lane == 0) n = atomicAdd(p.counters + c0 * 8 + t * 4 + quarter, 1);
+                n = __shfl_sync(0xffffffffu, n, 0);
+                if (n == pieces - 1) {
+                    __threadfence();
+                    join_pieces<D>(p, c0, pieces, t, quarter, ro.at, __ballot_sync(0xffffffffu, ro.ok));
+                }
+            }
+            g += s.ntiles + skip2;
+            a += s.ntiles;
+            ++k;
+            have = more;
+            s = nxt;
+        }
+        if (!alive) {
+            *abort_flag = 1;
+            atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kWarpMma) tmem_dealloc(tbase, kTmemCols);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
+    using C = Cfg<D, E4M3>;
+    if (p.B > kChunkMaxBatch || p.ctas < 1 || p.ctas > kChunkMaxCtas || p.G > kM) return cudaErrorInvalidValue;
+    CUtensorMap mk = {}, mv = {};
+    if (!E4M3) {
+        const long long pool_tokens = (long long)p.num_pool_pages * kPage;
+        if (!make_pool_map(&mk, p.k, p.Hkv, pool_tokens, D) || !make_pool_map(&mv, p.v, p.Hkv, pool_tokens, D))
+            return cudaErrorInvalidValue;
+    }
+    auto kern = chunk_tc_kernel<D, E4M3>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.ctas));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.offsets ? 0 : 1;                      // trees: start while the prologue runs
+    e = cudaLaunchKernelEx(&cfg, kern, p, mk, mv);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool chunk_tc_supported(int dtype, int batch, long long pool_tokens) {
+    return dtype == TREESPEC_DTYPE_BF16 && batch <= kChunkMaxBatch && pool_tokens < (1ll << 31);
+}
+
+cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s) {
+    if (kv_dtype == TREESPEC_DTYPE_E4M3) return p.D == 64 ? launch_typed<64, true>(p, s) : launch_typed<128, true>(p, s);
+    return p.D == 64 ? launch_typed<64, false>(p, s) : launch_typed<128, false>(p, s);
+}
+
+}  // namespace treespec

@@ -146,8 +146,8 @@ cudaError_t launch_attn_tc_2sm(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tc_pair(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_tc_stream(const AttnParams& p, cudaStream_t s);
 bool attn_tc_supported(int dtype, int D);
-// TMA map of a K or V page pool [P][16][Hkv][128] bf16, one page x 64 head dims per box
-bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens);
+// TMA map of a K or V page pool [P][16][Hkv][D] bf16, one page x 64 head dims per box
+bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens, int D = 128);
 cudaError_t launch_attn_merge(const AttnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_accept(const AcceptParams& p, int mode, cudaStream_t s, int* kernels);
 
@@ -197,7 +197,7 @@ constexpr int kPage = 16;                     // tokens per page
 constexpr int kChunkMaxBatch = 1024;          // persistent tensor-core form: sequences per call
 constexpr int kChunkMaxCtas = 1024;           // persistent tensor-core form: CTAs
 struct ChunkLayout {
-    size_t status, anc, lens, nn, ml, acc, total;
+    size_t status, cleared, anc, lens, nn, ml, acc, total;   // [status, cleared): zeroed before every call
 };
 struct ChunkParams {
     const void* q;
@@ -215,14 +215,17 @@ struct ChunkParams {
     uint32_t* status;
     float* part_ml;                           // SIMT: [splits][T][Hq][2], acc [splits][T][Hq][D]
     float* part_acc;                          // persistent: [2 CTAs][256][2] and [2 CTAs][256][D]
-    int32_t* counters;                        // persistent: [CTAs] arrivals at a cut unit, behind the status word
-    int B, T, N, Hq, Hkv, G, D, max_pages, num_pool_pages;
+    int32_t* counters;                        // persistent: [CTAs][8] warps that finished a piece of the unit that
+                                              // the CTA cut, zero at launch
+    int B, T, N, Hq, Hkv, G, D, ps, max_pages, num_pool_pages;
     int num_splits, split_tokens, rows_block; // SIMT
     int ctas;                                 // persistent
     float scale_log2;
     uint64_t wait_ns;
 };
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
+cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s);
+bool chunk_tc_supported(int dtype, int batch, long long pool_tokens);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int dtype, cudaStream_t s);
 
 // Rows of a sequence's new tokens: the first row, the rows, those of them that hold a

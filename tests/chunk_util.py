@@ -10,7 +10,6 @@ from oracle import chunk as och
 
 U_BF16 = 2.0 ** -8            # a rounding to bf16 is off by at most this share of the value
 U_F32 = 2.0 ** -24
-U_F16 = 2.0 ** -11
 U_E4M3 = 2.0 ** -4
 
 
@@ -79,32 +78,29 @@ def make(device, prefix, new, hq, hkv, dim, dtype, e4m3=False, seed=0, spare=3, 
                    ints(offsets))
 
 
-def attention_bound(ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores):
+def attention_bound(ref, spread, reach, tokens, dim, dtype, tensor_cores):
     """How far a kernel's rows may be from the float64 ones: [.., H, D].
 
     A score is a sum of `dim` products in 32 bits (tensor cores may truncate: 2^-23 a step)
-    and two scalings: it is off by ds <= (dim + 8) 2^-23 reach; over 8-bit K the tensor cores
-    take the query in fp16, after scaling its row below 2: 2^-11 reach more would be a normal
-    rounding of each element (bf16 values are exact above 2^-14 of the row's largest, below
-    it the error is 2^-25 of that: counted as 2^-11 reach for float32 queries only).  Every
-    weight is then off by exp(2 ds) - 1, by 2^-21 of exp2 and the running rescales, and by
-    half a step of the type that P is rounded to before it meets V (bf16, or fp16 over 8-bit
-    V); a sum of `tokens` terms in 32 bits adds tokens 2^-23.  The result is rounded once."""
+    and two scalings: it is off by ds <= (dim + 8) 2^-23 reach.  Every weight is then off by
+    exp(2 ds) - 1 and by 2^-21 of exp2 and the running rescales; on tensor cores the weight
+    (times V's scale, over 8-bit V) is rounded once to bf16 before it meets V, half a step of
+    which is 2^-8 of the value, while the sum that divides it is not: w + 2^-8.  Over 8-bit
+    V the codes themselves are exact in bf16.  A sum of `tokens` terms in 32 bits adds
+    tokens 2^-23.  The result is rounded once."""
     ds = (dim + 8) * 2.0 ** -23 * reach[..., None]
-    if tensor_cores and e4m3:
-        ds = ds + 2.0 ** -20 * reach[..., None]
     w = np.expm1(2 * ds) + 2.0 ** -21 + tokens * 2.0 ** -23
     if tensor_cores:
-        w = w + (U_F16 if e4m3 else U_BF16)
+        w = w + U_BF16
     out = U_BF16 if dtype == "bf16" else U_F32
     return w * spread * 1.0001 + out * (np.abs(ref) + w * spread) + 1e-30
 
 
-def check_attention(got, ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores):
+def check_attention(got, ref, spread, reach, tokens, dim, dtype, tensor_cores):
     g = got.double().cpu().numpy()
     assert np.array_equal(np.isnan(g), np.isnan(ref)), "NaN in other places than the definition's"
     live = ~np.isnan(ref)
-    bound = attention_bound(ref, spread, reach, tokens, dim, dtype, e4m3, tensor_cores)
+    bound = attention_bound(ref, spread, reach, tokens, dim, dtype, tensor_cores)
     err = np.abs(g - ref)
     bad = live & ~(err <= bound)
     assert not bad.any(), f"{bad.sum()} of {live.sum()} elements out of bounds, worst {np.nanmax(err / bound):.3g} times"

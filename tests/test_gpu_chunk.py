@@ -220,7 +220,7 @@ def check_chunk(ts, p, kernel, status=0):
                               p.chunk_offsets.cpu().numpy())
     tokens = max(a + b for a, b in zip(p.prefix, p.new))
     dtype = "bf16" if p.q.dtype == torch.bfloat16 else "f32"
-    check_attention(got, *ref, tokens, p.q.shape[2], dtype, p.k_scales is not None, dtype == "bf16")
+    check_attention(got, *ref, tokens, p.q.shape[2], dtype, dtype == "bf16")
     again, _ = attend(ts, p, kernel)
     bits = torch.int16 if dtype == "bf16" else torch.int32
     assert torch.equal(got.view(bits), again.view(bits)), "the same call gave other bits"
@@ -481,7 +481,7 @@ def test_verify_e4m3(ts, cuda_device, case, dtype):
         got = ts.tree_attn_verify_e4m3(q, p.k_pages, p.v_pages, p.k_scales, p.v_scales, p.page_table, p.prefix_lens,
                                        ints(parents, cuda_device), out, kernel=kernel, workspace=ws)
         assert ts.read_status(ws) == 0
-        check_attention(got, *tree_reference(p, q, parents), max(a + b for a, b in zip(prefix, sizes)), dim, dtype, True,
+        check_attention(got, *tree_reference(p, q, parents), max(a + b for a, b in zip(prefix, sizes)), dim, dtype,
                         dtype == "bf16")
 
 
@@ -521,8 +521,8 @@ def test_verify_e4m3_agrees_with_the_verification_of_the_same_values(ts, cuda_de
                                  ints(parents, cuda_device))
     b = ts.tree_attn_verify(q, p.k_pages.to(torch.bfloat16), p.v_pages.to(torch.bfloat16), p.page_table, p.prefix_lens,
                             ints(parents, cuda_device))
-    # both round the weights (2^-8, 2^-11) and the result (2^-8 each) of positive values
-    assert ((a.double() - b.double()).abs() <= 3.2 * U_BF16 * b.double().abs() + 1e-6).all()
+    # both round the weights and the result (2^-8 each) of positive values
+    assert ((a.double() - b.double()).abs() <= 4.1 * U_BF16 * b.double().abs() + 1e-6).all()
 
 
 @pytest.mark.parametrize("dim,hkv", [(128, 8), (64, 1)])
@@ -620,7 +620,7 @@ def test_prompt_tree_accept_commit_and_decode(ts, cuda_device, e4m3):
     from chunk_util import Problem
     p = Problem(lens, [N] * B, None, cache["k_pages"], cache["v_pages"], cache.get("k_scales"), cache.get("v_scales"), table,
                 prefix, offsets)
-    check_attention(out, *tree_reference(p, q, parents), max(lens) + N, D, "bf16", e4m3, True)
+    check_attention(out, *tree_reference(p, q, parents), max(lens) + N, D, "bf16", True)
     logits = torch.randn((B, N, 50), generator=gen, device=cuda_device)
     tokens = logits.argmax(-1)[torch.arange(B)[:, None], torch.from_numpy(np.maximum(parents, 0))].to(torch.int32)
     path, length, _bonus = ts.tree_accept(logits, tokens, None, ints(parents, cuda_device), None, 0.0)
