@@ -590,6 +590,8 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsign
     p.split_tokens = c.split_tokens;
     p.rows_block = c.rows_block;
     p.ctas = c.ctas;
+    p.tpq = 128 / p.G;
+    p.inv_g = (65536 + p.G - 1) / p.G;
     p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.D)));
     p.wait_ns = g_wait_ns.load();
     cudaError_t e = c.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_chunk_tc(p, kv_dtype, st)

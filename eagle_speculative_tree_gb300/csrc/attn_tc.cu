@@ -469,6 +469,19 @@ bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_t
     return r == CUDA_SUCCESS;
 }
 
+bool make_code_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens, int D) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hkv), cuuint64_t(pool_tokens)};
+    cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(Hkv) * D};
+    cuuint32_t box[3] = {cuuint32_t(D), 1, 16};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool attn_tc_supported(int dtype, int D) { return dtype == TREESPEC_DTYPE_BF16 && D == kD; }
 
 template <bool kPair>

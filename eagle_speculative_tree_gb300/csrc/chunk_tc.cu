@@ -20,10 +20,9 @@
 // issues the MMAs of each query tile, one warpgroup runs each tile's softmax with a row per
 // thread, and O is rescaled only when a row's running maximum grows by more than 2^8.
 //   bf16 K/V: warps 8 and 9 fill the K and V rings by TMA, a page of 16 tokens at a time.
-//   e4m3 K/V: four more warps copy codes into shared memory with cp.async (each thread the
-//   64 bytes it will convert, several tiles ahead), widen them exactly to bf16 operands, and
-//   leave the tile's scales beside them: K's multiplies a column of S inside the exponent's
-//   fused multiply-add, V's multiplies P before it is rounded.
+//   e4m3 K/V: warps 8 and 9 fill rings of codes and scales in the same way, and four more
+//   warps widen the codes exactly to bf16 operands.  K's scale multiplies a column of S
+//   inside the exponent's fused multiply-add, V's multiplies P before it is rounded.
 //
 // Rows are spread over the four warps of a tile (row r in lane r / 4 of warp r % 4), so that
 // the few rows of a decoded token share the epilogue's work.
@@ -49,7 +48,8 @@ constexpr int kM = 128;              // rows of a query tile = TMEM lanes
 constexpr int kNQ = 2;               // query tiles
 constexpr int kBN = 64;              // tokens per KV tile
 constexpr int kKappa = 7;            // a unit's fixed cost, in tiles
-constexpr int kRaw = 5;              // e4m3: tiles of codes in flight
+constexpr int kRaw = 5;              // e4m3: stages of the rings of codes
+constexpr int kMinTiles = 4;         // no range shorter than this
 constexpr int kScaleRing = 4;        // e4m3: tiles of scales (a slot is rewritten three tiles later at the earliest)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;        // S buffer b of tile t: [128 t + 64 b, 128 t + 64 b + 64)
@@ -65,7 +65,7 @@ struct Cfg {
     static constexpr int kQTile = kNP * kQPanel;
     static constexpr int kPanel = kBN * 128;
     static constexpr int kTile = kNP * kPanel;
-    static constexpr int kRawTile = E4M3 ? 2 * kBN * D : 0;   // K and V codes of a tile
+    static constexpr int kRawTile = E4M3 ? kBN * D : 0;   // codes of one operand's tile
     // registers: two softmax warpgroups, the producer / issuer one, the converting one; the
     // sum is what the launch allocates (384 x 168 or 512 x 128)
     static constexpr uint32_t kRegsSoftmax = 200;
@@ -77,17 +77,20 @@ struct Cfg {
     struct Bars {
         uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS];
         uint64_t q_full[kNQ], s_full[kNQ][2], p_full[kNQ][2], pv_done[kNQ][2], o_full[kNQ], o_free[kNQ], drain[kNQ];
-        uint64_t sc_full[kScaleRing];                     // e4m3: a tile's scales are in shared memory
+        // e4m3: a tile's codes have landed / been read; its scales stand where the softmax reads them
+        uint64_t rk_full[kRaw], rk_empty[kRaw], rv_full[kRaw], rv_empty[kRaw], sck_full[kScaleRing],
+            scv_full[kScaleRing];
     };
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + kNQ * kQTile;
     static constexpr int kOffV = kOffK + kNS * kTile;
     static constexpr int kOffRaw = kOffV + kNS * kTile;
-    static constexpr int kOffScale = kOffRaw + kRaw * kRawTile;
+    static constexpr int kOffRawScale = kOffRaw + 2 * kRaw * kRawTile;              // [K, V][kRaw][64]
+    static constexpr int kOffScale = kOffRawScale + (E4M3 ? 2 * kRaw * kBN * 4 : 0);   // [kScaleRing][K, V][64]
     static constexpr int kOffBar = kOffScale + (E4M3 ? kScaleRing * 2 * kBN * 4 : 0);
     static constexpr int kOffMisc = kOffBar + int(sizeof(Bars));
     static constexpr int kOffEnds = kOffMisc + 16;        // the two ends of the CTA's range
-    static constexpr int kOffWarp = kOffEnds + 2 * 16;    // scratch of the scan
+    static constexpr int kOffWarp = kOffEnds + 3 * 16;    // scratch of the scan
     static constexpr int kOffTiles = kOffWarp + 16 * 16;  // [kChunkMaxBatch + 1] tiles before a sequence, one kv head
     static constexpr int kOffUnits = kOffTiles + (kChunkMaxBatch + 1) * 8;   // and units
     static constexpr int kSmemBytes = kOffUnits + (kChunkMaxBatch + 1) * 4;
@@ -96,6 +99,13 @@ struct Cfg {
 };
 
 // ------------------------------------------------------------------ units and the cut
+
+// a / b of non-negative numbers; a 64-bit division costs several times a 32-bit one, and
+// nearly every batch's positions fit 32 bits
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return uint32_t(a) / uint32_t(b);
+    return a / b;
+}
 
 // sum over i = 0 .. n - 1 of floor((a i + b) / m); all terms and the sum within 32 bits / 64 bits
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
@@ -144,7 +154,7 @@ struct SeqUnits {
 __device__ __forceinline__ SeqUnits seq_units(const ChunkParams& p, const SeqRows& r) {
     SeqUnits u;
     u.tree = !p.offsets;
-    u.tpu = 2 * (kM / p.G);
+    u.tpu = 2 * p.tpq;
     u.S = r.S;
     u.live = r.S < 0 ? 0 : r.live;
     u.np = (u.live + u.tpu - 1) / u.tpu;
@@ -159,14 +169,29 @@ struct Cut {
     const int* units;
     long long total;
     int B, Hkv, k, parts;
+    int m;                            // 0: even cut; else parts m u .. m u + m - 1 share unit u
     __device__ __forceinline__ long long before(int b) const { return Hkv * (tiles[b] + (long long)k * units[b]); }
-    __device__ __forceinline__ long long bound(int c) const { return total * c / parts; }    // total x CTAs < 2^63
+    __device__ __forceinline__ long long bound(int c) const { return div_pos(total * c, parts); }    // total x CTAs < 2^63
     // the part that holds position x: the last c with bound(c) <= x
-    __device__ __forceinline__ int owner(long long x) const { return int(((x + 1) * parts - 1) / total); }
+    __device__ __forceinline__ int owner(long long x) const { return int(div_pos((x + 1) * parts - 1, total)); }
 };
 struct End {                          // tile j of unit (b, h, pr)
     int b, h, pr, j;
 };
+// Pieces of a unit of n tiles that m CTAs share: none shorter than kMinTiles.
+__device__ __forceinline__ int unit_pieces(int n, int m) { return min(m, max(1, n / kMinTiles)); }
+
+// Unit u of the batch, in the order of the cut.
+__device__ __forceinline__ End unit_at(const ChunkParams& p, const Cut& q, int u) {
+    int lo = 0, hi = q.B;                                  // the last b whose units begin at or before u
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (q.Hkv * q.units[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    const int np = q.units[lo + 1] - q.units[lo], off = u - q.Hkv * q.units[lo];
+    return End{lo, off / np, off % np, 0};
+}
 
 // The tile at or after position x of the cut, by one warp.  x < total.
 __device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long long x) {
@@ -180,9 +205,9 @@ __device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long l
     End e;
     e.b = lo;
     const SeqUnits u = seq_units(p, seq_rows(p, lo));
-    const long long head = (q.before(lo + 1) - q.before(lo)) / q.Hkv;
+    const long long head = div_pos(q.before(lo + 1) - q.before(lo), q.Hkv);
     long long y = x - q.before(lo);
-    e.h = int(y / head);
+    e.h = int(div_pos(y, head));
     y -= e.h * head;
     int at = 0, n = u.np;                                  // the last unit that begins at or before y, 32 ways
     while (n > 1) {
@@ -222,11 +247,12 @@ struct Walk {
         rows = seq_rows(*p, e.b);
         u = seq_units(*p, rows);
     }
-    __device__ __forceinline__ void start(const ChunkParams& pp, const End& a, const End& z) {
+    __device__ __forceinline__ void start(const ChunkParams& pp, const End& a, const End& z, const SeqRows& r) {
         p = &pp;
         e = a;
         end = z;
-        load();
+        rows = r;                                          // of sequence a.b
+        u = seq_units(pp, r);
     }
     __device__ __forceinline__ bool next(Seg& s) {
         if (e.b > end.b) return false;
@@ -275,9 +301,9 @@ struct Row {
     bool ok;
 };
 __device__ __forceinline__ Row row_of(const ChunkParams& p, const Seg& s, int t, int r, int D) {
-    const int tpq = kM / p.G;
+    const int tpq = p.tpq;
     Row o;
-    const int it = r / p.G, g = r - it * p.G;
+    const int it = (r * p.inv_g) >> 16, g = r - it * p.G;   // r / G: exact for r < 128, G <= 128
     o.ok = it < tpq && t * tpq + it < s.tokens;
     const int i = o.ok ? t * tpq + it : 0;
     o.i = s.i0 + i;
@@ -387,71 +413,80 @@ __device__ __noinline__ void slow_row(const ChunkParams& p, const Seg& s, const 
     l_out = l;
 }
 
-// One warp's 32 rows of a cut unit: partial k of the unit is in slot `first` (k = 0) or
-// 2 (c0 + k).  M = max m_k, out = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M).  `valid`: the
-// lanes that hold rows.
+// One warp's 32 rows of a cut unit: partial k of the unit is in slot 2 c0 + 1 (k = 0) or
+// 2 (c0 + k).  M = max m_k, out = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M), the pieces in
+// their order.  `valid`: the lanes that hold rows.  Four rows at a time: their (m, l) with a
+// piece per lane, their O with the columns across the lanes.
 template <int D>
-__device__ __forceinline__ void join_pieces(const ChunkParams& p, int c0, int pieces, int t, int quarter, size_t my_at,
-                                            unsigned valid) {
-    constexpr int DS = D / 32;
+__device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int pieces, int t, int quarter, size_t my_at,
+                                         unsigned valid) {
+    constexpr int DS = D / 32, kR = 4;
     const int lane = threadIdx.x & 31;
-    auto slot = [&](int k) { return size_t(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * kNQ + t; };
+    auto slot = [&](int k) { return (size_t(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * kNQ + t) * kM + quarter * 32; };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    const int mine = quarter * 32 + lane;
-    float M = -INFINITY, l = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < pieces; ++k) M = fmaxf(M, __ldcg(ml + slot(k) * kM + mine).x);
-    auto weight = [&](float2 x) {                          // a piece without a visible token has l = 0
-        return x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : ex2(x.x - M);
-    };
-#pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-        const float2 x = __ldcg(ml + slot(k) * kM + mine);
-        l += x.y * weight(x);
-    }
-    const float inv = 1.f / l;
-    // 8 rows at a time, a row's columns across the lanes
     for (unsigned left = valid; left;) {
-        int row[8];
-        bool on[8];
-        float acc[8][DS];
+        int row[kR];
+        bool on[kR];
+        float acc[kR][DS], M[kR], l[kR], w[kR];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < kR; ++i) {
             on[i] = left != 0;
             row[i] = on[i] ? __ffs(left) - 1 : 0;
             left &= left - 1;
+            M[i] = -INFINITY;
+            l[i] = 0.f;
 #pragma unroll
             for (int e = 0; e < DS; ++e) acc[i][e] = 0.f;
         }
-#pragma unroll 2
-        for (int k = 0; k < pieces; ++k) {
-            const size_t s0 = slot(k) * kM;
-            const float w = weight(__ldcg(ml + s0 + mine));
-            float x[8][DS];
+        float2 x[kR];
+        auto fetch = [&](int k0) {                         // pieces k0 .. k0 + 31
+            const int k = k0 + lane;
+            const size_t s0 = slot(k < pieces ? k : 0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float* src = p.part_acc + (s0 + quarter * 32 + row[i]) * D + lane * DS;
-                if constexpr (DS == 4) {
-                    const float4 y = on[i] ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0, 0, 0, 0);
-                    x[i][0] = y.x; x[i][1] = y.y; x[i][2] = y.z; x[i][3] = y.w;
-                } else {
-                    const float2 y = on[i] ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0, 0);
-                    x[i][0] = y.x; x[i][1] = y.y;
-                }
+            for (int i = 0; i < kR; ++i)
+                x[i] = on[i] && k < pieces ? __ldcg(ml + s0 + row[i]) : make_float2(-INFINITY, 0.f);
+        };
+        for (int k0 = 0; k0 < pieces; k0 += 32) {
+            fetch(k0);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) M[i] = fmaxf(M[i], warp_max(x[i].x));
+        }
+        for (int k0 = 0; k0 < pieces; k0 += 32) {
+            if (pieces > 32) fetch(k0);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) {                  // a piece without a visible token has l = 0
+                w[i] = x[i].x == -INFINITY ? (x[i].y == 0.f ? 0.f : 1.f) : ex2(x[i].x - M[i]);
+                l[i] += warp_sum(w[i] == 0.f ? 0.f : x[i].y * w[i]);
             }
+            const int kn = min(32, pieces - k0);
+#pragma unroll 4
+            for (int k = 0; k < kn; ++k) {
+                const float* src = p.part_acc + slot(k0 + k) * D + lane * DS;
+                float y[kR][DS];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, row[i]);
-                if (wi != 0.f)                             // an empty piece's O may hold anything
+                for (int i = 0; i < kR; ++i) {
+                    if constexpr (DS == 4) {
+                        const float4 z = on[i] ? __ldcg(reinterpret_cast<const float4*>(src + row[i] * D))
+                                               : make_float4(0, 0, 0, 0);
+                        y[i][0] = z.x; y[i][1] = z.y; y[i][2] = z.z; y[i][3] = z.w;
+                    } else {
+                        const float2 z = on[i] ? __ldcg(reinterpret_cast<const float2*>(src + row[i] * D)) : make_float2(0, 0);
+                        y[i][0] = z.x; y[i][1] = z.y;
+                    }
+                }
 #pragma unroll
-                    for (int e = 0; e < DS; ++e) acc[i][e] = fmaf(x[i][e], wi, acc[i][e]);
+                for (int i = 0; i < kR; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, w[i], k);
+#pragma unroll
+                    for (int e = 0; e < DS; ++e) acc[i][e] = wi == 0.f ? acc[i][e] : fmaf(y[i][e], wi, acc[i][e]);
+                }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = __shfl_sync(0xffffffffu, inv, row[i]);
+        for (int i = 0; i < kR; ++i) {
             const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)my_at, row[i]);
             if (!on[i]) continue;
+            const float f = 1.f / l[i];
             uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at) + lane * (DS / 2);
             if constexpr (DS == 4)
                 *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[i][0] * f, acc[i][1] * f),
@@ -462,15 +497,133 @@ __device__ __forceinline__ void join_pieces(const ChunkParams& p, int c0, int pi
     }
 }
 
+// (d0, d1) = (a0 b0 + c, a1 b1 + c) and (d0, d1) *= (b0, b1), one packed instruction each
+__device__ __forceinline__ void fma_pairs(float& d0, float& d1, float a0, float a1, float b0, float b1, float c) {
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %6};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c));
+}
+__device__ __forceinline__ void mul_pairs(float& d0, float& d1, float b0, float b1) {
+    asm("{\n\t.reg .b64 rb, rd;\n\tmov.b64 rd, {%0, %1};\n\tmov.b64 rb, {%2, %3};\n\t"
+        "mul.rn.f32x2 rd, rd, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "+f"(d0), "+f"(d1) : "f"(b0), "f"(b1));
+}
+
 // ------------------------------------------------------------------ e4m3 -> operands
 
 // Two e4m3 codes -> packed bf16, exact: every e4m3 value, NaN among them, is a bf16 value.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint16_t c) {
-    uint32_t h = e4m3x2_to_f16x2(c), r;
+// (Moving the bits with prmt, shifts, masks and a multiplication by 2^120 measured slower,
+// 599 us against 585 at 32 x 64 rows x 8 heads over 8256 tokens, before its NaN codes.)
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t c) {
+    const uint32_t h = e4m3x2_to_f16x2(uint16_t(c));
+    uint32_t r;
     asm("{\n\t.reg .f16 lo, hi;\n\t.reg .f32 a, b;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 a, lo;\n\tcvt.f32.f16 b, hi;\n\t"
         "cvt.rn.bf16x2.f32 %0, b, a;\n\t}"
         : "=r"(r) : "r"(h));
     return r;
+}
+// 16 codes -> 16 bf16
+__device__ __forceinline__ void codes_to_bf16(const uint4& in, uint4& a, uint4& b) {
+    a = make_uint4(e4m3x2_to_bf16x2(in.x), e4m3x2_to_bf16x2(in.x >> 16), e4m3x2_to_bf16x2(in.y),
+                   e4m3x2_to_bf16x2(in.y >> 16));
+    b = make_uint4(e4m3x2_to_bf16x2(in.z), e4m3x2_to_bf16x2(in.z >> 16), e4m3x2_to_bf16x2(in.w),
+                   e4m3x2_to_bf16x2(in.w >> 16));
+}
+
+// 64 contiguous bytes (a page's scales of one head) into shared memory
+__device__ __forceinline__ void bulk_load_64(void* dst, const void* src, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 64, [%2];" ::"r"(
+                     smem_u32(dst)), "l"(src), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// One warp streams the codes and scales of K (or V) of a segment into rings of kRaw stages,
+// a tile of 64 rows of D bytes and 64 floats per stage.  Lanes 0 .. 3 own a page each: a
+// page that lies wholly in the sequence arrives by TMA, the partly filled last one is written
+// by the warp, zeros behind the last token, and so is a bad page id (flagged) or a page
+// behind the segment.  `g` counts tiles over the CTA's life.  False after a timeout or an
+// abort.
+template <int D>
+__device__ __forceinline__ bool produce_codes(const ChunkParams& p, const CUtensorMap* map, const unsigned char* src,
+                                              const float* scales, unsigned char* ring, float* sring, uint64_t* full,
+                                              uint64_t* empty, const Seg& s, int& g, volatile uint32_t* abort_flag) {
+    const int lane = threadIdx.x & 31;
+    const int* ptab = p.page_table + size_t(s.b) * p.max_pages;
+    auto fetch = [&](int bi) -> int {                      // page ids of 8 tiles, one warp-wide load
+        const int pos = s.t0 + (8 * bi + lane / 4) * kBN + (lane % 4) * 16;
+        return pos < s.t1 ? __ldg(ptab + (pos >> 4)) : -1;
+    };
+    int cur = fetch(0), nxt = fetch(1);
+    for (int j = 0; j < s.ntiles; ++j, ++g) {
+        const int st = g % kRaw;
+        if (j > 0 && (j & 7) == 0) {
+            cur = nxt;
+            nxt = fetch(j / 8 + 1);
+        }
+        int page = __shfl_sync(0xffffffffu, cur, (j & 7) * 4 + (lane & 3));
+        const int base = s.t0 + j * kBN, pos0 = base + (lane & 3) * 16;
+        int kind = 0;                                      // 1: by TMA, 2: written here
+        if (lane < 4) {
+            kind = 2;
+            if (pos0 < s.t1) {
+                const bool ok = page >= 0 && page < p.num_pool_pages;
+                if (!ok) atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
+                if (ok && pos0 + 16 <= s.L) kind = 1;
+                if (!ok) page = -1;
+            } else {
+                page = -1;
+            }
+        }
+        if (g >= kRaw && !mbar_wait_bounded(&empty[st], ((g / kRaw) - 1) & 1, p.wait_ns)) {
+            *abort_flag = 1;
+            atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+        }
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+        unsigned char* dst = ring + st * (kBN * D);
+        float* sdst = sring + st * kBN;
+        const unsigned manual = __ballot_sync(0xffffffffu, kind == 2);
+        for (unsigned w = manual; w; w &= w - 1) {
+            const int pg = __ffs(w) - 1;
+            const int id = __shfl_sync(0xffffffffu, page, pg);
+            const int q0 = base + pg * 16;
+            for (int c = lane; c < D; c += 32) {
+                const int rr = c / (D / 16), cc = c % (D / 16);
+                uint4 val = make_uint4(0, 0, 0, 0);
+                if (id >= 0 && q0 + rr < s.t1)
+                    val = __ldg(reinterpret_cast<const uint4*>(src + ((size_t(id) * kPage + rr) * p.Hkv + s.h) * D) + cc);
+                *reinterpret_cast<uint4*>(dst + (pg * 16 + rr) * D + cc * 16) = val;
+            }
+            if (lane < 16)
+                sdst[pg * 16 + lane] =
+                    id >= 0 && q0 + lane < s.t1 ? __ldg(scales + (size_t(id) * p.Hkv + s.h) * kPage + lane) : 0.f;
+        }
+        // the writes above reach the converting warps through the arrival below; the next use of
+        // the stage by TMA comes after their own arrivals and needs the proxy fence
+        if (manual) fence_proxy_async_smem();
+        __syncwarp();
+        const unsigned viatma = __ballot_sync(0xffffffffu, kind == 1);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(__popc(viatma)) * (16u * D + 64u));
+        __syncwarp();
+        if (kind == 1) {
+            tma_load_3d(dst + lane * 16 * D, map, 0, s.h, page * 16, &full[st]);
+            bulk_load_64(sdst + lane * 16, scales + (size_t(page) * p.Hkv + s.h) * kPage, &full[st]);
+        }
+        __syncwarp();
+    }
+    return true;
+}
+
+// Wait for the phase with `parity` by polling, for the hand-offs inside the pipeline.  False
+// after limit_ns, or when the CTA has been told to stop.  Reading the clock at every poll
+// paces the polls: with one reading in 64 they take issue slots from the softmax (472 us
+// against 463 for 2048 rows x 64 heads over 6000 .. 12000 tokens).
+__device__ __forceinline__ bool poll(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort_flag) {
+    if (mbar_test_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if (*abort_flag || global_ns() - t0 >= limit_ns) return false;
+    }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -486,14 +639,54 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(sm + C::kOffMisc + 4);
     End* ends = reinterpret_cast<End*>(sm + C::kOffEnds);
+    SeqRows* first_rows = reinterpret_cast<SeqRows*>(ends + 2);
     long long* tiles_s = reinterpret_cast<long long*>(sm + C::kOffTiles);
     int* units_s = reinterpret_cast<int*>(sm + C::kOffUnits);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    grid_dep_wait();                                       // trees: the prologue's results
     if (smem_u32(sm) & 1023u) {                            // never expected; refuse rather than misread tiles
+        grid_dep_wait();
         if (tid == 0) atomicOr(p.status, TREESPEC_STATUS_INTERNAL);
         return;
     }
+    // barriers and tensor memory, while other warps look at the lengths
+    if (warp == kWarpMma) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == kWarpMma + 1 && lane == 0) {
+        for (int s = 0; s < kNS; ++s) {
+            mbar_init(&bars->k_full[s], E4M3 ? 64 : 1);
+            mbar_init(&bars->k_empty[s], kNQ);
+            mbar_init(&bars->v_full[s], E4M3 ? 64 : 1);
+            mbar_init(&bars->v_empty[s], kNQ);
+        }
+        for (int t = 0; t < kNQ; ++t) {
+            mbar_init(&bars->q_full[t], kM);
+            for (int bf = 0; bf < 2; ++bf) {
+                mbar_init(&bars->s_full[t][bf], 1);
+                mbar_init(&bars->p_full[t][bf], kM);
+                mbar_init(&bars->pv_done[t][bf], 1);
+            }
+            mbar_init(&bars->o_full[t], 1);
+            mbar_init(&bars->o_free[t], kM);
+            mbar_init(&bars->drain[t], 1);
+        }
+        if (E4M3) {
+            for (int s = 0; s < kRaw; ++s) {
+                mbar_init(&bars->rk_full[s], 1);
+                mbar_init(&bars->rk_empty[s], 64);
+                mbar_init(&bars->rv_full[s], 1);
+                mbar_init(&bars->rv_empty[s], 64);
+            }
+            for (int s = 0; s < kScaleRing; ++s) {
+                mbar_init(&bars->sck_full[s], kBN);
+                mbar_init(&bars->scv_full[s], kBN);
+            }
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    grid_dep_wait();                                       // trees: the prologue's results
 
     // ---- the sequences' tiles and units, and this CTA's range
     {
@@ -550,11 +743,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     cut.B = p.B;
     cut.Hkv = p.Hkv;
     {
-        // the fixed cost counts where the ranges are long against it
-        const long long w0 = p.Hkv * tiles_s[p.B], w1 = w0 + (long long)kKappa * p.Hkv * units_s[p.B];
-        cut.k = w1 >= (long long)(kKappa + 2) * gridDim.x ? kKappa : 0;
-        cut.total = cut.k ? w1 : w0;
-        cut.parts = int(max(1ll, min((long long)gridDim.x, cut.total)));
+        // A range that holds pieces of two units pays the fixed cost twice, so where there is less
+        // than about that cost for each CTA, every unit gets CTAs of its own instead (measured:
+        // FIXME)
+        const long long units = (long long)p.Hkv * units_s[p.B];
+        cut.k = kKappa;
+        cut.total = p.Hkv * tiles_s[p.B] + kKappa * units;
+        cut.m = cut.total < (long long)(kKappa + 2) * gridDim.x && units <= gridDim.x && units > 0
+                    ? int(gridDim.x) / int(units) : 0;
+        cut.parts = cut.m ? cut.m * int(units) : int(min((long long)gridDim.x, max(1ll, cut.total / (kKappa + 1))));
     }
     // rows without a token (a padded tree's, and those of an invalid sequence) are zeros
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -565,147 +762,90 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         for (size_t e = tid; e < words; e += C::kThreads) dst[e] = make_uint4(0, 0, 0, 0);
     }
     const int me = blockIdx.x;
-    if (cut.total == 0 || me >= cut.parts) return;
+    if (cut.total == 0 || me >= cut.parts) {               // nothing to compute
+        __syncthreads();
+        if (warp == kWarpMma) tmem_dealloc(*tmem_slot, kTmemCols);
+        return;
+    }
     if (warp < 2) {                                        // warp 0 the begin, warp 1 the end of the range
         const int c = me + warp;
         End e;
-        if (c >= cut.parts) e = End{p.B, 0, 0, 0};
-        else e = locate(p, cut, cut.bound(c));
-        if (lane == 0) ends[warp] = e;
+        if (cut.m) {
+            e = unit_at(p, cut, me / cut.m);
+            const int n = seq_units(p, seq_rows(p, e.b)).tiles(e.pr);
+            const int pieces = unit_pieces(n, cut.m), k = me % cut.m + warp;
+            e.j = k > pieces ? n : int((long long)n * k / pieces);   // beyond the last piece: nothing
+        } else if (c >= cut.parts) {
+            e = End{p.B, 0, 0, 0};
+        } else {
+            e = locate(p, cut, cut.bound(c));
+        }
+        if (lane == 0) {
+            ends[warp] = e;
+            if (warp == 0) *first_rows = seq_rows(p, e.b);
+        }
     }
 
-    if (tid == 0) {
-        for (int s = 0; s < kNS; ++s) {
-            mbar_init(&bars->k_full[s], E4M3 ? 128 : 1);
-            mbar_init(&bars->k_empty[s], kNQ);
-            mbar_init(&bars->v_full[s], E4M3 ? 128 : 1);
-            mbar_init(&bars->v_empty[s], kNQ);
-        }
-        for (int t = 0; t < kNQ; ++t) {
-            mbar_init(&bars->q_full[t], kM);
-            for (int bf = 0; bf < 2; ++bf) {
-                mbar_init(&bars->s_full[t][bf], 1);
-                mbar_init(&bars->p_full[t][bf], kM);
-                mbar_init(&bars->pv_done[t][bf], 1);
-            }
-            mbar_init(&bars->o_full[t], 1);
-            mbar_init(&bars->o_free[t], kM);
-            mbar_init(&bars->drain[t], 1);
-        }
-        for (int s = 0; s < kScaleRing; ++s) mbar_init(&bars->sc_full[s], kBN);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == kWarpMma) {
-        tmem_alloc(tmem_slot, kTmemCols);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
     const uint32_t sbase = smem_u32(sm);
     Walk walk;
-    walk.start(p, ends[0], ends[1]);
+    walk.start(p, ends[0], ends[1], *first_rows);
     Seg sg;
 
     if (E4M3 && warp >= kWarpConv) {
         // ------------------------------------------------------------ e4m3 -> bf16 operands
-        // Thread i converts half of the 16-byte words of row i / 2: words i % 2 + 2 k.  Its copies
-        // run kRaw tiles ahead in its own words of the raw ring, so only it waits for them.
+        // Two warps convert K, two V.  Thread i of the 64 converts 16-byte word i % (D / 16) of rows
+        // i / (D / 16) + (1024 / D) k, so that the lanes that read together cover whole rows.
         regs_lower<C::kRegsConv>();
-        constexpr int KW = D / 32;                         // 16-byte words per thread and operand
-        const int i = tid - kWarpConv * 32, rowi = i >> 1, half = i & 1;
-        uint4* raw = reinterpret_cast<uint4*>(sm + C::kOffRaw);           // [kRaw][K, V][KW][128]
-        float* scales = reinterpret_cast<float*>(sm + C::kOffScale);      // [kScaleRing][K, V][64]
-        Walk ahead = walk;
-        Seg sa;
-        int ja = 0;
-        bool have = ahead.next(sa);
-        float sc_k[kRaw], sc_v[kRaw];                      // this row's scales, loaded with the copies
-        auto copy = [&](int slot, float& k_scale, float& v_scale) {
-            if (have) {
-                const int pos = sa.t0 + ja * kBN + rowi;
-                long long at = -1;
-                if (pos < sa.t1) {
-                    const int page = __ldg(p.page_table + size_t(sa.b) * p.max_pages + (pos >> 4));
-                    if (page >= 0 && page < p.num_pool_pages) at = (long long)page * kPage + (pos & 15);
-                    else atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
-                }
-                const size_t off = at < 0 ? 0 : size_t(at * p.Hkv + sa.h) * D + half * 16;
-                uint4* dst = raw + size_t(slot) * 2 * KW * 128 + i;
-#pragma unroll
-                for (int k = 0; k < KW; ++k) {
-                    cp_async_16_zfill(dst + k * 128, static_cast<const unsigned char*>(p.k) + off + k * 32, at < 0 ? 0 : 16);
-                    cp_async_16_zfill(dst + (KW + k) * 128, static_cast<const unsigned char*>(p.v) + off + k * 32,
-                                      at < 0 ? 0 : 16);
-                }
-                const size_t sc = at < 0 ? 0 : (size_t(at >> 4) * p.Hkv + sa.h) * kPage + (at & 15);
-                k_scale = at < 0 ? 0.f : __ldg(p.k_scales + sc);
-                v_scale = at < 0 ? 0.f : __ldg(p.v_scales + sc);
-                if (++ja == sa.ntiles) {
-                    ja = 0;
-                    have = ahead.next(sa);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        // one operand's words of a tile into its stage
-        auto widen = [&](const uint4* src, unsigned char* stage) {
-#pragma unroll
-            for (int k = 0; k < KW; ++k) {
-                const uint4 w = src[k * 128];
-                const int word = half + 2 * k;             // 16 elements: panel word / 4, chunks 2 (word % 4) and the next
-                const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    o[2 * e] = e4m3x2_to_bf16x2(uint16_t(in[e]));
-                    o[2 * e + 1] = e4m3x2_to_bf16x2(uint16_t(in[e] >> 16));
-                }
-                unsigned char* dst = stage + (word >> 2) * C::kPanel;
-                const int ch = (word & 3) * 2;
-                *reinterpret_cast<uint4*>(dst + sw128_offset(rowi, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4*>(dst + sw128_offset(rowi, ch + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-        };
-#pragma unroll
-        for (int s = 0; s < kRaw; ++s) copy(s, sc_k[s], sc_v[s]);
+        constexpr int WPR = D / 16;                        // words of a row
+        constexpr int RPI = 64 / WPR;                      // rows at a time
+        const bool is_v = warp >= kWarpConv + 2;
+        const int i = tid & 63, word = i % WPR, row0 = (i / WPR) ^ (word >> 2);
+        // element 16 word: panel word / 4, 16-byte chunks 2 (word % 4) and the next of its row.  The
+        // lanes of the second panel work on the neighbouring row, whose swizzle sends them to the
+        // banks that the first panel's lanes leave free
+        const int ch = (word & 3) * 2;
+        const unsigned char* raw = sm + C::kOffRaw + (is_v ? kRaw * C::kRawTile : 0) + row0 * D + word * 16;
+        const float* rsc = reinterpret_cast<const float*>(sm + C::kOffRawScale) + (is_v ? kRaw * kBN : 0) + i;
+        float* scales = reinterpret_cast<float*>(sm + C::kOffScale) + (is_v ? kBN : 0) + i;
+        unsigned char* ring = sm + (is_v ? C::kOffV : C::kOffK) + (word >> 2) * C::kPanel;
+        uint64_t* raw_full = is_v ? bars->rv_full : bars->rk_full;
+        uint64_t* raw_empty = is_v ? bars->rv_empty : bars->rk_empty;
+        uint64_t* full = is_v ? bars->v_full : bars->k_full;
+        uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
+        uint64_t* sc_full = is_v ? bars->scv_full : bars->sck_full;
+        const float sc_mul = is_v ? 1.f : p.scale_log2;
         bool ok = true;
-        int g = 0, slot = 0;
+        int g = 0;
         while (ok && walk.next(sg)) {
             for (int j = 0; j < sg.ntiles; ++j, ++g) {
-                asm volatile("cp.async.wait_group %0;" ::"n"(kRaw - 1) : "memory");
-                const int st = g % kNS;
-                const uint4* src = raw + size_t(slot) * 2 * KW * 128 + i;
-                // the scale slot was read three tiles ago at the latest: V's stage of the tile
-                // before last has been freed by MMAs that came after those reads
-                float* sc = scales + (g % kScaleRing) * 2 * kBN;
-                if (half == 0) {
-                    sc[rowi] = sc_k[0] * p.scale_log2;
-                    sc[kBN + rowi] = sc_v[0];
-                    mbar_arrive(&bars->sc_full[g % kScaleRing]);
+                const int st = g % kNS, rs = g % kRaw;
+                ok = poll(&raw_full[rs], (g / kRaw) & 1, p.wait_ns, abort_flag) &&
+                     (g < kNS || poll(&empty[st], ((g / kNS) - 1) & 1, p.wait_ns, abort_flag)) && !*abort_flag;
+                if (!ok) break;
+                // The scale slot's last readers worked four tiles ago: K's stage was handed back by
+                // S of tile g - 2, which waited for P V of tile g - 4 (V's by P V of tile g - 2)
+                scales[(g % kScaleRing) * 2 * kBN] = rsc[rs * kBN] * sc_mul;
+                mbar_arrive(&sc_full[g % kScaleRing]);
+                const unsigned char* src = raw + rs * C::kRawTile;
+                unsigned char* dst = ring + st * C::kTile;
+#pragma unroll 2
+                for (int k = 0; k < kBN / RPI; ++k) {
+                    const uint4 in = *reinterpret_cast<const uint4*>(src + RPI * k * D);
+                    uint4 a, b;
+                    codes_to_bf16(in, a, b);
+                    const int r = row0 + RPI * k;
+                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch)) = a;
+                    *reinterpret_cast<uint4*>(dst + sw128_offset(r, ch + 1)) = b;
                 }
-                if (g >= kNS) ok = mbar_wait_bounded(&bars->k_empty[st], ((g / kNS) - 1) & 1, p.wait_ns);
-                if (!ok || *abort_flag) { ok = false; break; }
-                widen(src, sm + C::kOffK + st * C::kTile);
+                mbar_arrive(&raw_empty[rs]);
                 fence_proxy_async_smem();
-                mbar_arrive(&bars->k_full[st]);
-                if (g >= kNS) ok = mbar_wait_bounded(&bars->v_empty[st], ((g / kNS) - 1) & 1, p.wait_ns);
-                if (!ok || *abort_flag) { ok = false; break; }
-                widen(src + KW * 128, sm + C::kOffV + st * C::kTile);
-                fence_proxy_async_smem();
-                mbar_arrive(&bars->v_full[st]);
-#pragma unroll
-                for (int s = 0; s + 1 < kRaw; ++s) {
-                    sc_k[s] = sc_k[s + 1];
-                    sc_v[s] = sc_v[s + 1];
-                }
-                copy(slot, sc_k[kRaw - 1], sc_v[kRaw - 1]);
-                slot = slot + 1 == kRaw ? 0 : slot + 1;
+                mbar_arrive(&full[st]);
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (!ok) {
             *abort_flag = 1;
             atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
@@ -734,19 +874,33 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     if (!tcparts::produce_pages<kBN, D>(p, a, sg.b, sg.h, sg.t0, sg.t1, sg.L, sg.ntiles, armed, abort_flag))
                         break;
                 tcparts::drain_copies(a, armed);
+            } else {
+                const bool is_v = warp == kWarpV;
+                uint64_t* full = is_v ? bars->rv_full : bars->rk_full;
+                int armed = 0;
+                while (walk.next(sg))
+                    if (!produce_codes<D>(p, is_v ? &tmv : &tmk, static_cast<const unsigned char*>(is_v ? p.v : p.k),
+                                          is_v ? p.v_scales : p.k_scales, sm + C::kOffRaw + (is_v ? kRaw * C::kRawTile : 0),
+                                          reinterpret_cast<float*>(sm + C::kOffRawScale) + (is_v ? kRaw * kBN : 0), full,
+                                          is_v ? bars->rv_empty : bars->rk_empty, sg, armed, abort_flag))
+                        break;
+                tcparts::ProducerArgs a{};                 // only what the drain looks at
+                a.full = full;
+                a.nst = kRaw;
+                tcparts::drain_copies(a, armed);
             }
         } else {
             // ------------------------------------------------------------ MMA issuers
-            // Warp 10 + t issues every MMA of tile t; one elected lane issues each group and its
-            // commits.  g counts the KV tiles over the CTA's life (ring stages), a those that this
+            // Warp 10 + t issues every MMA of tile t; the whole warp runs the loop and one elected lane
+            // issues (a loop run by one lane alone measured 590 us for 460).  g counts the KV tiles over the CTA's life (ring stages), a those that this
             // query tile takes part in (S buffers), k its segments (Q, O).  A tile that sits a
             // segment out only hands the stages back.
             const int t = warp - kWarpMma;
-            auto ready = [&](uint64_t* x, uint32_t px) -> bool {
+            auto ready = [&](uint64_t* x, uint32_t px) -> bool {   // poll() of the whole warp
                 const uint64_t t0 = global_ns();
                 for (;;) {
                     if (__all_sync(0xffffffffu, mbar_test_wait(x, px))) return true;
-                    if (*abort_flag || global_ns() - t0 > p.wait_ns) return false;
+                    if (__any_sync(0xffffffffu, *abort_flag || global_ns() - t0 >= p.wait_ns)) return false;
                 }
             };
             constexpr uint32_t kIdS = idesc_bf16_f32(128, kBN, false);
@@ -789,8 +943,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                                 const uint64_t koff = uint64_t(((kk >> 2) * C::kPanel + (kk & 3) * 32) >> 4);
                                 mma_bf16_ss(dS + bf * 64u, dq + qoff, kb + koff, kIdS, kk > 0);
                             }
-                            mma_commit(&bars->k_empty[st]);
                             mma_commit(&bars->s_full[t][bf]);
+                            mma_commit(&bars->k_empty[st]);
                         }
                         __syncwarp();
                     }
@@ -807,8 +961,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                             for (int kk = 0; kk < kBN / 16; ++kk)
                                 mma_bf16_ts(dO, dS + bf * 64u + kk * 8, vb + uint64_t((kk * 2048) >> 4), kIdO,
                                             (jp > 0 || kk > 0));
-                            mma_commit(&bars->v_empty[st]);
                             mma_commit(&bars->pv_done[t][bf]);
+                            mma_commit(&bars->v_empty[st]);
                             if (jp == ntiles - 1) mma_commit(&bars->o_full[t]);
                         }
                         __syncwarp();
@@ -890,7 +1044,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     tcparts::tile_mask<kBN>(mw, base, s.S, s.t1, si.a0, si.a1, ro.ok);
                 }
                 const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xffffffffu || !ro.ok);
-                if (!mbar_wait_spin(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns)) { alive = false; break; }
+                if (!poll(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns, abort_flag)) { alive = false; break; }
                 tc_fence_after();
                 if (j == s.ntiles - 1) {                   // Q is read no more: the next segment's may come
                     more = next_seg(nxt, skip2);
@@ -915,7 +1069,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     } else {
                         const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) +
                                            ((g + j) % kScaleRing) * 2 * kBN;
-                        if (!mbar_wait_bounded(&bars->sc_full[(g + j) % kScaleRing], ((g + j) / kScaleRing) & 1, p.wait_ns)) {
+                        const uint32_t sph = ((g + j) / kScaleRing) & 1;
+                        if (!poll(&bars->sck_full[(g + j) % kScaleRing], sph, p.wait_ns, abort_flag) ||
+                            !poll(&bars->scv_full[(g + j) % kScaleRing], sph, p.wait_ns, abort_flag)) {
                             alive = false;
                             break;
                         }
@@ -928,23 +1084,27 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                             for (int c = 0; c < kBN / 4; ++c) {
                                 const float4 ks = reinterpret_cast<const float4*>(scl)[c];
                                 const float4 vs = reinterpret_cast<const float4*>(scl + kBN)[c];
-                                const float kk[4] = {ks.x, ks.y, ks.z, ks.w}, vv[4] = {vs.x, vs.y, vs.z, vs.w};
-                                float x[4], y[4];
+                                const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
+                                float vv[4] = {vs.x, vs.y, vs.z, vs.w};
+                                float x[4];
+                                fma_pairs(x[0], x[1], __uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]), kk[0], kk[1], -m);
+                                fma_pairs(x[2], x[3], __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]), kk[2], kk[3],
+                                          -m);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    x[e] = fmaf(__uint_as_float(v[4 * c + e]), kk[e], -m);
-                                    y[e] = vv[e];
                                     if constexpr (decltype(masked)::value) {
                                         const bool seen = (mw[c >> 3] >> ((4 * c + e) & 31)) & 1u;
                                         x[e] = seen ? x[e] : -INFINITY;
-                                        y[e] = seen ? y[e] : 0.f;
+                                        vv[e] = seen ? vv[e] : 0.f;
                                     }
                                     x[e] = ex2(x[e]);
                                 }
                                 add_f32x2(a0, a1, x[0], x[1]);
                                 add_f32x2(a2, a3, x[2], x[3]);
-                                v[2 * c] = pack_bf16x2(x[0] * y[0], x[1] * y[1]);
-                                v[2 * c + 1] = pack_bf16x2(x[2] * y[2], x[3] * y[3]);
+                                mul_pairs(x[0], x[1], vv[0], vv[1]);
+                                mul_pairs(x[2], x[3], vv[2], vv[3]);
+                                v[2 * c] = pack_bf16x2(x[0], x[1]);
+                                v[2 * c + 1] = pack_bf16x2(x[2], x[3]);
                             }
                             sum = (a0 + a1) + (a2 + a3);
                         };
@@ -1013,36 +1173,53 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             const bool head = s.j0 == 0;
             const size_t slot = size_t(2 * me + (head ? 1 : 0)) * kNQ + t;
             const size_t prow = slot * kM + tlane;
-            if (warp_rows) {
+            float odd = 0.f;                               // stays 0 unless some element is not finite
+            if (warp_rows && whole) {
                 const float inv = 1.f / l;
-                float odd = 0.f;                           // stays 0 unless some element is not finite
+                uint32_t w2[D / 2];                        // the row in bf16: O is free before it is stored
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32(ocol + c * 32, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
-                    if (ro.ok && whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ro.at + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t w4[4];
-#pragma unroll
-                            for (int k2 = 0; k2 < 4; ++k2)
-                                w4[k2] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k2]) * inv,
-                                                     __uint_as_float(o[8 * e + 2 * k2 + 1]) * inv);
-                            dst[e] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-                        }
-                    } else if (ro.ok) {
-                        float4* dst = reinterpret_cast<float4*>(p.part_acc + prow * D + c * 32);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                    for (int e = 0; e < 16; ++e) {
+                        const float x = __uint_as_float(o[2 * e]), y = __uint_as_float(o[2 * e + 1]);
+                        odd = fmaf(x, 0.f, odd);
+                        odd = fmaf(y, 0.f, odd);
+                        w2[c * 16 + e] = pack_bf16x2(x * inv, y * inv);
                     }
                 }
-                if (!whole && ro.ok) __stcg(reinterpret_cast<float2*>(p.part_ml) + prow, make_float2(m_used, l));
+                tc_fence_before();
+                mbar_arrive(&bars->o_free[t]);
+                if (ro.ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ro.at);
+#pragma unroll
+                    for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(w2[4 * e], w2[4 * e + 1], w2[4 * e + 2], w2[4 * e + 3]);
+                }
+            } else {
+                if (warp_rows) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(ocol + c * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
+                        if (ro.ok) {
+                            float4* dst = reinterpret_cast<float4*>(p.part_acc + prow * D + c * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+                        }
+                    }
+                    if (ro.ok) __stcg(reinterpret_cast<float2*>(p.part_ml) + prow, make_float2(m_used, l));
+                }
+                tc_fence_before();
+                mbar_arrive(&bars->o_free[t]);
+            }
+            if (warp_rows) {
                 for (unsigned w = __ballot_sync(0xffffffffu, ro.ok && !(odd == 0.f)); w; w &= w - 1) {
                     const int x = __ffs(w) - 1;            // one row at a time, by the whole warp
                     const Row rx = row_of(p, s, t, x * 4 + quarter, D);
@@ -1058,14 +1235,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     if (!whole && lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + px, make_float2(mx, lx));
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&bars->o_free[t]);
             if (!whole && warp_rows) {
                 // the last of the warps that hold these rows joins the unit's pieces
-                const SeqUnits u = seq_units(p, seq_rows(p, s.b));
-                const long long ub = cut.before(s.b) + s.h * ((cut.before(s.b + 1) - cut.before(s.b)) / cut.Hkv) +
-                                     u.tiles_before(s.pr) + (long long)cut.k * s.pr + cut.k;
-                const int c0 = cut.owner(ub), pieces = cut.owner(ub + s.n - 1) - c0 + 1;
+                int c0, pieces;
+                if (cut.m) {
+                    c0 = me / cut.m * cut.m;
+                    pieces = unit_pieces(s.n, cut.m);
+                } else {
+                    const SeqUnits u = seq_units(p, seq_rows(p, s.b));
+                    const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
+                                         u.tiles_before(s.pr) + (long long)cut.k * s.pr + cut.k;
+                    c0 = cut.owner(ub);
+                    pieces = cut.owner(ub + s.n - 1) - c0 + 1;
+                }
                 __threadfence();
                 __syncwarp();
                 int n = 0;
@@ -1099,11 +1281,9 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     using C = Cfg<D, E4M3>;
     if (p.B > kChunkMaxBatch || p.ctas < 1 || p.ctas > kChunkMaxCtas || p.G > kM) return cudaErrorInvalidValue;
     CUtensorMap mk = {}, mv = {};
-    if (!E4M3) {
-        const long long pool_tokens = (long long)p.num_pool_pages * kPage;
-        if (!make_pool_map(&mk, p.k, p.Hkv, pool_tokens, D) || !make_pool_map(&mv, p.v, p.Hkv, pool_tokens, D))
-            return cudaErrorInvalidValue;
-    }
+    const long long pool_tokens = (long long)p.num_pool_pages * kPage;
+    auto make = E4M3 ? make_code_map : make_pool_map;
+    if (!make(&mk, p.k, p.Hkv, pool_tokens, D) || !make(&mv, p.v, p.Hkv, pool_tokens, D)) return cudaErrorInvalidValue;
     auto kern = chunk_tc_kernel<D, E4M3>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;

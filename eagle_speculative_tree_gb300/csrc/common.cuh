@@ -148,6 +148,8 @@ cudaError_t launch_attn_tc_stream(const AttnParams& p, cudaStream_t s);
 bool attn_tc_supported(int dtype, int D);
 // TMA map of a K or V page pool [P][16][Hkv][D] bf16, one page x 64 head dims per box
 bool make_pool_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens, int D = 128);
+// TMA map of an 8-bit pool of codes [P][16][Hkv][D], one page of one head per box, not swizzled
+bool make_code_map(CUtensorMap* map, const void* base, int Hkv, long long pool_tokens, int D);
 cudaError_t launch_attn_merge(const AttnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_accept(const AcceptParams& p, int mode, cudaStream_t s, int* kernels);
 
@@ -219,7 +221,7 @@ struct ChunkParams {
                                               // the CTA cut, zero at launch
     int B, T, N, Hq, Hkv, G, D, ps, max_pages, num_pool_pages;
     int num_splits, split_tokens, rows_block; // SIMT
-    int ctas;                                 // persistent
+    int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
     float scale_log2;
     uint64_t wait_ns;
 };

@@ -321,6 +321,37 @@ def test_scores_that_rise_along_the_sequence(ts, cuda_device, dtype, e4m3):
     check_chunk(ts, p, ts.KERNEL_AUTO)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_every_e4m3_code_reads_as_its_value(ts, cuda_device, dtype, dim):
+    """One row per token and equal scores over a single token: row 0 of each one-token sequence
+    returns V itself.  256 sequences, V of sequence c filled with code c."""
+    p = make(cuda_device, [0] * 256, [1] * 256, 2, 1, dim, dtype, True, seed=3)
+    page = p.page_table[:, 0].long()
+    codes = torch.arange(256, dtype=torch.uint8, device=cuda_device)
+    p.v_pages.view(torch.uint8)[page, 0, 0, :] = codes[:, None]
+    p.v_scales[page, 0, 0] = 0.75
+    got, st = attend(ts, p, ts.KERNEL_AUTO)
+    ref = och.e4m3_values()[:, None, None] * 0.75
+    g = got.double().cpu().numpy()
+    assert st == 0 and np.array_equal(np.isnan(g), np.broadcast_to(np.isnan(ref), g.shape))
+    ok = ~np.isnan(ref[:, 0, 0])
+    assert np.array_equal(g[ok], np.broadcast_to(ref, g.shape)[ok])   # at most 5 significant bits: exact
+    # the same through K: scores 0.01 x code against a token of score 0, V one and zero
+    p = make(cuda_device, [1] * 254, [1] * 254, 1, 1, dim, dtype, True, seed=4)
+    page = p.page_table[:, 0].long()
+    keep = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8, device=cuda_device)
+    p.k_pages.view(torch.uint8)[page, :2] = 0
+    p.v_pages.view(torch.uint8)[page, :2] = 0
+    p.k_pages.view(torch.uint8)[page, 0, 0, 0] = keep
+    p.v_pages.view(torch.uint8)[page, 0] = 0x38
+    p.k_scales[page, 0, :2] = 0.01
+    p.v_scales[page, 0, :2] = 1.0
+    p.q.zero_()
+    p.q[:, 0, 0] = dim ** 0.5 if dim == 64 else 11.3125
+    check_chunk(ts, p, ts.KERNEL_AUTO)
+
+
 def test_chunk_attention_bad_lengths_and_pages(ts, cuda_device):
     for dtype, e4m3 in KINDS:
         p = make(cuda_device, [40, 33, 64], [10, 20, 5], 8, 2, 128, dtype, e4m3, seed=41, tail=4)
