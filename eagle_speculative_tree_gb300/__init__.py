@@ -8,6 +8,7 @@ Importing the package fails if the compiled library is missing -- build it with
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -395,21 +396,50 @@ def tree_rerank(node_parent, node_token, node_score, num_nodes: int, tree_parent
 
 
 # ------------------------------------------------- chunks of new tokens, 8-bit cache
+#
+# These calls are as short as a decoding step's launches, so their checks are one pass over
+# the tensors' attributes, and the C structs of a problem's sizes are made once per size.
 
-class _on_device:
-    """The library launches on the current device: make it the tensors' own for a call."""
+_I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
-    def __init__(self, device):
-        here = torch.cuda.current_device()
-        self._guard = None if device.index is None or device.index == here else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
+def _need_all(index: int, *wants) -> None:
+    """Each want is (tensor, name, dtype, shape): contiguous, on cuda:`index`."""
+    for t, name, dtype, shape in wants:
+        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+        if not t.is_cuda or t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{max(index, 0)}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be contiguous")
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _index_of(q: torch.Tensor, name: str) -> int:
+    if not q.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return q.get_device()
+
+
+def _pool_wants(q_dtype, k_pages, v_pages, k_scales, v_scales) -> tuple:
+    """What _need_all has to see of a pair of page pools."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must have shape [pages][16][kv heads][head_dim]")
+    shape = k_pages.shape
+    if k_pages.dtype is not _E4M3:
+        if k_scales is not None or v_scales is not None:
+            raise ValueError("scales belong to float8_e4m3fn pools only")
+        return (k_pages, "k_pages", q_dtype, shape), (v_pages, "v_pages", q_dtype, shape)
+    if k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales are needed with float8_e4m3fn pools")
+    scales = (shape[0], shape[2], shape[1])
+    return ((k_pages, "k_pages", _E4M3, shape), (v_pages, "v_pages", _E4M3, shape),
+            (k_scales, "k_scales", _F32, scales), (v_scales, "v_scales", _F32, scales))
 
 
 def _fresh(shape, dtype, device, stream) -> torch.Tensor:
@@ -420,41 +450,27 @@ def _fresh(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace_for(workspace, need: int, device, stream) -> torch.Tensor:
+def _workspace_for(workspace, need: int, index: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _fresh((need,), torch.uint8, device, stream)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
     return workspace
 
 
-def _need_shape(t: torch.Tensor, name: str, shape) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _launch(index: int, stream, fn, *args) -> None:
+    """The library launches on the current device: make it the tensors' own for the call."""
+    handle = stream.cuda_stream if stream is not None else _raw_stream(index)
+    if _current_device() == index:
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            code = fn(*args, handle)
+    if code != 0:
+        raise TreespecError(code)
 
 
-def _need_pools(q_dtype, k_pages, v_pages, k_scales, v_scales, device) -> int:
-    """Checks a pair of page pools and their scales; returns the pools' DTYPE_*."""
-    e4m3 = k_pages.dtype == torch.float8_e4m3fn
-    want = torch.float8_e4m3fn if e4m3 else q_dtype
-    _need(k_pages, "k_pages", want, device)
-    _need(v_pages, "v_pages", want, device)
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages must have shape [pages][16][kv heads][head_dim]")
-    _need_shape(v_pages, "v_pages", k_pages.shape)
-    if e4m3:
-        P, ps, Hkv, _ = k_pages.shape
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if t is None:
-                raise ValueError(f"{name} is needed with float8_e4m3fn pools")
-            _need(t, name, torch.float32, device)
-            _need_shape(t, name, (P, Hkv, ps))
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("scales belong to float8_e4m3fn pools only")
-    return DTYPE_E4M3 if e4m3 else DTYPE_BF16 if q_dtype == torch.bfloat16 else DTYPE_F32
-
-
-@dataclass
+@dataclass(frozen=True)
 class ChunkProblem:
     batch: int
     num_tokens: int
@@ -474,21 +490,36 @@ class ChunkProblem:
                           self.kernel)
 
 
-def chunk_problem(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, chunk_offsets: torch.Tensor, *,
-                  kernel: int = KERNEL_AUTO) -> ChunkProblem:
-    """Sizes of a tree_chunk_attn / tree_chunk_append call: q [T][Hq][D], page_table [B][max_pages]."""
+@functools.lru_cache(maxsize=1024)
+def _chunk_struct(*sizes):
+    return ctypes.pointer(ChunkShape(*sizes))
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_struct(*sizes):
+    return ctypes.pointer(AttnShape(*sizes))
+
+
+def _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel) -> tuple:
+    """The sizes of a call in the order of ChunkProblem's fields."""
     if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or chunk_offsets.dim() != 1:
         raise ValueError("q is [tokens][heads][head_dim], k_pages [pages][16][kv heads][head_dim], "
                          "page_table [batch][pages], chunk_offsets [batch + 1]")
     T, Hq, D = q.shape
     P, ps, Hkv, D2 = k_pages.shape
+    B, pages = page_table.shape
     if D2 != D:
         raise ValueError("head_dim of q and k_pages differ")
-    B = page_table.shape[0]
-    _need_shape(chunk_offsets, "chunk_offsets", (B + 1,))
-    dt = DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F32
-    kv = DTYPE_E4M3 if k_pages.dtype == torch.float8_e4m3fn else dt
-    return ChunkProblem(B, T, Hq, Hkv, D, ps, page_table.shape[1], P, dt, kv, kernel)
+    if chunk_offsets.shape[0] != B + 1:
+        raise ValueError(f"chunk_offsets must have shape {(B + 1,)}, got {tuple(chunk_offsets.shape)}")
+    dt = DTYPE_BF16 if q.dtype is _BF16 else DTYPE_F32
+    return B, T, Hq, Hkv, D, ps, pages, P, dt, DTYPE_E4M3 if k_pages.dtype is _E4M3 else dt, kernel
+
+
+def chunk_problem(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor, chunk_offsets: torch.Tensor, *,
+                  kernel: int = KERNEL_AUTO) -> ChunkProblem:
+    """Sizes of a tree_chunk_attn / tree_chunk_append call: q [T][Hq][D], page_table [B][max_pages]."""
+    return ChunkProblem(*_chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel))
 
 
 def append_workspace_bytes() -> int:
@@ -509,49 +540,50 @@ def tree_chunk_append(q, k, v, k_pages, v_pages, page_table, prefix_lens, chunk_
     q_norm / k_norm [D] and inv_freq [rot_dim / 2] float32 (None: no norm, no rotation).
     Returns q_out [T][Hq][D] (q itself may be given); the pools are written in place.  Rows
     that are left out stay as they are in `q_out` (and hold nothing of use in a new one)."""
-    dev, dt = q.device, q.dtype
-    if dt not in (torch.float32, torch.bfloat16):
+    dt = q.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise ValueError("q must be float32 or bfloat16")
-    prob = chunk_problem(q, k_pages, page_table, chunk_offsets)
-    T, Hq, D, Hkv = prob.num_tokens, prob.num_q_heads, prob.head_dim, prob.num_kv_heads
+    index = _index_of(q, "q")
+    sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, KERNEL_AUTO)
+    B, T, Hq, Hkv, D = sizes[:5]
+    strides = []
     for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if not t.is_cuda or t.device != dev or t.dtype != dt:
-            raise ValueError(f"{name} must be {dt} on {dev}")
-        _need_shape(t, name, (T, H, D))
-        if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        if t.dtype is not dt or t.get_device() != index or t.shape != (T, H, D):
+            raise ValueError(f"{name} must be {dt} on cuda:{index} with shape {(T, H, D)}")
+        to_token, to_head, to_element = t.stride()
+        if to_element != 1 or (H > 1 and to_head != D):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
-    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
-    ints = [("page_table", page_table), ("prefix_lens", prefix_lens), ("chunk_offsets", chunk_offsets)]
+        # one token has no distance to the next: its row counts as packed
+        strides.append(to_token if T > 1 else H * D)
+    wants = [*_pool_wants(dt, k_pages, v_pages, k_scales, v_scales), (page_table, "page_table", _I32, (B, sizes[6])),
+             (prefix_lens, "prefix_lens", _I32, (B,)), (chunk_offsets, "chunk_offsets", _I32, (B + 1,))]
     if positions is not None:
-        ints.append(("positions", positions))
-        _need_shape(positions, "positions", (T,))
-    for name, t in ints:
-        _need(t, name, torch.int32, dev)
-    _need_shape(prefix_lens, "prefix_lens", (prob.batch,))
-    for name, t, n in (("q_norm", q_norm, D), ("k_norm", k_norm, D), ("inv_freq", inv_freq, None)):
-        if t is not None:
-            _need(t, name, torch.float32, dev)
-            _need_shape(t, name, (t.numel() if n is None else n,))
-    # one token has no distance to the next: its rows count as packed
-    strides = [t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v)]
+        wants.append((positions, "positions", _I32, (T,)))
+    if q_norm is not None:
+        wants.append((q_norm, "q_norm", _F32, (D,)))
+    if k_norm is not None:
+        wants.append((k_norm, "k_norm", _F32, (D,)))
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        wants.append((inv_freq, "inv_freq", _F32, (rot // 2,)))
     if q_out is None:
-        q_out = _fresh((T, Hq, D), dt, dev, stream)
-    _need(q_out, "q_out", dt, dev)
-    _need_shape(q_out, "q_out", (T, Hq, D))
-    workspace = _workspace_for(workspace, append_workspace_bytes(), dev, stream)
-    opt = AppendOptions(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), _ptr(positions), float(norm_eps), float(rope_scale),
-                        0 if inv_freq is None else 2 * inv_freq.numel(), int(rope))
-    with _on_device(dev):
-        _check(_lib.tree_chunk_append(
-            _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v), strides[2], _ptr(q_out), _ptr(k_pages), _ptr(v_pages),
-            _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens), _ptr(chunk_offsets),
-            ctypes.byref(prob.c_shape()), ctypes.byref(opt), _ptr(workspace), workspace.nbytes,
-            _stream_handle(stream, dev)))
+        q_out = _fresh((T, Hq, D), dt, q.device, stream)
+    else:
+        wants.append((q_out, "q_out", dt, (T, Hq, D)))
+    _need_all(index, *wants)
+    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, append_workspace_bytes(), index, q.device, stream)
+    opt = AppendOptions(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), _ptr(positions), norm_eps, rope_scale, rot, rope)
+    _launch(index, stream, _lib.tree_chunk_append, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(),
+            strides[2], q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
+            page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(), _chunk_struct(*sizes), opt,
+            workspace.data_ptr(), workspace.nbytes)
     return q_out
 
 
 def chunk_attn_workspace_bytes(prob: ChunkProblem) -> int:
-    n = _lib.treespec_chunk_attn_workspace_bytes(ctypes.byref(prob.c_shape()))
+    n = _lib.treespec_chunk_attn_workspace_bytes(prob.c_shape())
     if n == 0:
         raise ValueError(f"unsupported chunk attention shape {prob}")
     return int(n)
@@ -568,25 +600,25 @@ def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets,
     prefix_lens [B], chunk_offsets [B + 1] int32.  Returns out [T][Hq][D] in q's dtype; rows
     that belong to no sequence are left as they are in `out` (and hold nothing of use in a
     new one)."""
-    dev, dt = q.device, q.dtype
-    if dt not in (torch.float32, torch.bfloat16):
+    dt = q.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise ValueError("q must be float32 or bfloat16")
-    _need(q, "q", dt, dev)
-    prob = chunk_problem(q, k_pages, page_table, chunk_offsets, kernel=kernel)
-    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
-    for name, t in (("page_table", page_table), ("prefix_lens", prefix_lens), ("chunk_offsets", chunk_offsets)):
-        _need(t, name, torch.int32, dev)
-    _need_shape(prefix_lens, "prefix_lens", (prob.batch,))
+    index = _index_of(q, "q")
+    sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel)
+    B = sizes[0]
+    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
+             (page_table, "page_table", _I32, (B, sizes[6])), (prefix_lens, "prefix_lens", _I32, (B,)),
+             (chunk_offsets, "chunk_offsets", _I32, (B + 1,))]
     if out is None:
-        out = _fresh(q.shape, dt, dev, stream)
-    _need(out, "out", dt, dev)
-    _need_shape(out, "out", q.shape)
-    workspace = _workspace_for(workspace, chunk_attn_workspace_bytes(prob), dev, stream)
-    with _on_device(dev):
-        _check(_lib.tree_chunk_attn(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens),
-            _ptr(chunk_offsets), _ptr(out), ctypes.byref(prob.c_shape()), _ptr(workspace), workspace.nbytes,
-            _stream_handle(stream, dev)))
+        out = _fresh(q.shape, dt, q.device, stream)
+    else:
+        wants.append((out, "out", dt, q.shape))
+    _need_all(index, *wants)
+    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, chunk_attn_workspace_bytes(ChunkProblem(*sizes)), index, q.device, stream)
+    _launch(index, stream, _lib.tree_chunk_attn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+            _ptr(v_scales), page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(), out.data_ptr(),
+            _chunk_struct(*sizes), workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -605,31 +637,34 @@ def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, p
     q [B][N][Hq][D] (float32 or bfloat16), k_pages / v_pages [P][16][Hkv][D] float8_e4m3fn,
     k_scales / v_scales [P][Hkv][16] float32, page_table [B][max_pages], prefix_lens [B],
     tree_parents [B][N] int32.  Returns out [B][N][Hq][D] in q's dtype."""
-    dev, dt = q.device, q.dtype
-    if dt not in (torch.float32, torch.bfloat16):
+    dt = q.dtype
+    if dt is not _BF16 and dt is not _F32:
         raise ValueError("q must be float32 or bfloat16")
-    _need(q, "q", dt, dev)
+    index = _index_of(q, "q")
     if q.dim() != 4 or page_table.dim() != 2:
         raise ValueError("q is [batch][nodes][heads][head_dim], page_table [batch][pages]")
-    if k_pages.dtype != torch.float8_e4m3fn:
-        raise ValueError(f"k_pages must be {torch.float8_e4m3fn}, got {k_pages.dtype}")
-    _need_pools(dt, k_pages, v_pages, k_scales, v_scales, dev)
-    prob = attn_problem(q, k_pages, page_table, kernel=kernel)
-    for name, t, shape in (("page_table", page_table, (prob.batch, prob.max_pages_per_seq)),
-                           ("prefix_lens", prefix_lens, (prob.batch,)),
-                           ("tree_parents", tree_parents, (prob.batch, prob.num_nodes))):
-        _need(t, name, torch.int32, dev)
-        _need_shape(t, name, shape)
+    if k_pages.dtype is not _E4M3:
+        raise ValueError(f"k_pages must be {_E4M3}, got {k_pages.dtype}")
+    B, N, Hq, D = q.shape
+    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
+             (page_table, "page_table", _I32, (B, page_table.shape[1])), (prefix_lens, "prefix_lens", _I32, (B,)),
+             (tree_parents, "tree_parents", _I32, (B, N))]
     if out is None:
-        out = _fresh(q.shape, dt, dev, stream)
-    _need(out, "out", dt, dev)
-    _need_shape(out, "out", q.shape)
-    workspace = _workspace_for(workspace, attn_e4m3_workspace_bytes(prob), dev, stream)
-    with _on_device(dev):
-        _check(_lib.tree_attn_verify_e4m3(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table), _ptr(prefix_lens),
-            _ptr(tree_parents), _ptr(out), ctypes.byref(prob.c_shape()), _ptr(workspace), workspace.nbytes,
-            _stream_handle(stream, dev)))
+        out = _fresh(q.shape, dt, q.device, stream)
+    else:
+        wants.append((out, "out", dt, q.shape))
+    _need_all(index, *wants)
+    P, ps, Hkv, D2 = k_pages.shape
+    if D2 != D:
+        raise ValueError("head_dim of q and k_pages differ")
+    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, attn_e4m3_workspace_bytes(attn_problem(q, k_pages, page_table, kernel=kernel)),
+                                   index, q.device, stream)
+    _launch(index, stream, _lib.tree_attn_verify_e4m3, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), prefix_lens.data_ptr(), tree_parents.data_ptr(),
+            out.data_ptr(), _attn_struct(B, N, Hq, Hkv, D, ps, page_table.shape[1], P,
+                                         DTYPE_BF16 if dt is _BF16 else DTYPE_F32, kernel, 0),
+            workspace.data_ptr(), workspace.nbytes)
     return out
 
 
@@ -638,29 +673,28 @@ def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix
     """Move the accepted path's codes and scales next to each prefix, in place; see
     include/treespec.h.  Pools and scales as for tree_attn_verify_e4m3, the rest as for
     tree_kv_commit.  Returns new_prefix_lens [B] int32."""
-    dev = k_pages.device
-    if k_pages.dtype != torch.float8_e4m3fn:
-        raise ValueError(f"k_pages must be {torch.float8_e4m3fn}, got {k_pages.dtype}")
-    _need_pools(torch.bfloat16, k_pages, v_pages, k_scales, v_scales, dev)
+    if k_pages.dtype is not _E4M3:
+        raise ValueError(f"k_pages must be {_E4M3}, got {k_pages.dtype}")
+    index = _index_of(k_pages, "k_pages")
     if accept_path.dim() != 2 or page_table.dim() != 2:
         raise ValueError("accept_path is [batch][nodes], page_table [batch][pages]")
     B, N = accept_path.shape
-    P, ps, Hkv, D = k_pages.shape
-    for name, t, shape in (("page_table", page_table, (B, page_table.shape[1])), ("prefix_lens", prefix_lens, (B,)),
-                           ("accept_path", accept_path, (B, N)), ("accept_len", accept_len, (B,))):
-        _need(t, name, torch.int32, dev)
-        _need_shape(t, name, shape)
-    shape = AttnShape(B, N, Hkv, Hkv, D, ps, page_table.shape[1], P, DTYPE_BF16, KERNEL_AUTO, 0)
+    wants = [*_pool_wants(None, k_pages, v_pages, k_scales, v_scales),
+             (page_table, "page_table", _I32, (B, page_table.shape[1])), (prefix_lens, "prefix_lens", _I32, (B,)),
+             (accept_path, "accept_path", _I32, (B, N)), (accept_len, "accept_len", _I32, (B,))]
     if new_prefix_lens is None:
-        new_prefix_lens = _fresh((B,), torch.int32, dev, stream)
-    _need(new_prefix_lens, "new_prefix_lens", torch.int32, dev)
-    _need_shape(new_prefix_lens, "new_prefix_lens", (B,))
-    workspace = _workspace_for(workspace, commit_workspace_bytes(), dev, stream)
-    with _on_device(dev):
-        _check(_lib.tree_kv_commit_e4m3(_ptr(k_pages), _ptr(v_pages), _ptr(k_scales), _ptr(v_scales), _ptr(page_table),
-                                        _ptr(prefix_lens), _ptr(accept_path), _ptr(accept_len), _ptr(new_prefix_lens),
-                                        ctypes.byref(shape), _ptr(workspace), workspace.nbytes,
-                                        _stream_handle(stream, dev)))
+        new_prefix_lens = _fresh((B,), _I32, k_pages.device, stream)
+    else:
+        wants.append((new_prefix_lens, "new_prefix_lens", _I32, (B,)))
+    _need_all(index, *wants)
+    P, ps, Hkv, D = k_pages.shape
+    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, commit_workspace_bytes(), index, k_pages.device, stream)
+    _launch(index, stream, _lib.tree_kv_commit_e4m3, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+            v_scales.data_ptr(), page_table.data_ptr(), prefix_lens.data_ptr(), accept_path.data_ptr(),
+            accept_len.data_ptr(), new_prefix_lens.data_ptr(),
+            _attn_struct(B, N, Hkv, Hkv, D, ps, page_table.shape[1], P, DTYPE_BF16, KERNEL_AUTO, 0),
+            workspace.data_ptr(), workspace.nbytes)
     return new_prefix_lens
 
 

@@ -506,14 +506,23 @@ ChunkPlan chunk_plan(int kernel, int dtype, long long batch, long long rows, int
         return c;
     }
     c.kernel = TREESPEC_KERNEL_SIMT;
+    // Row blocks no larger than the mean sequence fills, and smaller ones where those and
+    // splits of at least 128 tokens would leave SMs without a CTA: a block of 64 rows reads
+    // K and V an eighth as often as one of 8, but a small problem is bound by one CTA's run
+    // (5 sequences of up to 130 tokens x 4 heads over up to 830 tokens of 64, float32: 59 us
+    // with blocks of 64 rows in splits of 256 tokens, FIXME us with this rule).
     const long long mean = (rows + batch - 1) / batch;
-    c.rows_block = mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
-    const long long units = ((rows + c.rows_block - 1) / c.rows_block) * Hkv;
     const long long tokens = (long long)max_pages * kPage;
-    // two CTAs per SM where the row blocks alone do not give them, no split below 256 tokens
-    long long splits = units >= 2ll * sms ? 1 : 2ll * sms / units;
-    splits = std::max(1ll, std::min(splits, tokens / 256));
-    splits = std::min(splits, 256ll);
+    long long splits = 1;
+    for (int rb = 64; rb >= 8; rb /= 2) {
+        if (rb > 8 && mean <= rb / 2) continue;
+        c.rows_block = rb;
+        const long long units = ((rows + rb - 1) / rb) * Hkv;
+        // two CTAs per SM where the row blocks alone do not give them
+        splits = units >= 2ll * sms ? 1 : 2ll * sms / units;
+        splits = std::min(std::max(1ll, std::min(splits, tokens / 128)), 256ll);
+        if (units * splits >= sms) break;
+    }
     long long chunk = (tokens + splits - 1) / splits;
     chunk = (chunk + 127) / 128 * 128;
     c.split_tokens = int(chunk);

@@ -21,6 +21,7 @@ namespace treespec {
 namespace {
 
 constexpr int kRows = 64;                // query rows per CTA, at most
+constexpr int kMaxSmem = 224 * 1024;     // dynamic shared memory a CTA may ask for, beside its static 1 KB
 
 enum KvKind { kKvF32, kKvBf16, kKvE4m3 };
 
@@ -451,8 +452,10 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     if (RB < 1 || RB > kRows) return cudaErrorInvalidValue;
     const long long units = p.offsets ? total_rows / RB + p.B : (long long)p.B * ((p.N * p.G + RB - 1) / RB);
     const Shape sh = shape_of<KV, D>(RB);
+    if (sh.smem > size_t(kMaxSmem)) return cudaErrorInvalidValue;
     auto kern = chunk_simt_kernel<T, KV, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sh.smem));
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(kern, kMaxSmem, smem_set);
     if (e != cudaSuccess) return e;
     kern<<<dim3(unsigned(units), unsigned(p.Hkv), unsigned(p.num_splits)), sh.nwarps * 32, sh.smem, s>>>(p);
     return cudaGetLastError();

@@ -1285,7 +1285,8 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     auto make = E4M3 ? make_code_map : make_pool_map;
     if (!make(&mk, p.k, p.Hkv, pool_tokens, D) || !make(&mv, p.v, p.Hkv, pool_tokens, D)) return cudaErrorInvalidValue;
     auto kern = chunk_tc_kernel<D, E4M3>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(kern, C::kSmemBytes, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.ctas));

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "treespec.h"
 
 namespace treespec {
@@ -137,6 +139,21 @@ struct AcceptParams {
     int probs_on_host;  // draft_probs is host memory read over the CPU-GPU link: fetch a draft
                         // row only where a child is rejected, never ahead
 };
+
+// A kernel's dynamic shared-memory limit, set at its first launch on each device (the
+// attribute belongs to the function and the device; setting it again costs a microsecond).
+// `done`: a bit per device, one such word for each kernel.
+template <class Kernel>
+inline cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Kernel launchers (each returns cudaGetLastError() of its launch).
 cudaError_t launch_tree_prologue(const AttnParams& p, cudaStream_t s);

@@ -102,7 +102,8 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitP
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s) {
     const int smem = max(16, (p.N - 1) * (p.D * p.elem / 16) * 16);
     if (smem > kMaxStageBytes) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(kv_commit_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStageBytes);
+    static std::atomic<uint64_t> smem_set{0};
+    cudaError_t e = allow_smem(kv_commit_kernel, kMaxStageBytes, smem_set);
     if (e != cudaSuccess) return e;
     kv_commit_kernel<<<dim3(unsigned(p.B), unsigned(p.Hkv)), kCommitThreads, smem, s>>>(p);
     return cudaGetLastError();

@@ -437,7 +437,8 @@ size_t treespec_append_workspace_bytes(void);
  * The angle is reduced in 64-bit fixed point, so it keeps its accuracy at any position
  * (below 2^31) for inv_freq below 2^24.
  * 8-bit pools: scale = max(max |x| / 448, 2^-100) over the head, code = x / scale rounded
- * to nearest even; a head with a NaN or an infinity reads back as NaN.
+ * to nearest even (both through a reciprocal, in float32); a head with a NaN or an
+ * infinity reads back as NaN.
  *
  *   q [T][Hq][D], k, v [T][Hkv][D] in shape->dtype: heads contiguous, tokens q_stride /
  *      k_stride / v_stride elements apart (views of one projection's output work); rows
