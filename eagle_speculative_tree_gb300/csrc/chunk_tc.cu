@@ -49,8 +49,9 @@ constexpr int kNQ = 2;               // query tiles
 constexpr int kBN = 64;              // tokens per KV tile
 constexpr int kKappa = 7;            // a unit's fixed cost, in tiles
 constexpr int kRaw = 5;              // e4m3: stages of the rings of codes
-constexpr int kMinTiles = 4;         // no range shorter than this
-constexpr int kScaleRing = 4;        // e4m3: tiles of scales (a slot is rewritten three tiles later at the earliest)
+constexpr int kMinTiles = 4;         // no piece of a unit with CTAs of its own is shorter than this
+constexpr int kWholeTiles = 4;       // units up to this long are not cut
+constexpr int kScaleRing = 4;        // e4m3: tiles of scales
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;        // S buffer b of tile t: [128 t + 64 b, 128 t + 64 b + 64)
 constexpr uint32_t kColO = 256;      // O_t: [256 + 128 t, 256 + 128 t + D)
@@ -253,9 +254,11 @@ struct Walk {
         end = z;
         rows = r;                                          // of sequence a.b
         u = seq_units(pp, r);
+        if (e.b < pp.B && e.j >= u.tiles(e.pr)) advance();
     }
     __device__ __forceinline__ bool next(Seg& s) {
-        if (e.b > end.b) return false;
+        // behind the range: also where both its ends were moved to the same unit's end
+        if (e.b > end.b || (e.b == end.b && (e.h > end.h || (e.h == end.h && e.pr > end.pr)))) return false;
         const bool last = e.b == end.b && e.h == end.h && e.pr == end.pr;
         if (last && e.j >= end.j) return false;
         s.b = e.b;
@@ -274,10 +277,14 @@ struct Walk {
         const int vis = u.S + (u.tree ? u.live : s.i0 + s.tokens);
         s.t0 = s.j0 * kBN;
         s.t1 = min(vis, (s.j0 + s.ntiles) * kBN);
+        if (last) e.b = end.b + 1;                         // done
+        else advance();
+        return true;
+    }
+    // to the first tile of the next unit
+    __device__ __forceinline__ void advance() {
         e.j = 0;
-        if (last) {
-            e.b = end.b + 1;                               // done
-        } else if (++e.pr >= u.np) {
+        if (++e.pr >= u.np) {
             e.pr = 0;
             if (++e.h >= p->Hkv) {
                 e.h = 0;
@@ -288,7 +295,6 @@ struct Walk {
                 } while (u.np == 0);
             }
         }
-        return true;
     }
 };
 
@@ -744,8 +750,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     cut.Hkv = p.Hkv;
     {
         // A range that holds pieces of two units pays the fixed cost twice, so where there is less
-        // than about that cost for each CTA, every unit gets CTAs of its own instead (measured:
-        // FIXME)
+        // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
+        // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
+        // 42 and 29)
         const long long units = (long long)p.Hkv * units_s[p.B];
         cut.k = kKappa;
         cut.total = p.Hkv * tiles_s[p.B] + kKappa * units;
@@ -779,6 +786,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             e = End{p.B, 0, 0, 0};
         } else {
             e = locate(p, cut, cut.bound(c));
+            const int n = seq_units(p, seq_rows(p, e.b)).tiles(e.pr);
+            // Short units stay whole: the cut moves to the nearer end of one, and both neighbours
+            // see it there (160 units of 1 or 2 tiles: 43 us cut, 27 whole; with units of up to 10
+            // tiles kept whole the ranges of ragged prompts get uneven, 388 us against 380)
+            if (n <= kWholeTiles) e.j = 2 * e.j < n ? 0 : n;
         }
         if (lane == 0) {
             ends[warp] = e;
@@ -1044,6 +1056,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     tcparts::tile_mask<kBN>(mw, base, s.S, s.t1, si.a0, si.a1, ro.ok);
                 }
                 const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xffffffffu || !ro.ok);
+                if constexpr (E4M3) {                      // before S: they are there first
+                    const int ss = (g + j) % kScaleRing;
+                    const uint32_t ph = ((g + j) / kScaleRing) & 1;
+                    if (!poll(&bars->sck_full[ss], ph, p.wait_ns, abort_flag) ||
+                        !poll(&bars->scv_full[ss], ph, p.wait_ns, abort_flag)) {
+                        alive = false;
+                        break;
+                    }
+                }
                 if (!poll(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns, abort_flag)) { alive = false; break; }
                 tc_fence_after();
                 if (j == s.ntiles - 1) {                   // Q is read no more: the next segment's may come
@@ -1069,42 +1090,48 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     } else {
                         const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) +
                                            ((g + j) % kScaleRing) * 2 * kBN;
-                        const uint32_t sph = ((g + j) / kScaleRing) & 1;
-                        if (!poll(&bars->sck_full[(g + j) % kScaleRing], sph, p.wait_ns, abort_flag) ||
-                            !poll(&bars->scv_full[(g + j) % kScaleRing], sph, p.wait_ns, abort_flag)) {
-                            alive = false;
-                            break;
-                        }
                         // P = 2^(s ks - m), P vs leaves as bf16 (its one rounding); the sum is over P.
                         // Masked columns are replaced after the products: a scale that the row does not
                         // see may hold anything.
                         auto columns = [&](auto masked, float m, float& sum) {
                             float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
 #pragma unroll
-                            for (int c = 0; c < kBN / 4; ++c) {
-                                const float4 ks = reinterpret_cast<const float4*>(scl)[c];
-                                const float4 vs = reinterpret_cast<const float4*>(scl + kBN)[c];
-                                const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
-                                float vv[4] = {vs.x, vs.y, vs.z, vs.w};
-                                float x[4];
-                                fma_pairs(x[0], x[1], __uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]), kk[0], kk[1], -m);
-                                fma_pairs(x[2], x[3], __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]), kk[2], kk[3],
-                                          -m);
+                            for (int b = 0; b < kBN; b += 16) {    // 16 columns step by step: their chains overlap
+                                float x[16], y[16];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if constexpr (decltype(masked)::value) {
-                                        const bool seen = (mw[c >> 3] >> ((4 * c + e) & 31)) & 1u;
-                                        x[e] = seen ? x[e] : -INFINITY;
-                                        vv[e] = seen ? vv[e] : 0.f;
-                                    }
-                                    x[e] = ex2(x[e]);
+                                for (int c = 0; c < 4; ++c) {
+                                    const float4 ks = reinterpret_cast<const float4*>(scl + b)[c];
+                                    y[4 * c] = ks.x; y[4 * c + 1] = ks.y; y[4 * c + 2] = ks.z; y[4 * c + 3] = ks.w;
                                 }
-                                add_f32x2(a0, a1, x[0], x[1]);
-                                add_f32x2(a2, a3, x[2], x[3]);
-                                mul_pairs(x[0], x[1], vv[0], vv[1]);
-                                mul_pairs(x[2], x[3], vv[2], vv[3]);
-                                v[2 * c] = pack_bf16x2(x[0], x[1]);
-                                v[2 * c + 1] = pack_bf16x2(x[2], x[3]);
+#pragma unroll
+                                for (int c = 0; c < 16; c += 2)
+                                    fma_pairs(x[c], x[c + 1], __uint_as_float(v[b + c]), __uint_as_float(v[b + c + 1]), y[c],
+                                              y[c + 1], -m);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) {
+                                    const float4 vs = reinterpret_cast<const float4*>(scl + kBN + b)[c];
+                                    y[4 * c] = vs.x; y[4 * c + 1] = vs.y; y[4 * c + 2] = vs.z; y[4 * c + 3] = vs.w;
+                                }
+                                if constexpr (decltype(masked)::value) {
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) {
+                                        const bool seen = (mw[b >> 5] >> ((b + c) & 31)) & 1u;
+                                        x[c] = seen ? x[c] : -INFINITY;
+                                        y[c] = seen ? y[c] : 0.f;
+                                    }
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) x[c] = ex2(x[c]);
+#pragma unroll
+                                for (int c = 0; c < 16; c += 4) {
+                                    add_f32x2(a0, a1, x[c], x[c + 1]);
+                                    add_f32x2(a2, a3, x[c + 2], x[c + 3]);
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; c += 2) {
+                                    mul_pairs(x[c], x[c + 1], y[c], y[c + 1]);
+                                    v[(b + c) / 2] = pack_bf16x2(x[c], x[c + 1]);
+                                }
                             }
                             sum = (a0 + a1) + (a2 + a3);
                         };

@@ -381,6 +381,9 @@ int tree_rerank_pool(const int32_t *node_parent, const int32_t *node_token, cons
  * Offsets out of order or range set BAD_LENGTH: a sequence with such offsets has no rows,
  * and those of others may be left out too; nothing outside the call's buffers is touched.
  *
+ * A workspace serves one call at a time: calls that may run at the same time (on two
+ * streams, or as two graphs in flight) need one each.
+ *
  * 8-bit pools (TREESPEC_DTYPE_E4M3): k_pages / v_pages [P][16][Hkv][D] hold e4m3 codes
  * (1 byte each), k_scales / v_scales [P][Hkv][16] a float32 for each token and kv head;
  * an element stands for code * scale.  A page's 16 scales of one kv head are 64
