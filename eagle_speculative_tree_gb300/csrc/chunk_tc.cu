@@ -644,6 +644,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     Bars* bars = reinterpret_cast<Bars*>(sm + C::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(sm + C::kOffMisc + 4);
+    int* longest = reinterpret_cast<int*>(sm + C::kOffMisc + 8);       // KV tiles of the longest unit
     End* ends = reinterpret_cast<End*>(sm + C::kOffEnds);
     SeqRows* first_rows = reinterpret_cast<SeqRows*>(ends + 2);
     long long* tiles_s = reinterpret_cast<long long*>(sm + C::kOffTiles);
@@ -690,6 +691,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             }
         }
         *abort_flag = 0;
+        *longest = 0;
         fence_mbar_init();
     }
     grid_dep_wait();                                       // trees: the prologue's results
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         const int per = (p.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
         long long nt = 0;
-        int nu = 0;
+        int nu = 0, top = 0;
         bool bad = false;
         for (int b = b0; b < b1; ++b) {
             const SeqUnits u = seq_units(p, seq_rows(p, b));
@@ -709,6 +711,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             units_s[b] = nu;
             nt += u.np == 1 ? u.tiles(0) : u.tiles_before(u.np);
             nu += u.np;
+            if (u.np) top = max(top, u.tiles(u.np - 1));
         }
         if (bad && blockIdx.x == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
         long long it = nt;
@@ -727,6 +730,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             wt[2 * warp + 1] = iu;
         }
         __syncthreads();
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(longest, top);
         long long bt = it - nt;
         int bu = iu - nu;
         for (int w = 0; w < warp; ++w) {
@@ -752,12 +757,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         // A range that holds pieces of two units pays the fixed cost twice, so where there is less
         // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
         // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
-        // 42 and 29)
+        // 42 and 29), unless one long unit among short ones would then run far longer than its
+        // share of all tiles
         const long long units = (long long)p.Hkv * units_s[p.B];
         cut.k = kKappa;
         cut.total = p.Hkv * tiles_s[p.B] + kKappa * units;
-        cut.m = cut.total < (long long)(kKappa + 2) * gridDim.x && units <= gridDim.x && units > 0
-                    ? int(gridDim.x) / int(units) : 0;
+        cut.m = 0;
+        if (cut.total < (long long)(kKappa + 2) * gridDim.x && units <= gridDim.x && units > 0) {
+            const int m = int(gridDim.x) / int(units);
+            if (*longest / unit_pieces(*longest, m) <= int(cut.total) / int(gridDim.x) + 2 * kKappa) cut.m = m;
+        }
         cut.parts = cut.m ? cut.m * int(units) : int(min((long long)gridDim.x, max(1ll, cut.total / (kKappa + 1))));
     }
     // rows without a token (a padded tree's, and those of an invalid sequence) are zeros

@@ -268,6 +268,46 @@ def test_chunk_attention_long_context_few_rows(ts, cuda_device, dtype, e4m3, pre
     check_chunk(ts, make(cuda_device, prefix, new, 8, 1, 128, dtype, e4m3, seed=15), ts.KERNEL_AUTO)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("prefix,new,hq,hkv", [
+    ([20000], [1], 8, 1),                                      # one unit in more than 32 pieces
+    ([20000] + [5] * 40, [1] * 41, 4, 1),                      # a long unit among short ones
+    ([9000, 0, 700, 3], [1, 400, 3, 0], 16, 2),                # decoding beside a prompt
+    ([3000] * 40, [2] * 40, 8, 8),                             # more units than SMs, each cut somewhere
+])
+def test_chunk_attention_cuts(ts, cuda_device, prefix, new, hq, hkv, e4m3):
+    p = make(cuda_device, prefix, new, hq, hkv, 128, "bf16", e4m3, seed=17)
+    check_chunk(ts, p, ts.KERNEL_TC_STREAM)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_chunk_attention_at_the_batch_limit(ts, cuda_device, e4m3):
+    """1024 sequences run on the tensor cores, 1025 on CUDA cores; the explicit kernel is refused."""
+    rng = np.random.default_rng(23)
+    for B in (1024, 1025):
+        prefix, new = rng.integers(0, 40, B).tolist(), rng.integers(0, 3, B).tolist()
+        p = make(cuda_device, prefix, new, 4, 2, 64, "bf16", e4m3, seed=B)
+        check_chunk(ts, p, ts.KERNEL_AUTO)
+    with pytest.raises(ValueError):
+        attend(ts, p, ts.KERNEL_TC_STREAM)
+    p.q = p.q.float()
+    if e4m3:
+        with pytest.raises(ValueError):                        # float32 queries run on CUDA cores only
+            attend(ts, p, ts.KERNEL_TC_STREAM)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(ts, cuda_device, e4m3):
+    p = make(cuda_device, [2000, 300], [64, 70], 16, 2, 128, "bf16", e4m3, seed=19)
+    ts.set_wait_limit_ns(1)
+    try:
+        _, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+    finally:
+        ts.set_wait_limit_ns(0)
+    assert st & 16
+    check_chunk(ts, p, ts.KERNEL_TC_STREAM)
+
+
 @pytest.mark.parametrize("dtype,e4m3", KINDS, ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_non_finite_values_reach_only_the_rows_that_see_them(ts, cuda_device, dtype, e4m3, bad):
