@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) chunk_append_kernel(const AppendPara
             const int o0 = p.offsets[b], o1 = p.offsets[b + 1], S = p.prefix_lens[b];
             if (o0 >= 0 && o0 <= t && t < o1 && o1 <= p.T) {
                 const long long at = (long long)S + (t - o0);
-                const int pos = p.positions ? p.positions[t] : int(at);
+                const int pos = p.positions ? p.positions[t] : 0;
                 if (pos >= 0) {
                     if (S < 0 || at >= (long long)p.max_pages * kPage) {
                         if (blockIdx.y == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) chunk_append_kernel(const AppendPara
                             if (blockIdx.y == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
                         } else {
                             r.slot = (long long)page * kPage + (at & 15);
-                            r.pos = pos;
+                            r.pos = p.positions ? pos : int(at);   // at lies in the page table: below 2^30
                         }
                     }
                 }

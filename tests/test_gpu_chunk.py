@@ -195,6 +195,8 @@ def test_append_refuses_bad_pages_and_lengths_row_by_row(ts, cuda_device, tokens
     p.prefix_lens[1] = table.shape[1] * 16 - 1                 # one row fits, the others run past the table
     table[1, -1] = table[1, 0]
     assert check_append(ts, p, q, k, v, qw, kw, f, None, 0) == BAD_LENGTH
+    p.prefix_lens[1] = (1 << 31) - 1                           # positions past 32 bits
+    assert check_append(ts, p, q, k, v, qw, kw, f, None, 0) == BAD_LENGTH
     p.prefix_lens[1] = 3
     p.chunk_offsets[2] = -7                                    # sequences 1 and 2 have no rows
     assert check_append(ts, p, q, k, v, qw, kw, f, None, 0) == BAD_LENGTH
