@@ -496,8 +496,8 @@ struct ChunkPlan {
 
 // rows: query rows per kv head of the whole batch.  The lengths are on the device, so the
 // plan goes by the page table's width and the mean rows of a sequence.
-ChunkPlan chunk_plan(int kernel, int dtype, long long batch, long long rows, int Hkv, int max_pages, int pool_pages,
-                     int sms) {
+ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long long rows, int Hkv, int D,
+                     int max_pages, int pool_pages, int sms) {
     ChunkPlan c{};
     if (kernel != TREESPEC_KERNEL_SIMT && chunk_tc_supported(dtype, int(batch), (long long)pool_pages * kPage)) {
         c.kernel = TREESPEC_KERNEL_TC_STREAM;
@@ -510,12 +510,15 @@ ChunkPlan chunk_plan(int kernel, int dtype, long long batch, long long rows, int
     // splits of at least 128 tokens would leave SMs without a CTA: a block of 64 rows reads
     // K and V an eighth as often as one of 8, but a small problem is bound by one CTA's run
     // (5 sequences of up to 130 tokens x 4 heads over up to 830 tokens of 64, float32: 59 us
-    // with blocks of 64 rows in splits of 256 tokens, 29 us with this rule).
+    // with blocks of 64 rows in splits of 256 tokens, 27 us with this rule).
     const long long mean = (rows + batch - 1) / batch;
     const long long tokens = (long long)max_pages * kPage;
     long long splits = 1;
-    for (int rb = 64; rb >= 8; rb /= 2) {
-        if (rb > 8 && mean <= rb / 2) continue;
+    // No block smaller than leaves its CTA 8 warps: they share the loads even where only some
+    // hold rows.
+    const int least = chunk_simt_min_rows(D, kv_dtype == TREESPEC_DTYPE_E4M3 ? 1 : kv_dtype == TREESPEC_DTYPE_BF16 ? 2 : 4);
+    for (int rb = 64; rb >= least; rb /= 2) {
+        if (rb > least && mean <= rb / 2) continue;
         c.rows_block = rb;
         const long long units = ((rows + rb - 1) / rb) * Hkv;
         // two CTAs per SM where the row blocks alone do not give them
@@ -554,8 +557,8 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
 }
 
 ChunkPlan plan_of(const treespec_chunk_shape& s) {
-    return chunk_plan(s.kernel, s.dtype, s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads),
-                      s.num_kv_heads, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
+    return chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads),
+                      s.num_kv_heads, s.head_dim, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
 }
 ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c) {
     return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch);
@@ -578,8 +581,9 @@ int check_e4m3_verify_shape(const treespec_attn_shape* s) {
     return TREESPEC_OK;
 }
 ChunkPlan plan_of(const treespec_attn_shape& s) {
-    return chunk_plan(s.kernel, s.dtype, s.batch, (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads),
-                      s.num_kv_heads, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
+    return chunk_plan(s.kernel, s.dtype, TREESPEC_DTYPE_E4M3, s.batch,
+                      (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
+                      s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
 }
 ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c) {
     const long long rows = (long long)s.batch * s.num_nodes;

@@ -144,6 +144,8 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
     float* Pt = reinterpret_cast<float*>(kv + sh.kv_bytes);
     float* Sc = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(Pt) + sh.pt_bytes);   // [stage][K, V][TT]
     __shared__ uint64_t anc_s[kRows][kAncWords];
+    __shared__ unsigned long long at_s[kRows];           // element of q and out where a row begins
+    __shared__ float fin_s[4][kRows];                    // weights of the token slices of a row in the result
     __shared__ int seq_s;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,6 +183,8 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
         const int row = r0 + lr;
         return (size_t(split) * p.T + sq.row0 + row / p.G) * p.Hq + h * p.G + row % p.G;
     };
+    for (int lr = tid; lr < rows; lr += nthr) at_s[lr] = elem(lr);
+    __syncthreads();
     // last logical token any of the rows may see, and this split's share
     const int last_i = min((r0 + rows - 1) / p.G, sq.live - 1);
     const int L = S < 0 ? 0 : p.offsets ? S + last_i + 1 : S + sq.live;
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
     const int t1 = p.num_splits == 1 ? L : int(min((long long)L, (long long)t0 + p.split_tokens));
     if (t0 >= t1) {                                      // nothing here: zeros, or an empty partial
         if (p.num_splits == 1) {
-            for (int e = tid; e < rows * D; e += nthr) store_out<T>(p.out, elem(e / D) + e % D, 0.f);
+            for (int e = tid; e < rows * D; e += nthr) store_out<T>(p.out, at_s[e / D] + e % D, 0.f);
         } else {
             for (int lr = tid; lr < rows; lr += nthr) {
                 p.part_ml[part(lr) * 2] = -INFINITY;
@@ -198,9 +202,11 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
         return;
     }
 
+    const int live_rows = min(rows, sq.live * p.G - r0);  // rows of a padded tree's other slots lie behind them
+#pragma unroll 4
     for (int e = tid; e < RW * 8 * D; e += nthr) {
         const int lr = e / D;
-        Qs[e] = lr < rows && (r0 + lr) / p.G < sq.live ? load_q<T>(p.q, elem(lr) + e % D) * p.scale_log2 : 0.f;
+        Qs[e] = lr < live_rows ? load_q<T>(p.q, at_s[lr] + e % D) * p.scale_log2 : 0.f;
     }
     if (!p.offsets) {
         for (int e = tid; e < rows * kAncWords; e += nthr)
@@ -213,14 +219,18 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
         const int base = t0 + tile * TT;
         unsigned char* Kd = kv + size_t(stage) * 2 * TT * C::ROWB;
         unsigned char* Vd = Kd + size_t(TT) * C::ROWB;
-        for (int e = tid; e < TT * C::VPR; e += nthr) {
+        // the tile's page ids, one load per warp: lane l has that of tokens base + 16 l
+        const int at = base + kPage * lane;
+        const int pages = lane < TT / kPage && at < t1 ? __ldg(ptab + at / kPage) : -1;
+#pragma unroll 2
+        for (int e = tid; e < TT * C::VPR; e += nthr) {  // a warp takes part in a round as a whole
             const int tt = e / C::VPR, vi = e % C::VPR;
             const int pos = base + tt;
+            const int page = __shfl_sync(0xffffffffu, pages, tt / kPage);
             const unsigned char* ks = static_cast<const unsigned char*>(p.k);
             const unsigned char* vs = static_cast<const unsigned char*>(p.v);
             int bytes = 0;
             if (pos < t1) {
-                const int page = ptab[pos / kPage];
                 if (page >= 0 && page < p.num_pool_pages) {
                     const size_t off = ((size_t(page) * kPage + pos % kPage) * p.Hkv + h) * (size_t(D) * C::EB) +
                                        size_t(vi) * 16;
@@ -373,28 +383,39 @@ __global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
         }
     }
     __syncthreads();
-    for (int e = tid; e < rows * D; e += nthr) {
-        const int lr = e / D, d = e % D, rwi = lr / 8, r = lr % 8;
-        float mm = -INFINITY;
+    // a row's state over the token slices, and what each slice's accumulators weigh in it
+    for (int lr = tid; lr < rows; lr += nthr) {
+        const int rwi = lr / 8, r = lr % 8;
+        float mm = -INFINITY, lsum = 0.f;
         for (int t = 0; t < TS; ++t) mm = fmaxf(mm, scr[size_t((t * RW + rwi) * 8 + r) * (D + 2) + D]);
-        float lsum = 0.f, a = 0.f;
         for (int t = 0; t < TS; ++t) {
             const float* src = scr + size_t((t * RW + rwi) * 8 + r) * (D + 2);
             // a slice whose scores are all NaN has m = -inf and l = NaN: kept, not skipped
-            if (src[D] == -INFINITY && src[D + 1] == 0.f) continue;
-            const float f = src[D] == -INFINITY ? 1.f : exp2f(src[D] - mm);
-            lsum = fmaf(src[D + 1], f, lsum);
-            a = fmaf(src[d], f, a);
+            const bool none = src[D] == -INFINITY && src[D + 1] == 0.f;
+            const float f = none ? 0.f : src[D] == -INFINITY ? 1.f : exp2f(src[D] - mm);
+            if (!none) lsum = fmaf(src[D + 1], f, lsum);
+            fin_s[t][lr] = f;
         }
         if (p.num_splits == 1) {
-            store_out<T>(p.out, elem(lr) + d, (r0 + lr) / p.G < sq.live ? a / lsum : 0.f);
+            const float inv = 1.f / lsum;
+            for (int t = 0; t < TS; ++t) fin_s[t][lr] *= inv;
         } else {
-            p.part_acc[part(lr) * D + d] = a;
-            if (d == 0) {
-                p.part_ml[part(lr) * 2] = mm;
-                p.part_ml[part(lr) * 2 + 1] = lsum;
-            }
+            p.part_ml[part(lr) * 2] = mm;
+            p.part_ml[part(lr) * 2 + 1] = lsum;
         }
+        at_s[lr] = p.num_splits == 1 ? at_s[lr] : part(lr) * D;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int e = tid; e < rows * D; e += nthr) {
+        const int lr = e / D, d = e % D;
+        const float* src = scr + size_t(lr) * (D + 2) + d;   // slice t of the row: RW * 8 rows further each
+        float a = 0.f;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            if (t < TS && fin_s[t][lr] != 0.f) a = fmaf(src[size_t(t) * RW * 8 * (D + 2)], fin_s[t][lr], a);
+        if (p.num_splits == 1) store_out<T>(p.out, at_s[lr] + d, lr < live_rows ? a : 0.f);
+        else p.part_acc[at_s[lr] + d] = a;
     }
 }
 
@@ -462,6 +483,11 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int chunk_simt_min_rows(int D, int elem) {
+    const int ts = 160 * 1024 / (4 * 32 * (D * elem + 16));
+    return 64 / (ts >= 4 ? 4 : ts >= 2 ? 2 : 1);
+}
 
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s) {
     const bool d64 = p.D == 64;

@@ -243,6 +243,8 @@ struct ChunkParams {
     uint64_t wait_ns;
 };
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
+// the smallest row block whose CTA still has 8 warps, `elem` bytes per K/V element
+int chunk_simt_min_rows(int D, int elem);
 cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s);
 bool chunk_tc_supported(int dtype, int batch, long long pool_tokens);
 cudaError_t launch_chunk_merge(const ChunkParams& p, int dtype, cudaStream_t s);
