@@ -460,7 +460,8 @@ int tree_chunk_append(const void *q, int64_t q_stride, const void *k, int64_t k_
                       const treespec_chunk_shape *shape, const treespec_append_options *options,
                       void *workspace, size_t workspace_bytes, treespec_stream_t stream);
 
-/* Workspace bytes tree_chunk_attn needs for `shape` (0 if the shape is invalid). */
+/* Workspace bytes tree_chunk_attn needs for `shape` (0 if the shape is invalid): about 40 MB
+ * in the tensor-core form at head dim 128 on 152 SMs, whatever the sizes. */
 size_t treespec_chunk_attn_workspace_bytes(const treespec_chunk_shape *shape);
 
 /*
