@@ -49,7 +49,10 @@ constexpr int kNQ = 2;               // query tiles
 constexpr int kBN = 64;              // tokens per KV tile
 constexpr int kKappa = 7;            // a unit's fixed cost, in tiles
 constexpr int kRaw = 5;              // e4m3: stages of the rings of codes
-constexpr int kMinTiles = 4;         // no piece of a unit with CTAs of its own is shorter than this
+// No piece of a unit with CTAs of its own is shorter than this.  Joining costs by the row, so
+// units of many rows are cut into longer pieces (8 nodes x 4 heads over 2048 e4m3 tokens: 28.7
+// us in pieces of 4 tiles, 30.9 of 9; 3 prompts of up to 816 tokens, 4 heads: 33 and 25).
+constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
 constexpr int kWholeTiles = 4;       // units up to this long are not cut
 constexpr int kScaleRing = 4;        // e4m3: tiles of scales
 constexpr uint32_t kTmemCols = 512;
@@ -179,8 +182,10 @@ struct Cut {
 struct End {                          // tile j of unit (b, h, pr)
     int b, h, pr, j;
 };
-// Pieces of a unit of n tiles that m CTAs share: none shorter than kMinTiles.
-__device__ __forceinline__ int unit_pieces(int n, int m) { return min(m, max(1, n / kMinTiles)); }
+// Pieces of a unit of n tiles and that many rows that m CTAs share.
+__device__ __forceinline__ int unit_pieces(int n, int rows, int m) {
+    return min(m, max(1, n / (rows > 64 ? kMinTilesManyRows : kMinTiles)));
+}
 
 // Unit u of the batch, in the order of the cut.
 __device__ __forceinline__ End unit_at(const ChunkParams& p, const Cut& q, int u) {
@@ -829,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         cut.m = 0;
         if (cut.total < (long long)(kKappa + 2) * gridDim.x && units <= gridDim.x && units > 0) {
             const int m = int(gridDim.x) / int(units);
-            if (*longest / unit_pieces(*longest, m) <= int(cut.total) / int(gridDim.x) + 2 * kKappa) cut.m = m;
+            if (*longest / unit_pieces(*longest, 1, m) <= int(cut.total) / int(gridDim.x) + 2 * kKappa) cut.m = m;
         }
         cut.parts = cut.m ? cut.m * int(units) : int(min((long long)gridDim.x, max(1ll, cut.total / (kKappa + 1))));
     }
@@ -852,8 +857,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         End e;
         if (cut.m) {
             e = unit_at(p, cut, me / cut.m);
-            const int n = seq_units(p, seq_rows(p, e.b)).tiles(e.pr);
-            const int pieces = unit_pieces(n, cut.m), k = me % cut.m + warp;
+            const SeqUnits u = seq_units(p, seq_rows(p, e.b));
+            const int n = u.tiles(e.pr);
+            const int pieces = unit_pieces(n, min(u.tpu, u.live - e.pr * u.tpu) * p.G, cut.m), k = me % cut.m + warp;
             e.j = k > pieces ? n : int((long long)n * k / pieces);   // beyond the last piece: nothing
         } else if (c >= cut.parts) {
             e = End{p.B, 0, 0, 0};
@@ -1340,7 +1346,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 int c0, pieces;
                 if (cut.m) {
                     c0 = me / cut.m * cut.m;
-                    pieces = unit_pieces(s.n, cut.m);
+                    pieces = unit_pieces(s.n, s.tokens * p.G, cut.m);
                 } else {
                     const SeqUnits u = seq_units(p, seq_rows(p, s.b));
                     const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
