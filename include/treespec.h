@@ -451,8 +451,9 @@ size_t treespec_append_workspace_bytes(void);
  *      8-bit.
  * A row with a negative position is padding: nothing of it is read or written.  A row
  * whose slot lies outside its page table (BAD_LENGTH) or whose page lies outside the pool
- * (BAD_PAGE) is left out in the same way.  Two sequences whose new tokens share a slot
- * are the caller's mistake; one of them is kept.
+ * (BAD_PAGE) is left out in the same way.  New tokens of two sequences must not share a
+ * slot: what it holds afterwards is not defined.  (Pages that hold cached tokens may be
+ * shared by any number of sequences, here and in the attention calls.)
  */
 int tree_chunk_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                       int64_t v_stride, void *q_out, void *k_pages, void *v_pages, float *k_scales, float *v_scales,
