@@ -472,7 +472,8 @@ size_t treespec_chunk_attn_workspace_bytes(const treespec_chunk_shape *shape);
  * (tree_chunk_append).  For row t, the i-th of sequence b, and query head hq:
  *     out[t][hq] = softmax_u( q[t][hq] . K[u][hq / G] / sqrt(D) ) applied to V[u][hq / G],
  *                  over the logical tokens u = 0 .. prefix_lens[b] + i.
- *   q, out [T][Hq][D] contiguous, in shape->dtype; pools and scales as above.
+ *   q, out [T][Hq][D] contiguous, in shape->dtype; out overlaps nothing else.  Pools and
+ *   scales as above.
  * Tokens that a row may not see, and slots behind a sequence's last token, do not reach
  * the row's result, whatever they hold (NaN and infinities included).
  * The rows of a sequence with prefix_len < 0 or prefix_len + n_b > max_pages * 16 are
