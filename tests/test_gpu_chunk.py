@@ -718,3 +718,53 @@ def test_prompt_tree_accept_commit_and_decode(ts, cuda_device, e4m3):
     offsets = ints(np.arange(B + 1), cuda_device)
     q = append(cache, project(B), new, offsets)
     check(cache, q, new, offsets)
+
+
+# ------------------------------------------------------------------------------ uses that meet in one program
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_two_calls_at_once_with_a_workspace_each(ts, cuda_device, e4m3):
+    p = make(cuda_device, [3000, 10, 900], [1, 200, 64], 16, 2, 128, "bf16", e4m3, seed=91)
+    prob = ts.chunk_problem(p.q, p.k_pages, p.page_table, p.chunk_offsets)
+    want, _ = attend(ts, p, ts.KERNEL_AUTO)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.empty(ts.chunk_attn_workspace_bytes(prob), dtype=torch.uint8, device=cuda_device) for _ in streams]
+    outs = [[torch.empty_like(p.q) for _ in range(8)] for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for st, ws, out in zip(streams, spaces, outs):
+            ts.tree_chunk_attn(p.q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, p.chunk_offsets, out[i], workspace=ws,
+                               stream=st, **p.scales())
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for out in outs for o in out)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS, ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
+def test_sequences_that_share_the_pages_of_a_prefix(ts, cuda_device, dtype, e4m3):
+    p = make(cuda_device, [64, 70, 64], [20, 5, 1], 8, 2, 128, dtype, e4m3, seed=93)
+    p.page_table[1:, :4] = p.page_table[0, :4]                 # 64 tokens in four whole pages
+    check_chunk(ts, p, ts.KERNEL_AUTO)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_zero_and_negative_scales(ts, cuda_device, dtype):
+    """Scales that a program made itself: any finite float32 multiplies its codes."""
+    p = make(cuda_device, [150, 3], [70, 2], 8, 2, 128, dtype, True, seed=95)
+    gen = torch.Generator(device=cuda_device)
+    gen.manual_seed(1)
+    for s in (p.k_scales, p.v_scales):
+        s *= torch.randint(-1, 2, s.shape, generator=gen, device=cuda_device)
+    check_chunk(ts, p, ts.KERNEL_AUTO)
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS, ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
+def test_a_query_that_is_not_finite_spoils_its_own_row_only(ts, cuda_device, dtype, e4m3):
+    p = make(cuda_device, [90], [40], 8, 2, 128, dtype, e4m3, seed=97)
+    clean, _ = attend(ts, p, ts.KERNEL_AUTO)
+    p.q[7, 3, 5], p.q[20, 6, 100] = float("nan"), float("inf")
+    got, st = attend(ts, p, ts.KERNEL_AUTO)
+    assert st == 0 and torch.isnan(got[7, 3]).all() and torch.isnan(got[20, 6]).all()
+    keep = torch.ones(40, 8, dtype=torch.bool, device=cuda_device)
+    keep[7, 3] = keep[20, 6] = False
+    tol = (2 * U_BF16 if dtype == "bf16" else 1e-5) * clean.abs().amax().item()
+    assert (got[keep].double() - clean[keep].double()).abs().max().item() <= tol
