@@ -1135,7 +1135,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                     tcparts::tile_mask<kBN>(mw, base, s.S, s.t1, si.a0, si.a1, ro.ok);
                 }
                 const bool full = __all_sync(0xffffffffu, (mw[0] & mw[1]) == 0xffffffffu || !ro.ok);
-                if constexpr (E4M3) {                      // before S: they are there first
+                if (!poll(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns, abort_flag)) { alive = false; break; }
+                tc_fence_after();
+                if constexpr (E4M3) {
+                    // Only behind S: a parity tells a slot's use from the one before it, not from
+                    // older ones, and a tile that sat a segment out has passed over many.  S of tile
+                    // g comes after K of g and V of g - 2 were converted, so the slot's use before
+                    // this one, tile g - 4, is complete by now
                     const int ss = (g + j) % kScaleRing;
                     const uint32_t ph = ((g + j) / kScaleRing) & 1;
                     if (!poll(&bars->sck_full[ss], ph, p.wait_ns, abort_flag) ||
@@ -1144,8 +1150,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                         break;
                     }
                 }
-                if (!poll(&bars->s_full[t][bf], (aj >> 1) & 1, p.wait_ns, abort_flag)) { alive = false; break; }
-                tc_fence_after();
                 if (j == s.ntiles - 1) {                   // Q is read no more: the next segment's may come
                     more = next_seg(nxt, skip2);
                     if (more) issue_q(nxt);

@@ -1,6 +1,7 @@
 """Problems and error bounds of the chunk and 8-bit cache tests."""
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass
 
 import numpy as np
@@ -104,3 +105,88 @@ def check_attention(got, ref, spread, reach, tokens, dim, dtype, tensor_cores):
     err = np.abs(g - ref)
     bad = live & ~(err <= bound)
     assert not bad.any(), f"{bad.sum()} of {live.sum()} elements out of bounds, worst {np.nanmax(err / bound):.3g} times"
+
+
+def make_8bit(device, prefix, new, hq, hkv, dim, seed=0, rows=None, spread=1.0):
+    """As make(), for larger problems over 8-bit pools, drawn on the device: codes of normal
+    values, scales 0.01 x 10^u with u even in [-spread, spread] for each token and kv head, so that a
+    scale of another token is far from the right one."""
+    gen = torch.Generator(device=device)
+    gen.manual_seed(seed)
+    rows = rows or new
+    need = [(p + n + 15) // 16 for p, n in zip(prefix, rows)]
+    pool = sum(need) + 3
+    order = torch.randperm(pool, generator=gen, device=device).to(torch.int32)
+    table = torch.full((len(prefix), max(need)), pool + 5, dtype=torch.int32, device=device)
+    used = torch.zeros((pool, 16), dtype=torch.bool, device=device)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+        t = torch.arange(prefix[b] + new[b], device=device)
+        used[table[b].long()[t // 16], t % 16] = True
+    pools, scales = [], []
+    for _ in range(2):
+        x = torch.randn((pool, 16, hkv, dim), generator=gen, device=device) * 100
+        codes = x.clamp(-448, 448).to(torch.float8_e4m3fn)
+        codes.view(torch.uint8)[~used] = 0x7f
+        u = 2 * torch.rand((pool, hkv, 16), generator=gen, device=device) - 1
+        sc = 0.01 * 10.0 ** (spread * u)
+        sc.transpose(1, 2)[~used] = math.nan
+        pools.append(codes)
+        scales.append(sc)
+    scales[0] *= 0.1                                           # scores of a few units
+    q = torch.randn((sum(rows), hq, dim), generator=gen, device=device).to(torch.bfloat16)
+    ints = lambda a: torch.tensor(a, dtype=torch.int32, device=device)  # noqa: E731
+    offsets = np.concatenate(([0], np.cumsum(rows))).tolist()
+    return Problem(list(prefix), list(new), q, pools[0], pools[1], scales[0], scales[1], table, ints(prefix), ints(offsets))
+
+
+def attend64(p, q, b, seen):
+    """Sequence b in 64 bits, all of its rows at once: q [n][Hq][D], seen [n][L] -> (out, spread, reach)
+    of oracle.chunk.attend as tensors."""
+    n, H, D = q.shape
+    t = torch.arange(seen.shape[1], device=q.device)
+    page, at = p.page_table[b].long()[t // 16], t % 16
+    kv = []
+    for pages, scales in ((p.k_pages, p.k_scales), (p.v_pages, p.v_scales)):
+        x = pages.view(torch.uint8)[page, at].view(pages.dtype) if pages.element_size() == 1 else pages[page, at]
+        x = x.double()
+        kv.append(x if scales is None else x * scales.transpose(1, 2)[page, at].double()[..., None])
+    out, spread = (torch.empty((n, H, D), dtype=torch.float64, device=q.device) for _ in "os")
+    reach = torch.empty((n, H), dtype=torch.float64, device=q.device)
+    G = H // kv[0].shape[1]
+    for h in range(H):
+        k, v, x = kv[0][:, h // G], kv[1][:, h // G], q[:, h].double()
+        s = (x @ k.T / math.sqrt(D)).masked_fill(~seen, -math.inf)
+        w = torch.softmax(s, -1)
+        out[:, h], spread[:, h] = w @ v, w @ v.abs()
+        reach[:, h] = (x.abs() @ k.abs().T / math.sqrt(D)).masked_fill(~seen, 0).amax(-1)
+    return out, spread, reach
+
+
+def causal64(p):
+    """(out, spread, reach) of every packed row, as numpy arrays."""
+    parts = []
+    offsets = p.chunk_offsets.tolist()
+    for b, (S, n) in enumerate(zip(p.prefix, p.new)):
+        t = torch.arange(S + n, device=p.q.device)
+        i = torch.arange(n, device=p.q.device)
+        parts.append(attend64(p, p.q[offsets[b]:offsets[b] + n], b, t[None] <= S + i[:, None]))
+    return tuple(torch.cat(x).cpu().numpy() for x in zip(*parts))
+
+
+def tree64(p, q, parents):
+    """The same for padded trees q [B][N][Hq][D]; rows of padding slots are zeros."""
+    out, spread, reach = (torch.zeros(s, dtype=torch.float64) for s in (q.shape, q.shape, q.shape[:3]))
+    for b, (S, n) in enumerate(zip(p.prefix, p.new)):
+        seen = torch.zeros((n, S + n), dtype=torch.bool)
+        seen[:, :S] = True
+        for i in range(n):
+            j = i
+            while j >= 0:
+                seen[i, S + j] = True
+                j = int(parents[b, j])
+        for whole, part in zip((out, spread, reach), attend64(p, q[b, :n], b, seen.to(q.device))):
+            whole[b, :n] = part.cpu()
+    return out.numpy(), spread.numpy(), reach.numpy()

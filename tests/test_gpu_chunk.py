@@ -9,7 +9,7 @@ from oracle import attention as oatt
 from oracle import chunk as och
 from oracle import kv_commit as okc
 
-from chunk_util import U_BF16, U_E4M3, U_F32, check_attention, make
+from chunk_util import U_BF16, U_E4M3, U_F32, causal64, check_attention, make, make_8bit, tree64
 
 pytestmark = pytest.mark.gpu
 
@@ -768,3 +768,50 @@ def test_a_query_that_is_not_finite_spoils_its_own_row_only(ts, cuda_device, dty
     keep[7, 3] = keep[20, 6] = False
     tol = (2 * U_BF16 if dtype == "bf16" else 1e-5) * clean.abs().amax().item()
     assert (got[keep].double() - clean[keep].double()).abs().max().item() <= tol
+
+
+# ------------------------------------------------------------------------------ units of one and of two query tiles
+
+MIXED = [
+    # kind, prefix, new, rows of a sequence, hq, hkv, dim.  128 // (hq // hkv) tokens fill a query tile: every case has units
+    # of one tile beside units of two, and more units than SMs, so that a CTA walks several of them
+    ("tree", [1000 + 7 * b for b in range(32)], [40] * 32, 40, 64, 8, 128),
+    ("tree", [1100 - 9 * b for b in range(32)], [20, 50] * 16, 50, 32, 8, 128),
+    ("tree", [700 + 64 * (b % 5) for b in range(24)], [48, 3, 33, 17] * 6, 48, 64, 8, 64),
+    ("chunk", [1500, 900, 2100, 1300], [488, 500, 484, 510], None, 64, 8, 128),
+    ("chunk", [0] * 24, [35 + 11 * b for b in range(24)], None, 32, 8, 128),
+    ("chunk", [900 + 130 * (b % 7) for b in range(48)], [10, 64] * 24, None, 32, 8, 128),
+]
+
+
+@pytest.mark.parametrize("case", MIXED, ids=lambda c: f"{c[0]}-{len(c[1])}x{max(c[2])}-{c[4]}x{c[5]}-d{c[6]}")
+def test_8bit_units_of_one_and_two_query_tiles(ts, cuda_device, case):
+    """The scales of V differ by up to two orders of magnitude from token to token, so a row that
+    is weighed with another tile's scales is far off."""
+    kind, prefix, new, width, hq, hkv, dim = case
+    p = make_8bit(cuda_device, prefix, new, hq, hkv, dim, seed=len(new))
+    table = (p.k_pages, p.v_pages, p.k_scales, p.v_scales, p.page_table, p.prefix_lens)
+    if kind == "tree":
+        rng = np.random.default_rng(len(new))
+        parents = trees.padded([trees.random_recursive(rng, n) for n in new], width)
+        gen = torch.Generator(device=cuda_device)
+        gen.manual_seed(7)
+        q = torch.randn((len(new), width, hq, dim), generator=gen, device=cuda_device).to(torch.bfloat16)
+        ws = torch.empty(ts.attn_e4m3_workspace_bytes(ts.attn_problem(q, p.k_pages, p.page_table, kernel=ts.KERNEL_TC_STREAM)),
+                         dtype=torch.uint8, device=cuda_device)
+        par = ints(parents, cuda_device)
+        call = lambda: ts.tree_attn_verify_e4m3(q, *table, par, kernel=ts.KERNEL_TC_STREAM, workspace=ws)  # noqa: E731
+        ref = tree64(p, q, parents)
+    else:
+        ws = torch.empty(ts.chunk_attn_workspace_bytes(ts.chunk_problem(p.q, p.k_pages, p.page_table, p.chunk_offsets)),
+                         dtype=torch.uint8, device=cuda_device)
+        call = lambda: ts.tree_chunk_attn(p.q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, p.chunk_offsets,  # noqa: E731
+                                          kernel=ts.KERNEL_TC_STREAM, workspace=ws, **p.scales())
+        ref = causal64(p)
+    got = call()
+    assert ts.read_status(ws) == 0
+    check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), dim, "bf16", True)
+    for _ in range(20):
+        again = call()
+        assert torch.equal(again.view(torch.int16), got.view(torch.int16)), "the same call gave other bits"
+    assert ts.read_status(ws) == 0

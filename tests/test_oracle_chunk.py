@@ -111,3 +111,23 @@ def test_empty_and_invalid_sequences():
     q = rng.standard_normal((5, 1, 4))
     out, _, _ = och.chunk_attention(q, kp, vp, np.array([[0], [1], [2]]), [3, -1, 16], [0, 2, 3, 4])
     assert np.isfinite(out[:2]).all() and not out[2:4].any() and np.isnan(out[4]).all()
+
+
+def test_the_batched_reference_of_larger_problems_is_the_definition():
+    """chunk_util.causal64 and tree64, which serve larger GPU cases, against the row-by-row oracle."""
+    import torch
+    from chunk_util import causal64, make, make_8bit, tree64
+    for p in (make("cpu", [20, 3], [5, 18], 4, 2, 16, "f32", True, seed=2), make_8bit("cpu", [9, 0], [3, 7], 4, 1, 8, seed=4)):
+        args = (p.q.double().numpy(), *p.pools64(), p.page_table.numpy(), p.prefix, p.chunk_offsets.tolist())
+        for got, ref in zip(causal64(p), och.chunk_attention(*args)):
+            assert np.allclose(got, ref, rtol=1e-12, atol=1e-12)
+    parents = np.array([[-1, 0, 0, 2, -2], [-1, 0, 1, 1, 0]])
+    p = make_8bit("cpu", [13, 2], [4, 5], 2, 1, 8, seed=5)
+    q = torch.randn(2, 5, 2, 8, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    out, _, _ = tree64(p, q, parents)
+    kp, vp = p.pools64()
+    for b in range(2):
+        n = p.new[b]
+        ref = oatt.tree_attention(q[b:b + 1, :n].double().numpy(), kp, vp, p.page_table[b:b + 1].numpy(),
+                                  np.array(p.prefix[b:b + 1]), parents[b:b + 1, :n].astype(np.int32), 16)
+        assert np.allclose(out[b, :n], ref[0], atol=1e-12) and not out[b, n:].any()
