@@ -1330,7 +1330,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 mbar_arrive(&bars->o_free[t]);
             }
             if (warp_rows) {
-                for (unsigned w = __ballot_sync(0xffffffffu, ro.ok && !(odd == 0.f)); w; w &= w - 1) {
+                const unsigned again = __ballot_sync(0xffffffffu, ro.ok && !(odd == 0.f));
+                if (again) __syncwarp();                   // the lanes' stores above come before those below
+                for (unsigned w = again; w; w &= w - 1) {
                     const int x = __ffs(w) - 1;            // one row at a time, by the whole warp
                     const Row rx = row_of(p, s, t, x * 4 + quarter, D);
                     float o4[4], mx, lx;

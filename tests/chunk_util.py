@@ -144,7 +144,7 @@ def make_8bit(device, prefix, new, hq, hkv, dim, seed=0, rows=None, spread=1.0):
 
 def attend64(p, q, b, seen):
     """Sequence b in 64 bits, all of its rows at once: q [n][Hq][D], seen [n][L] -> (out, spread, reach)
-    of oracle.chunk.attend as tensors."""
+    of oracle.chunk.attend as tensors; NaN where a row sees a NaN or an infinity in V."""
     n, H, D = q.shape
     t = torch.arange(seen.shape[1], device=q.device)
     page, at = p.page_table[b].long()[t // 16], t % 16
@@ -160,7 +160,10 @@ def attend64(p, q, b, seen):
         k, v, x = kv[0][:, h // G], kv[1][:, h // G], q[:, h].double()
         s = (x @ k.T / math.sqrt(D)).masked_fill(~seen, -math.inf)
         w = torch.softmax(s, -1)
-        out[:, h], spread[:, h] = w @ v, w @ v.abs()
+        # a value that is not finite reaches the rows that see it, and no product with a weight of 0 may bring it to others
+        odd = seen.double() @ (~v.isfinite()).double() > 0
+        plain = torch.where(v.isfinite(), v, 0.0)
+        out[:, h], spread[:, h] = (w @ plain).masked_fill(odd, math.nan), w @ plain.abs()
         reach[:, h] = (x.abs() @ k.abs().T / math.sqrt(D)).masked_fill(~seen, 0).amax(-1)
     return out, spread, reach
 

@@ -815,3 +815,36 @@ def test_8bit_units_of_one_and_two_query_tiles(ts, cuda_device, case):
         again = call()
         assert torch.equal(again.view(torch.int16), got.view(torch.int16)), "the same call gave other bits"
     assert ts.read_status(ws) == 0
+
+
+# ------------------------------------------------------------------------------ hidden values that are not finite
+
+def poison(p, tokens, columns):
+    """A NaN in V of kv head h at new token tokens[b][h] of sequence b, in `columns` of the head (8-bit: the code)."""
+    for b, of_head in enumerate(tokens):
+        for h, i in enumerate(of_head):
+            page, at = int(p.page_table[b, (p.prefix[b] + i) // 16]), (p.prefix[b] + i) % 16
+            if p.k_scales is None:
+                p.v_pages[page, at, h, columns] = float("nan")
+            else:
+                p.v_pages.view(torch.uint8)[page, at, h, columns] = 0x7f
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("prefix,new,hq,hkv,dim", [
+    ([300, 40], [96, 64], 16, 2, 128),                         # few units: CTAs of their own, cut into pieces
+    ([70] * 40, [34] * 40, 32, 4, 64),                         # more units than SMs
+])
+def test_all_rows_of_a_tile_beside_a_hidden_nan(ts, cuda_device, prefix, new, hq, hkv, dim, e4m3):
+    """The last new token of every sequence holds a NaN: it shares a tile with every row, and all rows
+    but its own are finite, stored whole and in pieces, in every call."""
+    p = make(cuda_device, prefix, new, hq, hkv, dim, "bf16", e4m3, seed=101)
+    poison(p, [[n - 1] * hkv for n in new], slice(3, 4))
+    ref = causal64(p)
+    assert np.isnan(ref[0]).sum() == len(new) * hq
+    got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+    assert st == 0
+    check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), dim, "bf16", True)
+    for _ in range(20):
+        again, _ = attend(ts, p, ts.KERNEL_TC_STREAM)
+        assert torch.equal(again.view(torch.int16), got.view(torch.int16))
