@@ -30,7 +30,8 @@
 // A value that a row may not see must not reach it.  S is masked by selection, but P V
 // multiplies a masked token's V by zero, and 0 x NaN is NaN.  A row whose O comes out
 // non-finite is therefore recomputed from the visible tokens alone, on CUDA cores: rare and
-// slow, and no cost to the others but a test in the epilogue.
+// slow, and no cost to the others but a test in the epilogue.  It is done behind the CTA's last
+// segment, where no hand-off of the pipeline, whose waits are bounded, depends on its time.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records TREESPEC_STATUS_TIMEOUT, drains
 // its own copies and MMAs, frees its tensor memory and exits.
@@ -185,6 +186,30 @@ struct End {                          // tile j of unit (b, h, pr)
 // Pieces of a unit of n tiles and that many rows that m CTAs share.
 __device__ __forceinline__ int unit_pieces(int n, int rows, int m) {
     return min(m, max(1, n / (rows > 64 ? kMinTilesManyRows : kMinTiles)));
+}
+
+// The cut of a batch: the prefix sums and the KV tiles of its longest unit.
+__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest) {
+    // A range that holds pieces of two units pays the fixed cost twice, so where there is less
+    // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
+    // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
+    // 42 and 29), unless one long unit among short ones would then run far longer than its
+    // share of all tiles
+    Cut cut;
+    const long long n = (long long)p.Hkv * units[p.B];
+    cut.tiles = tiles;
+    cut.units = units;
+    cut.B = p.B;
+    cut.Hkv = p.Hkv;
+    cut.k = kKappa;
+    cut.total = p.Hkv * tiles[p.B] + kKappa * n;
+    cut.m = 0;
+    if (cut.total < (long long)(kKappa + 2) * gridDim.x && n <= gridDim.x && n > 0) {
+        const int m = int(gridDim.x) / int(n);
+        if (longest / unit_pieces(longest, 1, m) <= int(cut.total) / int(gridDim.x) + 2 * kKappa) cut.m = m;
+    }
+    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)gridDim.x, max(1ll, cut.total / (kKappa + 1))));
+    return cut;
 }
 
 // Unit u of the batch, in the order of the cut.
@@ -572,6 +597,84 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
     }
 }
 
+// The last of the warps that hold these rows of a cut unit joins its pieces.
+template <int D>
+__device__ __forceinline__ void join_unit(const ChunkParams& p, const Cut& cut, const Seg& s, int me, int t, int quarter,
+                                          const Row& ro) {
+    int c0, pieces;
+    if (cut.m) {
+        c0 = me / cut.m * cut.m;
+        pieces = unit_pieces(s.n, s.tokens * p.G, cut.m);
+    } else {
+        const SeqUnits u = seq_units(p, seq_rows(p, s.b));
+        const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
+                             u.tiles_before(s.pr) + (long long)cut.k * s.pr + cut.k;
+        c0 = cut.owner(ub);
+        pieces = cut.owner(ub + s.n - 1) - c0 + 1;
+    }
+    __threadfence();
+    __syncwarp();
+    int n = 0;
+    if ((threadIdx.x & 31) == 0) n = atomicAdd(p.counters + c0 * 8 + t * 4 + quarter, 1);
+    n = __shfl_sync(0xffffffffu, n, 0);
+    if (n == pieces - 1) {
+        __threadfence();
+        join_pieces<D>(p, c0, pieces, t, quarter, ro.at, __ballot_sync(0xffffffffu, ro.ok));
+    }
+}
+
+// One warp's rows that came out non-finite, segment by segment of the CTA's range, recomputed and
+// stored behind what the epilogue stored; then the joins that waited for them: those of the
+// range's last (pending & 2) and first (pending & 1) piece.  `sm`: the CTA's shared memory.
+template <int D, bool E4M3>
+__device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char* sm, uint32_t pending) {
+    using C = Cfg<D, E4M3>;
+    constexpr int DS = D / 32;
+    const int lane = threadIdx.x & 31, t = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3, me = blockIdx.x;
+    const Cut cut = cut_of(p, reinterpret_cast<const long long*>(sm + C::kOffTiles),
+                           reinterpret_cast<const int*>(sm + C::kOffUnits),
+                           *reinterpret_cast<const int*>(sm + C::kOffMisc + 8));
+    const End* ends = reinterpret_cast<const End*>(sm + C::kOffEnds);
+    __syncwarp();                                          // the lanes' stores come before what is read and stored here
+    Walk walk;
+    walk.start(p, ends[0], ends[1], *reinterpret_cast<const SeqRows*>(ends + 2));
+    Seg s;
+    while (walk.next(s)) {
+        if (t >= s.nq) continue;
+        const Row ro = row_of(p, s, t, lane * 4 + quarter, D);
+        const unsigned valid = __ballot_sync(0xffffffffu, ro.ok);
+        if (!valid) continue;
+        const bool whole = s.whole(), head = s.j0 == 0;
+        const size_t prow = (size_t(2 * me + (head ? 1 : 0)) * kNQ + t) * kM + quarter * 32;
+        for (unsigned w = valid; w; w &= w - 1) {
+            const int x = __ffs(w) - 1;
+            const size_t at = __shfl_sync(0xffffffffu, (unsigned long long)ro.at, x);
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < DS; ++e) {
+                const int d = lane * DS + e;
+                o[e] = whole ? bf16_to_f32(__ldcg(static_cast<const uint16_t*>(p.out) + at + d))
+                             : __ldcg(p.part_acc + (prow + x) * D + d);
+            }
+            float odd = 0.f;
+#pragma unroll
+            for (int e = 0; e < DS; ++e) odd = fmaf(o[e], 0.f, odd);
+            if (!__any_sync(0xffffffffu, !(odd == 0.f))) continue;
+            const Row rx = row_of(p, s, t, x * 4 + quarter, D);
+            float m, l;
+            slow_row<D, E4M3>(p, s, rx, sight_of(p, s, rx), o, m, l);
+#pragma unroll
+            for (int e = 0; e < DS; ++e) {
+                const int d = lane * DS + e;
+                if (whole) static_cast<uint16_t*>(p.out)[at + d] = f32_to_bf16_rne(o[e] / l);
+                else __stcg(p.part_acc + (prow + x) * D + d, o[e]);
+            }
+            if (!whole && lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + prow + x, make_float2(m, l));
+        }
+        if (!whole && (pending & (head ? 2u : 1u))) join_unit<D>(p, cut, s, me, t, quarter, ro);
+    }
+}
+
 // (d0, d1) = (a0 b0 + c, a1 b1 + c) and (d0, d1) *= (b0, b1), one packed instruction each
 __device__ __forceinline__ void fma_pairs(float& d0, float& d1, float a0, float a1, float b0, float b1, float c) {
     asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %6};\n\t"
@@ -714,6 +817,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(sm + C::kOffMisc + 4);
     int* longest = reinterpret_cast<int*>(sm + C::kOffMisc + 8);       // KV tiles of the longest unit
+    uint32_t* redo = reinterpret_cast<uint32_t*>(sm + C::kOffMisc + 12);   // 4 bits for each softmax warp: some row came
+                                                           // out non-finite in the range's first (1) or last (2) piece, or
+                                                           // in a whole unit (4)
     End* ends = reinterpret_cast<End*>(sm + C::kOffEnds);
     SeqRows* first_rows = reinterpret_cast<SeqRows*>(ends + 2);
     long long* tiles_s = reinterpret_cast<long long*>(sm + C::kOffTiles);
@@ -761,6 +867,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         *abort_flag = 0;
         *longest = 0;
+        *redo = 0;
         fence_mbar_init();
     }
     grid_dep_wait();                                       // trees: the prologue's results
@@ -817,27 +924,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
         __syncthreads();
     }
-    Cut cut;
-    cut.tiles = tiles_s;
-    cut.units = units_s;
-    cut.B = p.B;
-    cut.Hkv = p.Hkv;
-    {
-        // A range that holds pieces of two units pays the fixed cost twice, so where there is less
-        // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
-        // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
-        // 42 and 29), unless one long unit among short ones would then run far longer than its
-        // share of all tiles
-        const long long units = (long long)p.Hkv * units_s[p.B];
-        cut.k = kKappa;
-        cut.total = p.Hkv * tiles_s[p.B] + kKappa * units;
-        cut.m = 0;
-        if (cut.total < (long long)(kKappa + 2) * gridDim.x && units <= gridDim.x && units > 0) {
-            const int m = int(gridDim.x) / int(units);
-            if (*longest / unit_pieces(*longest, 1, m) <= int(cut.total) / int(gridDim.x) + 2 * kKappa) cut.m = m;
-        }
-        cut.parts = cut.m ? cut.m * int(units) : int(min((long long)gridDim.x, max(1ll, cut.total / (kKappa + 1))));
-    }
+    const Cut cut = cut_of(p, tiles_s, units_s, *longest);
     // rows without a token (a padded tree's, and those of an invalid sequence) are zeros
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const SeqRows r = seq_rows(p, b);
@@ -1330,44 +1417,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 mbar_arrive(&bars->o_free[t]);
             }
             if (warp_rows) {
-                const unsigned again = __ballot_sync(0xffffffffu, ro.ok && !(odd == 0.f));
-                if (again) __syncwarp();                   // the lanes' stores above come before those below
-                for (unsigned w = again; w; w &= w - 1) {
-                    const int x = __ffs(w) - 1;            // one row at a time, by the whole warp
-                    const Row rx = row_of(p, s, t, x * 4 + quarter, D);
-                    float o4[4], mx, lx;
-                    slow_row<D, E4M3>(p, s, rx, sight_of(p, s, rx), o4, mx, lx);
-                    const size_t px = slot * kM + quarter * 32 + x;
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        const int d = lane * (D / 32) + e;
-                        if (whole) static_cast<uint16_t*>(p.out)[rx.at + d] = f32_to_bf16_rne(o4[e] / lx);
-                        else __stcg(p.part_acc + px * D + d, o4[e]);
-                    }
-                    if (!whole && lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + px, make_float2(mx, lx));
-                }
-            }
-            if (!whole && warp_rows) {
-                // the last of the warps that hold these rows joins the unit's pieces
-                int c0, pieces;
-                if (cut.m) {
-                    c0 = me / cut.m * cut.m;
-                    pieces = unit_pieces(s.n, s.tokens * p.G, cut.m);
-                } else {
-                    const SeqUnits u = seq_units(p, seq_rows(p, s.b));
-                    const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
-                                         u.tiles_before(s.pr) + (long long)cut.k * s.pr + cut.k;
-                    c0 = cut.owner(ub);
-                    pieces = cut.owner(ub + s.n - 1) - c0 + 1;
-                }
-                __threadfence();
-                __syncwarp();
-                int n = 0;
-                if (lane == 0) n = atomicAdd(p.counters + c0 * 8 + t * 4 + quarter, 1);
-                n = __shfl_sync(0xffffffffu, n, 0);
-                if (n == pieces - 1) {
-                    __threadfence();
-                    join_pieces<D>(p, c0, pieces, t, quarter, ro.at, __ballot_sync(0xffffffffu, ro.ok));
+                if (__any_sync(0xffffffffu, ro.ok && !(odd == 0.f))) {
+                    if (lane == 0) atomicOr(redo, (whole ? 4u : head ? 2u : 1u) << (4 * warp));
+                } else if (!whole) {
+                    join_unit<D>(p, cut, s, me, t, quarter, ro);
                 }
             }
             g += s.ntiles + skip2;
@@ -1379,6 +1432,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         if (!alive) {
             *abort_flag = 1;
             atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+        } else {
+            __syncwarp();
+            const uint32_t mine = (*redo >> (4 * warp)) & 15u;
+            if (mine) redo_rows<D, E4M3>(p, sm, mine);
         }
     }
 

@@ -848,3 +848,37 @@ def test_all_rows_of_a_tile_beside_a_hidden_nan(ts, cuda_device, prefix, new, hq
     for _ in range(20):
         again, _ = attend(ts, p, ts.KERNEL_TC_STREAM)
         assert torch.equal(again.view(torch.int16), got.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind,e4m3", [("chunk", False), ("chunk", True), ("tree", True)])
+def test_recomputed_rows_outlast_the_wait_limit(ts, cuda_device, kind, e4m3):
+    """Rows that share a tile with a hidden NaN are recomputed for far longer than the limit of the
+    waits, while the rest of the CTA waits for them: no wait runs out, and every row is right.  (The
+    hand-offs of the fast path take microseconds, the limit is a millisecond.)"""
+    prefix, new = ([1500, 900, 2100, 1300], [488, 500, 484, 510]) if kind == "chunk" else ([1500] * 24, [40] * 24)
+    if e4m3:
+        p = make_8bit(cuda_device, prefix, new, 64, 8, 128, seed=103, spread=0.3)
+    else:
+        p = make(cuda_device, prefix, new, 64, 8, 128, "bf16", seed=103)
+    gen = np.random.default_rng(7)
+    # the last token of a unit of 32 (a chunk), or the last leaf: every row before it in its unit is recomputed
+    poison(p, [[31 + 32 * int(gen.integers(3)) for _ in range(8)] if kind == "chunk" else [39] * 8 for _ in new], slice(17, 18))
+    ts.set_wait_limit_ns(1_000_000)
+    try:
+        if kind == "chunk":
+            got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+            ref = causal64(p)
+        else:
+            rng = np.random.default_rng(3)
+            parents = np.stack([trees.random_recursive(rng, 40) for _ in new])
+            q = p.q.view(len(new), 40, 64, 128)
+            ws = torch.empty(ts.attn_e4m3_workspace_bytes(ts.attn_problem(q, p.k_pages, p.page_table)), dtype=torch.uint8,
+                             device=cuda_device)
+            got = ts.tree_attn_verify_e4m3(q, p.k_pages, p.v_pages, p.k_scales, p.v_scales, p.page_table, p.prefix_lens,
+                                           ints(parents, cuda_device), workspace=ws)
+            st = ts.read_status(ws)
+            ref = tree64(p, q, parents)
+    finally:
+        ts.set_wait_limit_ns(0)
+    assert st == 0
+    check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), 128, "bf16", True)
