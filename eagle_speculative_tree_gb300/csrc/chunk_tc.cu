@@ -420,7 +420,7 @@ __device__ __noinline__ void slow_row(const ChunkParams& p, const Seg& s, const 
         const float mt = warp_max(ok ? x : -INFINITY);
         const float mn = fmaxf(m, mt);
         const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        const float pr = ok ? exp2f(x - mn) : 0.f;
+        const float pr = ok ? exp2f(x - (mn == -INFINITY ? 0.f : mn)) : 0.f;   // a score of -inf weighs 0
         l = l * alpha + warp_sum(pr);
         m = mn;
 #pragma unroll

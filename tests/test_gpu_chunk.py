@@ -882,3 +882,45 @@ def test_recomputed_rows_outlast_the_wait_limit(ts, cuda_device, kind, e4m3):
         ts.set_wait_limit_ns(0)
     assert st == 0
     check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), 128, "bf16", True)
+
+
+# ------------------------------------------------------------------------------ scores of minus infinity
+
+MINUS_INF = [
+    # prefix, new, tokens whose score is -inf for every row
+    ([32], [1], [32]),                                         # alone in its slice of 32 tokens
+    ([300], [20], list(range(32)) + list(range(128, 160))),    # whole slices, before and between finite ones
+    ([0], [40], [0]),                                          # row 0 sees nothing else: NaN by definition
+    ([70, 400], [50, 3], list(range(64))),                     # a whole tile
+]
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS, ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
+@pytest.mark.parametrize("kernel,hidden", [("auto", False), ("auto", True), ("simt", False)])
+@pytest.mark.parametrize("case", MINUS_INF, ids=["own", "slices", "first", "tile"])
+def test_a_score_of_minus_infinity_weighs_nothing(ts, cuda_device, case, kernel, hidden, dtype, e4m3):
+    """Such a token has weight 0, wherever it stands; `hidden`: beside a NaN that the rows do not see, which
+    has the tensor-core form recompute them."""
+    prefix, new, tokens = case
+    if hidden and new[-1] == 1:
+        pytest.skip("a row alone hides nothing")
+    p = make(cuda_device, prefix, new, 8, 2, 128, dtype, e4m3, seed=sum(new))
+    p.q[:] = p.q.abs() * 0.2 + 0.01                            # all products of the token are -inf or finite and positive
+    where = [(int(p.page_table[b, t // 16]), t % 16) for b in range(len(prefix)) for t in tokens]
+    if hidden:
+        poison(p, [[n - 1] * 2 for n in new], slice(9, 10))
+    finite = [x.copy() for x in p.pools64()]
+    for page, at in where:
+        finite[0][page, at] = 0
+        if e4m3:
+            p.k_pages.view(torch.uint8)[page, at] = 0x38
+            p.k_scales[page, :, at] = -float("inf")
+        else:
+            p.k_pages[page, at, :, 5] = -float("inf")
+    host = (p.page_table.cpu().numpy(), p.prefix_lens.cpu().numpy(), p.chunk_offsets.cpu().numpy())
+    q64 = p.q.double().cpu().numpy()
+    out, spread, _ = och.chunk_attention(q64, *p.pools64(), *host)
+    reach = och.chunk_attention(q64, *finite, *host)[2]        # what errors of the finite scores scale with
+    got, st = attend(ts, p, ts.KERNEL_AUTO if kernel == "auto" else ts.KERNEL_SIMT)
+    assert st == 0
+    check_attention(got, out, spread, reach, max(a + b for a, b in zip(prefix, new)), 128, dtype, dtype == "bf16")
