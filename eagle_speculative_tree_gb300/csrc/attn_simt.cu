@@ -249,7 +249,8 @@ __global__ void __launch_bounds__(256) attn_simt_kernel(AttnParams p) {
                 const float sv = ok ? s[r] : -INFINITY;
                 const float mnew = fmaxf(m[r], warp_max(sv));
                 const float alpha = (mnew == -INFINITY) ? 1.f : exp2f(m[r] - mnew);
-                const float pv = ok ? exp2f(sv - mnew) : 0.f;
+                // while no score above -inf has come, 0 is subtracted: a score of -inf weighs 0, not NaN
+                const float pv = ok ? exp2f(sv - (mnew == -INFINITY ? 0.f : mnew)) : 0.f;
                 l[r] = fmaf(l[r], alpha, pv);
                 m[r] = mnew;
 #pragma unroll

@@ -924,3 +924,27 @@ def test_a_score_of_minus_infinity_weighs_nothing(ts, cuda_device, case, kernel,
     got, st = attend(ts, p, ts.KERNEL_AUTO if kernel == "auto" else ts.KERNEL_SIMT)
     assert st == 0
     check_attention(got, out, spread, reach, max(a + b for a, b in zip(prefix, new)), 128, dtype, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_tree_verification_on_cuda_cores_with_scores_of_minus_infinity(ts, cuda_device, dtype, splits):
+    sizes, N, prefix = [9, 12], 12, [400, 64]
+    rng = np.random.default_rng(5)
+    parents = trees.padded([trees.random_recursive(rng, n) for n in sizes], N)
+    p = make(cuda_device, prefix, sizes, 8, 2, 128, dtype, seed=111)
+    for t in (p.k_pages, p.v_pages):                           # tree_attn_verify reads a page's unused slots
+        t.nan_to_num_()
+    q = torch.rand((2, N, 8, 128), device=cuda_device).to(p.q.dtype)
+    finite = p.k_pages.clone()
+    for b in range(2):
+        for t in list(range(32)) + list(range(300, 332)):
+            if t < prefix[b]:
+                page, at = int(p.page_table[b, t // 16]), t % 16
+                p.k_pages[page, at, :, 5] = -float("inf")
+                finite[page, at] = 0
+    out, spread, _ = tree64(p, q, parents)
+    got = ts.tree_attn_verify(q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, ints(parents, cuda_device),
+                              kernel=ts.KERNEL_SIMT, num_splits=splits)
+    p.k_pages = finite
+    check_attention(got, out, spread, tree64(p, q, parents)[2], 412, 128, dtype, False)
