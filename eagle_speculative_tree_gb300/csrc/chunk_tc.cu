@@ -365,6 +365,12 @@ __device__ __forceinline__ Sight sight_of(const ChunkParams& p, const Seg& s, co
     return v;
 }
 
+// Whether the row sees the token at `pos`, below the segment's t1.
+__device__ __forceinline__ bool sees(const ChunkParams& p, const Seg& s, const Sight& v, int pos) {
+    const int j = pos - s.S;
+    return j < 0 || (p.offsets ? pos < v.end : ((j < 64 ? v.a0 >> j : v.a1 >> (j - 64)) & 1ull) != 0);
+}
+
 // A row's exact attention over the segment's visible tokens, by one warp on CUDA cores:
 // (m, l) and O in lane-wise slices of D / 32 elements.  Nothing of a token that the row does
 // not see is read.
@@ -380,11 +386,7 @@ __device__ __noinline__ void slow_row(const ChunkParams& p, const Seg& s, const 
     const uint16_t* q = static_cast<const uint16_t*>(p.q) + r.at;
     for (int base = s.t0; base < s.t1; base += 32) {
         const int pos = base + lane;
-        bool ok = pos < s.t1;
-        if (ok && pos >= s.S) {
-            const int j = pos - s.S;
-            ok = p.offsets ? pos < v.end : ((j < 64 ? v.a0 >> j : v.a1 >> (j - 64)) & 1ull) != 0;
-        }
+        const bool ok = pos < s.t1 && sees(p, s, v, pos);
         long long slot = -1;                               // a page outside the pool holds zeros
         if (ok) {
             const int page = ptab[pos >> 4];
@@ -597,6 +599,57 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
     }
 }
 
+// What a run of tokens holds that is not finite, in the lane's D / 32 columns (a bit each).
+struct Spoil {
+    uint32_t nan, inf;     // of V, in tokens that the row sees
+    uint32_t hidden;       // of V as the MMA reads it, in tokens that it does not see
+    bool key;              // a NaN in K of a token that it sees
+};
+// Adds tokens from .. to - 1 of the segment's sequence, by one warp; pages outside the pool hold zeros.
+template <int D, bool E4M3>
+__device__ __forceinline__ void look(const ChunkParams& p, const Seg& s, const Sight& v, int from, int to, Spoil& f) {
+    constexpr int DS = D / 32;
+    using Code = std::conditional_t<E4M3, unsigned char, uint16_t>;
+    using Word = std::conditional_t<DS * sizeof(Code) == 8, unsigned long long,
+                                    std::conditional_t<DS * sizeof(Code) == 4, uint32_t, uint16_t>>;
+    const int lane = threadIdx.x & 31;
+    const int* ptab = p.page_table + size_t(s.b) * p.max_pages;
+    for (int q0 = from & ~(kPage - 1); q0 < to; q0 += kPage) {
+        const int page = __ldg(ptab + q0 / kPage);
+        if (page < 0 || page >= p.num_pool_pages) continue;
+#pragma unroll 8
+        for (int i = 0; i < kPage; ++i) {
+            const int pos = q0 + i;
+            const size_t at = ((size_t(page) * kPage + i) * p.Hkv + s.h) * D + lane * DS;
+            uint32_t nan[2] = {0, 0}, inf[2] = {0, 0};     // K, V
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                const Word word = __ldg(reinterpret_cast<const Word*>(static_cast<const Code*>(kv ? p.v : p.k) + at));
+#pragma unroll
+                for (int e = 0; e < DS; ++e) {
+                    const uint32_t x = uint32_t(word >> (8 * int(sizeof(Code)) * e)) & (E4M3 ? 0x7fu : 0x7fffu);
+                    nan[kv] |= uint32_t(E4M3 ? x == 0x7fu : x > 0x7f80u) << e;
+                    inf[kv] |= uint32_t(!E4M3 && x == 0x7f80u) << e;
+                }
+            }
+            const bool in = pos >= from && pos < to, seen = in && sees(p, s, v, pos);
+            if (in && !seen) f.hidden |= nan[1] | inf[1];
+            if constexpr (E4M3) {                          // the scale of a token that a row does not see never counts
+                const size_t sc = (size_t(page) * p.Hkv + s.h) * kPage + i;
+                const float ks = __ldg(p.k_scales + sc), vs = __ldg(p.v_scales + sc);
+                if (ks != ks) nan[0] = 1;
+                if (vs != vs) nan[1] = ~0u;
+                else if (isinf(vs)) inf[1] = ~0u;
+            }
+            if (seen) {
+                f.nan |= nan[1];
+                f.inf |= inf[1];
+                f.key |= nan[0] != 0;
+            }
+        }
+    }
+}
+
 // The last of the warps that hold these rows of a cut unit joins its pieces.
 template <int D>
 __device__ __forceinline__ void join_unit(const ChunkParams& p, const Cut& cut, const Seg& s, int me, int t, int quarter,
@@ -626,6 +679,14 @@ __device__ __forceinline__ void join_unit(const ChunkParams& p, const Cut& cut, 
 // One warp's rows that came out non-finite, segment by segment of the CTA's range, recomputed and
 // stored behind what the epilogue stored; then the joins that waited for them: those of the
 // range's last (pending & 2) and first (pending & 1) piece.  `sm`: the CTA's shared memory.
+//
+// A row stands as it is where it sees what spoils it: a NaN in K spoils the whole row; a NaN in
+// a column of V, or an infinity there and nothing hidden in that column, spoils that column and
+// no other.  (An infinity at a weight below 2^-126 gives NaN.)  So what a row may not see counts
+// only among the unit's own tokens and those that share a page with its last one, and one NaN in a
+// prompt does not have all rows behind it recomputed (64 heads, 512 new tokens over 3000, a NaN in
+// token 19: 84 ms if every row is recomputed, 1.8 ms this way, 0.16 ms without the NaN; 32 heads, a
+// prompt of 32768 tokens, a NaN in token 5: 87 ms, 6.0 without).
 template <int D, bool E4M3>
 __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char* sm, uint32_t pending) {
     using C = Cfg<D, E4M3>;
@@ -639,6 +700,8 @@ __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char
     Walk walk;
     walk.start(p, ends[0], ends[1], *reinterpret_cast<const SeqRows*>(ends + 2));
     Seg s;
+    Spoil before{};                                        // tokens `from` .. `upto` - 1 of kv head h of sequence b, which
+    int b = -1, h = -1, from = 0, upto = 0;                // every row of the units at hand sees
     while (walk.next(s)) {
         if (t >= s.nq) continue;
         const Row ro = row_of(p, s, t, lane * 4 + quarter, D);
@@ -656,13 +719,26 @@ __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char
                 o[e] = whole ? bf16_to_f32(__ldcg(static_cast<const uint16_t*>(p.out) + at + d))
                              : __ldcg(p.part_acc + (prow + x) * D + d);
             }
-            float odd = 0.f;
+            uint32_t odd = 0;
 #pragma unroll
-            for (int e = 0; e < DS; ++e) odd = fmaf(o[e], 0.f, odd);
-            if (!__any_sync(0xffffffffu, !(odd == 0.f))) continue;
+            for (int e = 0; e < DS; ++e) odd |= uint32_t(!(o[e] * 0.f == 0.f)) << e;
+            if (!__any_sync(0xffffffffu, odd != 0)) continue;
             const Row rx = row_of(p, s, t, x * 4 + quarter, D);
+            const Sight v = sight_of(p, s, rx);
+            const int own = min(s.t1, s.S + (p.offsets ? s.i0 : 0));      // the first token that a row may not see
+            if (s.b != b || s.h != h || s.t0 != from) {
+                before = Spoil{};
+                b = s.b;
+                h = s.h;
+                from = upto = s.t0;
+            }
+            look<D, E4M3>(p, s, v, upto, own, before);
+            upto = max(upto, own);
+            Spoil f = before;
+            look<D, E4M3>(p, s, v, max(s.t0, own), min(s.L, (s.t1 + kPage - 1) & ~(kPage - 1)), f);
+            if (__any_sync(0xffffffffu, f.key) || !__any_sync(0xffffffffu, (odd & ~(f.nan | (f.inf & ~f.hidden))) != 0)) continue;
             float m, l;
-            slow_row<D, E4M3>(p, s, rx, sight_of(p, s, rx), o, m, l);
+            slow_row<D, E4M3>(p, s, rx, v, o, m, l);
 #pragma unroll
             for (int e = 0; e < DS; ++e) {
                 const int d = lane * DS + e;

@@ -948,3 +948,55 @@ def test_tree_verification_on_cuda_cores_with_scores_of_minus_infinity(ts, cuda_
                               kernel=ts.KERNEL_SIMT, num_splits=splits)
     p.k_pages = finite
     check_attention(got, out, spread, tree64(p, q, parents)[2], 412, 128, dtype, False)
+
+
+def gpu_ms(call):
+    """Milliseconds of a call on the device, the best of three after one that warms up."""
+    call()
+    best = float("inf")
+    for _ in range(3):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("what", ["v", "v_inf", "k", "both"])
+def test_values_that_all_rows_see_do_not_have_them_recomputed(ts, cuda_device, what, e4m3):
+    """One NaN (or infinity) near the start of a sequence reaches every later row by definition.  The rows
+    are what the definition says, beside a NaN at a unit's end that the unit's other rows do not see, and
+    the call does not take hundreds of times as long (a recomputed row costs some microseconds per 10
+    tokens, and there are 65536 of them)."""
+    prefix, new = [3000, 700], [512, 512]
+    if e4m3:
+        p = make_8bit(cuda_device, prefix, new, 64, 8, 128, seed=121, spread=0.3)
+    else:
+        p = make(cuda_device, prefix, new, 64, 8, 128, "bf16", seed=121)
+    clean = gpu_ms(lambda: attend(ts, p, ts.KERNEL_TC_STREAM))
+    page, at = int(p.page_table[0, 1]), 3                      # token 19 of sequence 0
+    bad = float("inf") if what == "v_inf" else float("nan")
+    if what != "k":
+        if e4m3:
+            p.v_scales[page, 2:6, at] = bad                    # kv heads 2 .. 5
+        else:
+            p.v_pages[page, at, 2:6, 77] = bad
+    if what in ("k", "both"):
+        if e4m3:
+            p.k_pages.view(torch.uint8)[page, at, 4, 90] = 0xff
+        else:
+            p.k_pages[page, at, 4, 90] = bad
+    spoiled = gpu_ms(lambda: attend(ts, p, ts.KERNEL_TC_STREAM))
+    poison(p, [[63] * 8, [127] * 8], slice(100, 101))          # hidden from rows of their units
+    got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+    assert st == 0
+    ref = causal64(p)
+    g = got.double().cpu().numpy()
+    # an infinity may come out as itself or as NaN (8-bit: codes of both signs); finite values have to be finite
+    assert np.array_equal(np.isfinite(g), np.isfinite(ref[0]))
+    got[~torch.isfinite(got)] = float("nan")
+    check_attention(got, *ref, 3512, 128, "bf16", True)
+    assert spoiled < 30 * clean + 1, (spoiled, clean)
