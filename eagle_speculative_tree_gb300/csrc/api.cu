@@ -14,8 +14,11 @@ std::atomic<uint64_t> g_launches{0};
 std::atomic<uint64_t> g_wait_ns{kDefaultWaitNs};     // see treespec_set_wait_limit_ns
 std::atomic<int> g_launch_error{0};                 // cudaError_t of the last rejected launch
 
-// TREESPEC_ERR_LAUNCH for a launch the runtime rejected, keeping the runtime's code
+// TREESPEC_ERR_LAUNCH for a launch (or memset, copy or wait) the runtime rejected, keeping the
+// runtime's code.  The runtime also keeps it as the thread's last error, which the check after
+// the next launch would take for that launch's own: it is cleared here.
 int launch_failed(cudaError_t e) {
+    cudaGetLastError();
     g_launch_error.store(int(e));
     return TREESPEC_ERR_LAUNCH;
 }
@@ -309,8 +312,8 @@ extern "C" int tree_attn_verify(const void* q, const void* k_pages, const void* 
     p.stream_flags = plan.kernel == TREESPEC_KERNEL_TC_STREAM ? reinterpret_cast<int32_t*>(ws + lay.flags) : nullptr;
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
-    if (launch_tree_prologue(p, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st); e != cudaSuccess) return launch_failed(e);
+    if (const cudaError_t e = launch_tree_prologue(p, st); e != cudaSuccess) return launch_failed(e);
     g_launches++;
     const cudaError_t e = plan.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_attn_tc_stream(p, st)
                           : plan.kernel == TREESPEC_KERNEL_TC_PAIR ? launch_attn_tc_pair(p, st)
@@ -320,7 +323,7 @@ extern "C" int tree_attn_verify(const void* q, const void* k_pages, const void* 
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;
     if (plan.merge) {
-        if (launch_attn_merge(p, s.dtype, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+        if (const cudaError_t e = launch_attn_merge(p, s.dtype, st); e != cudaSuccess) return launch_failed(e);
         g_launches++;
     }
     return TREESPEC_OK;
@@ -380,9 +383,9 @@ extern "C" int tree_accept_with_mode(const float* target_logits, const int32_t* 
         else cudaGetLastError();                         // not a pointer CUDA knows: treat as device memory
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st); e != cudaSuccess) return launch_failed(e);
     int kernels = 0;
-    if (launch_accept(p, mode, st, &kernels) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = launch_accept(p, mode, st, &kernels); e != cudaSuccess) return launch_failed(e);
     g_launches += kernels;
     return TREESPEC_OK;
 }
@@ -437,8 +440,8 @@ int commit(void* k_pages, void* v_pages, float* k_scales, float* v_scales, const
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
-    if (launch_kv_commit(p, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st); e != cudaSuccess) return launch_failed(e);
+    if (const cudaError_t e = launch_kv_commit(p, st); e != cudaSuccess) return launch_failed(e);
     g_launches++;
     return TREESPEC_OK;
 }
@@ -689,7 +692,7 @@ extern "C" int tree_chunk_append(const void* q, int64_t q_stride, const void* k,
     p.rope_scale = o.rope_scale;
     p.sms = sm_count_or_default();
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st); e != cudaSuccess) return launch_failed(e);
     const cudaError_t err = launch_chunk_append(p, s.dtype, s.kv_dtype, st);
     if (err != cudaSuccess) return launch_failed(err);
     g_launches++;
@@ -740,7 +743,7 @@ extern "C" int tree_chunk_attn(const void* q, const void* k_pages, const void* v
     p.num_pool_pages = s.num_pool_pages;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
     return run_chunk(p, plan, lay, ws, s.dtype, s.kv_dtype, st);
 }
 
@@ -799,7 +802,7 @@ extern "C" int tree_attn_verify_e4m3(const void* q, const void* k_pages, const v
     a.max_pages = s.max_pages_per_seq;
     a.ps = kPage;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
     const cudaError_t e = launch_tree_prologue(a, st);
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;
@@ -867,7 +870,7 @@ extern "C" int tree_draft_step(const float* logprobs, int32_t batch, int32_t fro
     }
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     // the top-k kernel clears the status word (no memset: one stream operation fewer a step)
-    if (launch_draft_step(p, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = launch_draft_step(p, st); e != cudaSuccess) return launch_failed(e);
     g_launches += 2;
     return TREESPEC_OK;
 }
@@ -906,8 +909,8 @@ extern "C" int tree_rerank_pool(const int32_t* node_parent, const int32_t* node_
     p.M = max_nodes;
     p.N = num_nodes;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
-    if (launch_rerank(p, st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaMemsetAsync(p.status, 0, sizeof(uint32_t), st); e != cudaSuccess) return launch_failed(e);
+    if (const cudaError_t e = launch_rerank(p, st); e != cudaSuccess) return launch_failed(e);
     g_launches++;
     return TREESPEC_OK;
 }
@@ -915,9 +918,9 @@ extern "C" int tree_rerank_pool(const int32_t* node_parent, const int32_t* node_
 extern "C" int treespec_read_status(const void* workspace, uint32_t* status, treespec_stream_t stream) {
     if (!workspace || !status) return TREESPEC_ERR_NULL_POINTER;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaStreamSynchronize(st) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
-    if (cudaMemcpy(status, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return TREESPEC_ERR_LAUNCH;
+    if (const cudaError_t e = cudaStreamSynchronize(st); e != cudaSuccess) return launch_failed(e);
+    if (const cudaError_t e = cudaMemcpy(status, workspace, sizeof(uint32_t), cudaMemcpyDeviceToHost); e != cudaSuccess)
+        return launch_failed(e);
     return TREESPEC_OK;
 }
 

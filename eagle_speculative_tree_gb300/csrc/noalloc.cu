@@ -88,8 +88,5 @@ extern "C" int treespec_noalloc_read_status(uint32_t* status, treespec_stream_t 
     void* scratch = nullptr;
     const int rc = scratch_of_current_device(&scratch);
     if (rc != TREESPEC_OK) return rc;
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return TREESPEC_ERR_LAUNCH;
-    if (cudaMemcpy(status, scratch, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
-        return TREESPEC_ERR_LAUNCH;
-    return TREESPEC_OK;
+    return treespec_read_status(scratch, status, stream);
 }

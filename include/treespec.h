@@ -522,8 +522,8 @@ const char *treespec_error_string(int code);
 int treespec_version(void);
 
 /* The CUDA runtime's error code (a cudaError_t; 0 if none) behind the most recent
- * TREESPEC_ERR_LAUNCH of tree_attn_verify in this process, and its name in *name when
- * name is not NULL. */
+ * TREESPEC_ERR_LAUNCH of any call in this process, and its name in *name when name is not
+ * NULL. */
 int treespec_last_launch_error(const char **name);
 
 /* Kernels this process has launched through the library so far (all entry points). */

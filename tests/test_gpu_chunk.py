@@ -1000,3 +1000,45 @@ def test_values_that_all_rows_see_do_not_have_them_recomputed(ts, cuda_device, w
     got[~torch.isfinite(got)] = float("nan")
     check_attention(got, *ref, 3512, 128, "bf16", True)
     assert spoiled < 30 * clean + 1, (spoiled, clean)
+
+
+# ------------------------------------------------------------------------------ the library's host side
+
+def test_a_rejected_call_does_not_fail_the_next_one(ts, cuda_device):
+    """A stream whose capture was made invalid (by waiting for it) refuses what is launched on it; the calls
+    after that, on other streams, succeed."""
+    import ctypes
+    driver = ctypes.CDLL("libcuda.so.1")
+    p = make(cuda_device, [20, 5], [4, 3], 8, 2, 128, "bf16", seed=131)
+    q, k, v, qw, kw, f = append_inputs(cuda_device, p, 1, 128, True)
+    prob = ts.chunk_problem(p.q, p.k_pages, p.page_table, p.chunk_offsets)
+    ws = torch.empty(ts.chunk_attn_workspace_bytes(prob), dtype=torch.uint8, device=cuda_device)
+    q_out, out = torch.empty_like(p.q), torch.empty_like(p.q)
+    path, length, lens = ints([[1, -1]] * 2, cuda_device), ints([1, 1], cuda_device), ints([0, 0], cuda_device)
+
+    def calls(stream):
+        yield lambda: ts.tree_chunk_append(q, k, v, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, p.chunk_offsets, q_out,
+                                           q_norm=qw, k_norm=kw, inv_freq=f, workspace=ws, stream=stream)
+        for kernel in (ts.KERNEL_AUTO, ts.KERNEL_SIMT):
+            yield lambda: ts.tree_chunk_attn(p.q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, p.chunk_offsets, out,
+                                             kernel=kernel, workspace=ws, stream=stream)
+        yield lambda: ts.tree_kv_commit(p.k_pages, p.v_pages, p.page_table, p.prefix_lens, path, length, lens, workspace=ws,
+                                        stream=stream)
+
+    for c in calls(None):
+        c()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    handle = ctypes.c_void_p(stream.cuda_stream)
+    for n in range(4):
+        assert driver.cuStreamBeginCapture_v2(handle, 1) == 0  # thread-local: nothing else is affected
+        assert driver.cuStreamSynchronize(handle) != 0         # not allowed while capturing
+        with pytest.raises(ts.TreespecError):
+            list(calls(stream))[n]()
+        graph = ctypes.c_void_p()
+        assert driver.cuStreamEndCapture(handle, ctypes.byref(graph)) != 0 and not graph.value
+        for c in calls(None):
+            c()
+        assert ts.last_launch_error()[0] != 0                  # the rejected one's
+    torch.cuda.synchronize()
+    assert ts.read_status(ws) == 0
