@@ -404,20 +404,39 @@ _I32, _F32, _BF16, _E4M3 = torch.int32, torch.float32, torch.bfloat16, torch.flo
 _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _need_all(index: int, *wants) -> None:
-    """Each want is (tensor, name, dtype, shape): contiguous, on cuda:`index`."""
-    for t, name, dtype, shape in wants:
-        if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
-            continue
+def _need_tensors(**named) -> None:
+    for name, t in named.items():
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
-        if not t.is_cuda or t.get_device() != index:
-            raise ValueError(f"{name} must be on cuda:{max(index, 0)}")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_all(index: int, *wants) -> None:
+    """Each want is (tensor, name, dtype, shape): contiguous, on cuda:`index`."""
+    try:
+        for t, name, dtype, shape in wants:
+            if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+                continue
+            _need_tensors(**{name: t})
+            if not t.is_cuda or t.get_device() != index:
+                raise ValueError(f"{name} must be on cuda:{max(index, 0)}")
+            if t.dtype is not dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.shape != shape:
+                raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+            raise ValueError(f"{name} must be contiguous")
+    except AttributeError:                                     # no cost to the calls that are right
+        _need_tensors(**{want[1]: want[0] for want in wants})
+        raise
+
+
+def _float_type_error(q) -> ValueError:
+    _need_tensors(q=q)
+    return ValueError("q must be float32 or bfloat16")
+
+
+def _code_type_error(k_pages) -> ValueError:
+    _need_tensors(k_pages=k_pages)
+    return ValueError(f"k_pages must be {_E4M3}, got {k_pages.dtype}")
 
 
 def _index_of(q: torch.Tensor, name: str) -> int:
@@ -453,6 +472,7 @@ def _fresh(shape, dtype, device, stream) -> torch.Tensor:
 def _workspace_for(workspace, need: int, index: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _fresh((need,), torch.uint8, device, stream)
+    _need_tensors(workspace=workspace)
     if workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{index}")
     return workspace
@@ -502,9 +522,13 @@ def _attn_struct(*sizes):
 
 def _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel) -> tuple:
     """The sizes of a call in the order of ChunkProblem's fields."""
-    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or chunk_offsets.dim() != 1:
-        raise ValueError("q is [tokens][heads][head_dim], k_pages [pages][16][kv heads][head_dim], "
-                         "page_table [batch][pages], chunk_offsets [batch + 1]")
+    try:
+        if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2 or chunk_offsets.dim() != 1:
+            raise ValueError("q is [tokens][heads][head_dim], k_pages [pages][16][kv heads][head_dim], "
+                             "page_table [batch][pages], chunk_offsets [batch + 1]")
+    except AttributeError:
+        _need_tensors(q=q, k_pages=k_pages, page_table=page_table, chunk_offsets=chunk_offsets)
+        raise
     T, Hq, D = q.shape
     P, ps, Hkv, D2 = k_pages.shape
     B, pages = page_table.shape
@@ -540,15 +564,16 @@ def tree_chunk_append(q, k, v, k_pages, v_pages, page_table, prefix_lens, chunk_
     q_norm / k_norm [D] and inv_freq [rot_dim / 2] float32 (None: no norm, no rotation).
     Returns q_out [T][Hq][D] (q itself may be given); the pools are written in place.  Rows
     that are left out stay as they are in `q_out` (and hold nothing of use in a new one)."""
-    dt = q.dtype
+    dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
-        raise ValueError("q must be float32 or bfloat16")
+        raise _float_type_error(q)
     index = _index_of(q, "q")
     sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, KERNEL_AUTO)
     B, T, Hq, Hkv, D = sizes[:5]
     strides = []
     for name, t, H in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t.dtype is not dt or t.get_device() != index or t.shape != (T, H, D):
+        if getattr(t, "dtype", None) is not dt or t.get_device() != index or t.shape != (T, H, D):
+            _need_tensors(**{name: t})
             raise ValueError(f"{name} must be {dt} on cuda:{index} with shape {(T, H, D)}")
         to_token, to_head, to_element = t.stride()
         if to_element != 1 or (H > 1 and to_head != D):
@@ -565,6 +590,7 @@ def tree_chunk_append(q, k, v, k_pages, v_pages, page_table, prefix_lens, chunk_
         wants.append((k_norm, "k_norm", _F32, (D,)))
     rot = 0
     if inv_freq is not None:
+        _need_tensors(inv_freq=inv_freq)
         rot = 2 * inv_freq.numel()
         wants.append((inv_freq, "inv_freq", _F32, (rot // 2,)))
     if q_out is None:
@@ -572,7 +598,7 @@ def tree_chunk_append(q, k, v, k_pages, v_pages, page_table, prefix_lens, chunk_
     else:
         wants.append((q_out, "q_out", dt, (T, Hq, D)))
     _need_all(index, *wants)
-    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         workspace = _workspace_for(workspace, append_workspace_bytes(), index, q.device, stream)
     opt = AppendOptions(_ptr(q_norm), _ptr(k_norm), _ptr(inv_freq), _ptr(positions), norm_eps, rope_scale, rot, rope)
     _launch(index, stream, _lib.tree_chunk_append, q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(),
@@ -600,9 +626,9 @@ def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets,
     prefix_lens [B], chunk_offsets [B + 1] int32.  Returns out [T][Hq][D] in q's dtype; rows
     that belong to no sequence are left as they are in `out` (and hold nothing of use in a
     new one)."""
-    dt = q.dtype
+    dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
-        raise ValueError("q must be float32 or bfloat16")
+        raise _float_type_error(q)
     index = _index_of(q, "q")
     sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel)
     B = sizes[0]
@@ -614,7 +640,7 @@ def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets,
     else:
         wants.append((out, "out", dt, q.shape))
     _need_all(index, *wants)
-    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         workspace = _workspace_for(workspace, chunk_attn_workspace_bytes(ChunkProblem(*sizes)), index, q.device, stream)
     _launch(index, stream, _lib.tree_chunk_attn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
             _ptr(v_scales), page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(), out.data_ptr(),
@@ -637,14 +663,15 @@ def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, p
     q [B][N][Hq][D] (float32 or bfloat16), k_pages / v_pages [P][16][Hkv][D] float8_e4m3fn,
     k_scales / v_scales [P][Hkv][16] float32, page_table [B][max_pages], prefix_lens [B],
     tree_parents [B][N] int32.  Returns out [B][N][Hq][D] in q's dtype."""
-    dt = q.dtype
+    dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
-        raise ValueError("q must be float32 or bfloat16")
+        raise _float_type_error(q)
     index = _index_of(q, "q")
-    if q.dim() != 4 or page_table.dim() != 2:
+    if getattr(k_pages, "dtype", None) is not _E4M3:
+        raise _code_type_error(k_pages)
+    if not isinstance(page_table, torch.Tensor) or q.dim() != 4 or page_table.dim() != 2:
+        _need_tensors(page_table=page_table)
         raise ValueError("q is [batch][nodes][heads][head_dim], page_table [batch][pages]")
-    if k_pages.dtype is not _E4M3:
-        raise ValueError(f"k_pages must be {_E4M3}, got {k_pages.dtype}")
     B, N, Hq, D = q.shape
     wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
              (page_table, "page_table", _I32, (B, page_table.shape[1])), (prefix_lens, "prefix_lens", _I32, (B,)),
@@ -657,7 +684,7 @@ def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, p
     P, ps, Hkv, D2 = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and k_pages differ")
-    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         workspace = _workspace_for(workspace, attn_e4m3_workspace_bytes(attn_problem(q, k_pages, page_table, kernel=kernel)),
                                    index, q.device, stream)
     _launch(index, stream, _lib.tree_attn_verify_e4m3, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
@@ -673,10 +700,12 @@ def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix
     """Move the accepted path's codes and scales next to each prefix, in place; see
     include/treespec.h.  Pools and scales as for tree_attn_verify_e4m3, the rest as for
     tree_kv_commit.  Returns new_prefix_lens [B] int32."""
-    if k_pages.dtype is not _E4M3:
-        raise ValueError(f"k_pages must be {_E4M3}, got {k_pages.dtype}")
+    if getattr(k_pages, "dtype", None) is not _E4M3:
+        raise _code_type_error(k_pages)
     index = _index_of(k_pages, "k_pages")
-    if accept_path.dim() != 2 or page_table.dim() != 2:
+    if not isinstance(accept_path, torch.Tensor) or not isinstance(page_table, torch.Tensor) or \
+            accept_path.dim() != 2 or page_table.dim() != 2:
+        _need_tensors(accept_path=accept_path, page_table=page_table)
         raise ValueError("accept_path is [batch][nodes], page_table [batch][pages]")
     B, N = accept_path.shape
     wants = [*_pool_wants(None, k_pages, v_pages, k_scales, v_scales),
@@ -688,7 +717,7 @@ def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix
         wants.append((new_prefix_lens, "new_prefix_lens", _I32, (B,)))
     _need_all(index, *wants)
     P, ps, Hkv, D = k_pages.shape
-    if workspace is None or workspace.get_device() != index or not workspace.is_contiguous():
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         workspace = _workspace_for(workspace, commit_workspace_bytes(), index, k_pages.device, stream)
     _launch(index, stream, _lib.tree_kv_commit_e4m3, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
             v_scales.data_ptr(), page_table.data_ptr(), prefix_lens.data_ptr(), accept_path.data_ptr(),

@@ -169,3 +169,19 @@ def test_binding_refusals_name_the_argument():
         ts.tree_kv_commit_e4m3(pool, pool, pool, pool, table, ints, table, ints)
     with pytest.raises(ValueError, match="unsupported"):
         ts.chunk_attn_workspace_bytes(ts.ChunkProblem(1, 1, 3, 2, 64, 16, 1, 1, 0, 0))
+
+
+def test_binding_names_an_argument_that_is_no_tensor():
+    import torch
+    q, pool = torch.zeros(4, 8, 64), torch.zeros(3, 16, 2, 64)
+    table, offsets = torch.zeros(1, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for name in ("q", "k_pages", "page_table", "chunk_offsets"):
+        args = dict(q=q, k_pages=pool, page_table=table, chunk_offsets=offsets)
+        args[name] = None
+        with pytest.raises(ValueError, match=f"{name} must be a tensor, got NoneType"):
+            ts.chunk_problem(**args)
+    for call, n in ((ts.tree_chunk_attn, 6), (ts.tree_chunk_append, 8), (ts.tree_attn_verify_e4m3, 8)):
+        with pytest.raises(ValueError, match="q must be a tensor, got list"):
+            call(*[[1.0]] * n)
+    with pytest.raises(ValueError, match="k_pages must be a tensor"):
+        ts.tree_kv_commit_e4m3(*[None] * 8)

@@ -1042,3 +1042,25 @@ def test_a_rejected_call_does_not_fail_the_next_one(ts, cuda_device):
         assert ts.last_launch_error()[0] != 0                  # the rejected one's
     torch.cuda.synchronize()
     assert ts.read_status(ws) == 0
+
+
+def test_an_argument_that_is_no_tensor_is_named(ts, cuda_device):
+    import inspect
+    p = make(cuda_device, [20, 5], [4, 4], 8, 2, 128, "bf16", True, seed=133)
+    tree = ints([[-1, 0, 1, 1]] * 2, cuda_device)
+    have = dict(q=p.q, k=p.q[:, :2], v=p.q[:, 2:4], k_pages=p.k_pages, v_pages=p.v_pages, k_scales=p.k_scales,
+                v_scales=p.v_scales, page_table=p.page_table, prefix_lens=p.prefix_lens, chunk_offsets=p.chunk_offsets,
+                tree_parents=tree, accept_path=tree, accept_len=ints([1, 1], cuda_device))
+    extra = dict(positions=None, q_norm=None, k_norm=None, inv_freq=None, q_out=None, out=None, new_prefix_lens=None,
+                 workspace=None)
+    for fn in (ts.tree_chunk_append, ts.tree_chunk_attn, ts.tree_attn_verify_e4m3, ts.tree_kv_commit_e4m3):
+        names = inspect.signature(fn).parameters
+        args = {n: t for n, t in have.items() if n in names}
+        if fn is ts.tree_attn_verify_e4m3:
+            args["q"] = p.q.view(2, 4, 8, 128)
+        for name in [n for n in (*have, *extra) if n in names]:
+            with pytest.raises(ValueError, match=name.replace("_scales", "_scales|scales")):
+                fn(**{**args, name: 3.5})
+            if name in have:
+                with pytest.raises(ValueError, match=name):
+                    fn(**{**args, name: None})
