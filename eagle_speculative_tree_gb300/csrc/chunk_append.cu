@@ -27,14 +27,18 @@ namespace {
 constexpr float kScaleMin = 7.8886090522101181e-31f;   // 2^-100, the scale of an all-zero head
 
 // inv_freq in turns per position, as a fraction of 2^64 (modulo whole turns).  f = m 2^(e - 150)
-// with a 24-bit m, and 2 / pi = C 2^-64, so f / (2 pi) 2^64 = m C 2^(e - 152).
+// with a 24-bit m, and 2 / pi = C 2^-96, so f / (2 pi) 2^64 = m C 2^(e - 184).  96 bits of 2 / pi
+// leave f below 2^24 an error under 2^-73 of a turn per position.
 __device__ __forceinline__ uint64_t turns_fixed(float f) {
     const uint32_t u = __float_as_uint(f);
     const int ex = int((u >> 23) & 255u);
     const uint64_t m = (u & 0x7fffffu) | (ex ? 0x800000u : 0u);
-    const uint64_t C = 0xA2F9836E4E441529ull;            // floor(2^65 / pi)
-    const uint64_t lo = m * C, hi = __umul64hi(m, C);
-    const int s = 152 - (ex ? ex : 1);                   // right shift of the 88-bit product
+    // C = floor(2^97 / pi) in words of 32 bits; m C in 120 bits, hi and lo
+    const uint64_t p0 = m * 0xFC2757D1u;
+    const uint64_t p1 = m * 0x4E441529u + (p0 >> 32);
+    const uint64_t hi = m * 0xA2F9836Eu + (p1 >> 32);
+    const uint64_t lo = (p1 << 32) | uint32_t(p0);
+    const int s = 184 - (ex ? ex : 1);                   // right shift of the product
     uint64_t t;
     if (s >= 128) t = 0;
     else if (s >= 64) t = hi >> (s - 64);

@@ -1064,3 +1064,15 @@ def test_an_argument_that_is_no_tensor_is_named(ts, cuda_device):
             if name in have:
                 with pytest.raises(ValueError, match=name):
                     fn(**{**args, name: None})
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_append_angles_at_the_stated_limit_of_the_frequencies(ts, cuda_device, layout):
+    """Frequencies up to the last float32 below 2^24 at positions up to 2^31 - 1."""
+    p = make(cuda_device, [0], [6], 2, 1, 64, "f32", seed=2)
+    q, k, v, qw, kw, _ = append_inputs(cuda_device, p, 4, 64, False)
+    f = torch.tensor([2.0 ** 24 - 1, 1024.5, 65537.25, 1048577.0, 12345678.0, 333333.34, 4095.9998, 7.0] * 4,
+                     device=cuda_device)
+    pos = ints([0, 1, 65537, 123456789, (1 << 30) + 7, (1 << 31) - 1], cuda_device)
+    assert check_append(ts, p, q, k, v, qw, kw, f, pos, layout) == 0
+    assert check_append(ts, p, q, k, v, qw, kw, -f, pos, layout) == 0
