@@ -511,7 +511,7 @@ ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long 
     c.kernel = TREESPEC_KERNEL_SIMT;
     // Row blocks no larger than the mean sequence fills, and smaller ones where those and
     // splits of at least 128 tokens would leave SMs without a CTA: a block of 64 rows reads
-    // K and V an eighth as often as one of 8, but a small problem is bound by one CTA's run
+    // K and V a quarter as often as one of 16, but a small problem is bound by one CTA's run
     // (5 sequences of up to 130 tokens x 4 heads over up to 830 tokens of 64, float32: 59 us
     // with blocks of 64 rows in splits of 256 tokens, 27 us with this rule).
     const long long mean = (rows + batch - 1) / batch;

@@ -1,7 +1,7 @@
 // Attention of packed chunks (tree_chunk_attn), and of trees over 8-bit pools, on CUDA
 // cores: any dtype, head dim 64 or 128, any group size.
 //
-// A CTA holds up to RB = 8, 16, 32 or 64 query rows of one kv head (the host takes the
+// A CTA holds up to RB = 16, 32 or 64 query rows of one kv head (the host takes the
 // size that the batch's mean rows per sequence fill; row r = token i * G + g of a
 // sequence's new tokens) and one split of the sequence's logical tokens, and keeps the usual partial
 // state per row: m = max s, l = sum 2^(s - m), acc = sum 2^(s - m) V, with s = q . K
@@ -112,7 +112,7 @@ template <KvKind KV, int D>
 __host__ __device__ inline Shape shape_of(int rows) {
     using C = Cfg<KV, D>;
     Shape s;
-    s.RW = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+    s.RW = rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
     int ts = 8 / s.RW;
     s.TS = ts > C::TSMAX ? C::TSMAX : ts;
     s.nwarps = s.RW * s.TS;
@@ -471,7 +471,7 @@ template <typename T, KvKind KV, int D>
 cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     const long long total_rows = (long long)p.T * p.G;
     const int RB = p.rows_block;
-    if (RB < 1 || RB > kRows) return cudaErrorInvalidValue;
+    if (RB != 16 && RB != 32 && RB != kRows) return cudaErrorInvalidValue;
     const long long units = p.offsets ? total_rows / RB + p.B : (long long)p.B * ((p.N * p.G + RB - 1) / RB);
     const Shape sh = shape_of<KV, D>(RB);
     if (sh.smem > size_t(kMaxSmem)) return cudaErrorInvalidValue;
