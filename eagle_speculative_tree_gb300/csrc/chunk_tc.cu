@@ -1506,6 +1506,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             s = nxt;
         }
         if (!alive) {
+            cp_async_wait_all_groups();                    // the next segment's Q may be on its way
             *abort_flag = 1;
             atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
         } else {

@@ -1076,3 +1076,26 @@ def test_append_angles_at_the_stated_limit_of_the_frequencies(ts, cuda_device, l
     pos = ints([0, 1, 65537, 123456789, (1 << 30) + 7, (1 << 31) - 1], cuda_device)
     assert check_append(ts, p, q, k, v, qw, kw, f, pos, layout) == 0
     assert check_append(ts, p, q, k, v, qw, kw, -f, pos, layout) == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_waits_that_run_out_anywhere_leave_the_next_call_right(ts, cuda_device, e4m3):
+    """Limits from below the first hand-off to about a call's whole time: the call ends with TIMEOUT or is
+    right, and so is one without a limit after it."""
+    p = make_8bit(cuda_device, [1500, 300, 0, 900], [200, 3, 129, 64], 32, 4, 128, seed=141)
+    if not e4m3:
+        p.k_pages, p.v_pages = ((x.float() * 0.01).to(torch.bfloat16) for x in (p.k_pages, p.v_pages))
+        p.k_scales = p.v_scales = None
+    want, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+    assert st == 0
+    for limit in (1, 500, 1000, 1500, 2000, 3000, 5000, 8000, 15000, 25000, 60000):
+        ts.set_wait_limit_ns(limit)
+        try:
+            got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+        finally:
+            ts.set_wait_limit_ns(0)
+        assert st in (0, 16)
+        if st == 0:
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
+        assert st == 0 and torch.equal(got.view(torch.int16), want.view(torch.int16))
