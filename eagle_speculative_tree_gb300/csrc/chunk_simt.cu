@@ -132,8 +132,10 @@ __device__ __forceinline__ long long block_base(const ChunkParams& p, int b) {
     return p.offsets ? (long long)max(0, p.offsets[b]) * p.G / RB + b : (long long)b * ((p.N * p.G + RB - 1) / RB);
 }
 
+// float32 K/V take 139 KB of shared memory, so one CTA fits an SM: told so, the compiler uses the
+// registers there are (5 short chunks of 64-element heads: 26.7 us, 29 with 128 registers and spills)
 template <typename T, KvKind KV, int D>
-__global__ void __launch_bounds__(256) chunk_simt_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(const ChunkParams p) {
     using C = Cfg<KV, D>;
     constexpr int DS = C::DS;
     extern __shared__ __align__(16) unsigned char smem[];
