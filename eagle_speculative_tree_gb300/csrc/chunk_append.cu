@@ -321,35 +321,28 @@ __global__ void __launch_bounds__(kThreads) chunk_append_kernel(const AppendPara
     }
 }
 
-// Launch shapes, measured at 32 q / 8 kv heads of 128 in bf16 or over 8-bit pools:
+// Launch shapes, three heads per thread at a time in all but the first (five measured
+// slower nearly everywhere: 2048 tokens x 80 heads 28.7 us against 24.6, 13114 tokens x 36 heads
+// into 8 bits 60.1 against 52.6; faster by 3% for 13114 x 80 in bf16):
 //   few tokens: one CTA per token and group of heads, so that the latency is that of one head
-//   (1 token: 6.3 us with its status word's clearing, 2 us of it the kernel's own chain);
-//   up to 32 tokens per SM: CTAs of 256 threads, 4 tokens each once there are 8 per SM (2048
-//   tokens x 80 heads: 22.4 us, 24.7 with 128 threads, 26.7 with 8 tokens);
-//   more: CTAs of 128 threads, which leave more of an SM's registers in use at once (13114
-//   tokens x 48 heads, 8-bit: 63.6 us = 4.7 TB/s, 70.0 with 256 threads).
+//   (1 token x 48 heads: 6.3 us with its status word's clearing, 2 us of it the kernel's own chain);
+//   up to 32 tokens per SM: CTAs of 256 threads, 2 tokens each once there are 8 per SM (2048 tokens x
+//   80 heads 22.6 us; 4 tokens 24.6, 4 tokens by 128 threads 26.7, 8 tokens 27.0);
+//   more: CTAs of 128 threads, 4 tokens each, which leave more of an SM's registers in use at once (13114
+//   tokens x 48 heads, 8-bit: 63.5 us = 4.7 TB/s, 68.6 with 256 threads).
 template <typename T, bool E4M3, int D>
 cudaError_t launch_typed(const AppendParams& p, cudaStream_t s) {
     const int H = p.Hq + 2 * p.Hkv;
     constexpr int GRP = 256 / (D / 8);
     const int rounds = (H + GRP - 1) / GRP;              // of GRP heads by 256 threads
-    const unsigned T4 = unsigned((p.T + 3ll) / 4);
-    if ((long long)p.T * rounds <= 2ll * p.sms) {
+    if ((long long)p.T * rounds <= 2ll * p.sms)
         chunk_append_kernel<T, E4M3, D, 1, 1, 256><<<dim3(unsigned(p.T), unsigned(rounds)), 256, 0, s>>>(p, GRP);
-    } else if (p.T < 32 * p.sms) {
-        const bool five = rounds > 3 && rounds != 6;     // five heads per thread at a time, or three
-        if (p.T < 8 * p.sms) {
-            if (five) chunk_append_kernel<T, E4M3, D, 1, 5, 256><<<dim3(unsigned(p.T)), 256, 0, s>>>(p, H);
-            else chunk_append_kernel<T, E4M3, D, 1, 3, 256><<<dim3(unsigned(p.T)), 256, 0, s>>>(p, H);
-        } else {
-            if (five) chunk_append_kernel<T, E4M3, D, 4, 5, 256><<<dim3(T4), 256, 0, s>>>(p, H);
-            else chunk_append_kernel<T, E4M3, D, 4, 3, 256><<<dim3(T4), 256, 0, s>>>(p, H);
-        }
-    } else {
-        const int r128 = (H + GRP / 2 - 1) / (GRP / 2);
-        if (r128 > 3 && r128 != 6) chunk_append_kernel<T, E4M3, D, 4, 5, 128><<<dim3(T4), 128, 0, s>>>(p, H);
-        else chunk_append_kernel<T, E4M3, D, 4, 3, 128><<<dim3(T4), 128, 0, s>>>(p, H);
-    }
+    else if (p.T < 8 * p.sms)
+        chunk_append_kernel<T, E4M3, D, 1, 3, 256><<<dim3(unsigned(p.T)), 256, 0, s>>>(p, H);
+    else if (p.T < 32 * p.sms)
+        chunk_append_kernel<T, E4M3, D, 2, 3, 256><<<dim3(unsigned((p.T + 1ll) / 2)), 256, 0, s>>>(p, H);
+    else
+        chunk_append_kernel<T, E4M3, D, 4, 3, 128><<<dim3(unsigned((p.T + 3ll) / 4)), 128, 0, s>>>(p, H);
     return cudaGetLastError();
 }
 

@@ -1099,3 +1099,16 @@ def test_waits_that_run_out_anywhere_leave_the_next_call_right(ts, cuda_device, 
             assert torch.equal(got.view(torch.int16), want.view(torch.int16))
         got, st = attend(ts, p, ts.KERNEL_TC_STREAM)
         assert st == 0 and torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("tokens,hq,hkv,dim,dtype,e4m3", [
+    (1217, 28, 4, 64, "bf16", True),                           # 8 tokens per SM and a last CTA with one token
+    (1400, 60, 2, 128, "f32", False),
+    (4863, 5, 5, 128, "bf16", False),                          # just below 32 tokens per SM, just above
+    (4867, 3, 1, 64, "bf16", True),
+])
+def test_append_at_the_borders_of_the_launch_shapes(ts, cuda_device, tokens, hq, hkv, dim, dtype, e4m3):
+    a = tokens // 3
+    p = make(cuda_device, [5, 0, 40], [a, 7, tokens - a - 7], hq, hkv, dim, dtype, e4m3, seed=tokens, lead=1)
+    q, k, v, qw, kw, f = append_inputs(cuda_device, p, 3, 48, True)
+    assert check_append(ts, p, q, k, v, qw, kw, f, None, tokens % 2) == 0
