@@ -395,13 +395,16 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
             const float* src = scr + size_t((t * RW + rwi) * 8 + r) * (D + 2);
             // a slice whose scores are all NaN has m = -inf and l = NaN: kept, not skipped
             const bool none = src[D] == -INFINITY && src[D + 1] == 0.f;
-            const float f = none ? 0.f : src[D] == -INFINITY ? 1.f : exp2f(src[D] - mm);
+            // one without weight is left out (-1), not one whose weight rounds to 0: a NaN stays one
+            const float f = none ? -1.f : src[D] == -INFINITY ? 1.f : exp2f(src[D] - mm);
             if (!none) lsum = fmaf(src[D + 1], f, lsum);
             fin_s[t][lr] = f;
         }
         if (p.num_splits == 1) {
             const float inv = 1.f / lsum;
-            for (int t = 0; t < TS; ++t) fin_s[t][lr] *= inv;
+            if (lsum == 0.f) fin_s[0][lr] = NAN;           // no token of a weight above 0: undefined
+            else
+                for (int t = 0; t < TS; ++t) fin_s[t][lr] *= inv;
         } else {
             p.part_ml[part(lr) * 2] = mm;
             p.part_ml[part(lr) * 2 + 1] = lsum;
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
         float a = 0.f;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-            if (t < TS && fin_s[t][lr] != 0.f) a = fmaf(src[size_t(t) * RW * 8 * (D + 2)], fin_s[t][lr], a);
+            if (t < TS && !(fin_s[t][lr] < 0.f)) a = fmaf(src[size_t(t) * RW * 8 * (D + 2)], fin_s[t][lr], a);
         if (p.num_splits == 1) store_out<T>(p.out, at_s[lr] + d, lr < live_rows ? a : 0.f);
         else p.part_acc[at_s[lr] + d] = a;
     }

@@ -453,8 +453,9 @@ __device__ __noinline__ void slow_row(const ChunkParams& p, const Seg& s, const 
 
 // One warp's 32 rows of a cut unit: partial k of the unit is in slot 2 c0 + 1 (k = 0) or
 // 2 (c0 + k).  M = max m_k, out = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M), the pieces in
-// their order.  `valid`: the lanes that hold rows.  O is read with the columns across the
-// lanes.  Few pieces (a unit of many rows cut once or twice): a lane works out its own row's
+// their order; a piece that gives the row no weight (no visible token, or only scores of -inf) has
+// l = 0 and is left out, one whose weight rounds to 0 is not: a NaN that the row sees stays a NaN.
+// `valid`: the lanes that hold rows.  O is read with the columns across the lanes.  Few pieces (a unit of many rows cut once or twice): a lane works out its own row's
 // weights, then eight rows at a time (54 nodes x 4 heads over 736 tokens, three pieces: 32 us a call, 39 by the
 // other way).  More: four rows at a time, their (m, l) with a piece per lane.
 template <int D>
@@ -480,8 +481,8 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
         for (int k = 0; k < 4; ++k) M = fmaxf(M, x[k].x);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            w[k] = x[k].x == -INFINITY ? (x[k].y == 0.f ? 0.f : 1.f) : ex2(x[k].x - M);
-            if (w[k] != 0.f) l += x[k].y * w[k];
+            w[k] = x[k].x == -INFINITY ? (x[k].y == 0.f ? -1.f : 1.f) : ex2(x[k].x - M);
+            if (w[k] >= 0.f) l += x[k].y * w[k];
         }
         const float inv = 1.f / l;
         for (unsigned left = valid; left;) {
@@ -516,7 +517,7 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
                 for (int i = 0; i < kF; ++i) {
                     const float wi = __shfl_sync(0xffffffffu, w[k], row[i]);
 #pragma unroll
-                    for (int e = 0; e < DS; ++e) acc[i][e] = wi == 0.f ? acc[i][e] : fmaf(y[i][e], wi, acc[i][e]);
+                    for (int e = 0; e < DS; ++e) acc[i][e] = wi < 0.f ? acc[i][e] : fmaf(y[i][e], wi, acc[i][e]);
                 }
             }
 #pragma unroll
@@ -560,9 +561,9 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
         for (int k0 = 0; k0 < pieces; k0 += 32) {
             if (pieces > 32) fetch(k0);
 #pragma unroll
-            for (int i = 0; i < kR; ++i) {                  // a piece without a visible token has l = 0
-                w[i] = x[i].x == -INFINITY ? (x[i].y == 0.f ? 0.f : 1.f) : ex2(x[i].x - M[i]);
-                l[i] += warp_sum(w[i] == 0.f ? 0.f : x[i].y * w[i]);
+            for (int i = 0; i < kR; ++i) {
+                w[i] = x[i].x == -INFINITY ? (x[i].y == 0.f ? -1.f : 1.f) : ex2(x[i].x - M[i]);
+                l[i] += warp_sum(w[i] < 0.f ? 0.f : x[i].y * w[i]);
             }
             const int kn = min(32, pieces - k0);
 #pragma unroll 4
@@ -584,7 +585,7 @@ __device__ __noinline__ void join_pieces(const ChunkParams& p, int c0, int piece
                 for (int i = 0; i < kR; ++i) {
                     const float wi = __shfl_sync(0xffffffffu, w[i], k);
 #pragma unroll
-                    for (int e = 0; e < DS; ++e) acc[i][e] = wi == 0.f ? acc[i][e] : fmaf(y[i][e], wi, acc[i][e]);
+                    for (int e = 0; e < DS; ++e) acc[i][e] = wi < 0.f ? acc[i][e] : fmaf(y[i][e], wi, acc[i][e]);
                 }
             }
         }

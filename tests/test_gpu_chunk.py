@@ -1112,3 +1112,33 @@ def test_append_at_the_borders_of_the_launch_shapes(ts, cuda_device, tokens, hq,
     p = make(cuda_device, [5, 0, 40], [a, 7, tokens - a - 7], hq, hkv, dim, dtype, e4m3, seed=tokens, lead=1)
     q, k, v, qw, kw, f = append_inputs(cuda_device, p, 3, 48, True)
     assert check_append(ts, p, q, k, v, qw, kw, f, None, tokens % 2) == 0
+
+
+@pytest.mark.parametrize("dtype,e4m3", KINDS, ids=["f32", "bf16", "f32-e4m3", "bf16-e4m3"])
+@pytest.mark.parametrize("kernel", ["auto", "simt"])
+@pytest.mark.parametrize("where", ["k", "v"])
+@pytest.mark.parametrize("prefix,new", [([3000], [1]), ([1500], [70]), ([900, 40], [5, 1]), ([1000] * 40, [1] * 40),
+                                        ([100], [1])])
+def test_a_nan_among_tokens_of_no_weight_is_not_lost(ts, cuda_device, prefix, new, where, kernel, dtype, e4m3):
+    """The scores of the first 700 tokens lie hundreds below the others, so that whole pieces, splits and slices
+    weigh 0 in 32 bits; a NaN that a row sees among them makes the row (K) or its column (V) NaN all the same."""
+    p = make(cuda_device, prefix, new, 8, 1, 128, dtype, e4m3, seed=151)
+    p.q[:] = p.q.abs() + 0.1
+    for b, S in enumerate(prefix):
+        t = torch.arange(min(700, S), device=cuda_device)
+        page, at = p.page_table[b].long()[t // 16], t % 16
+        if e4m3:
+            p.k_pages.view(torch.uint8)[page, at] = 0xe0       # -32
+            p.k_scales[page, :, at] = 1.0
+        else:
+            p.k_pages[page, at] = -32.0
+    page, at = int(p.page_table[0, 0]), 10
+    if e4m3:
+        (p.k_pages if where == "k" else p.v_pages).view(torch.uint8)[page, at, 0, 77] = 0x7f
+    else:
+        (p.k_pages if where == "k" else p.v_pages)[page, at, 0, 77] = float("nan")
+    ref = causal64(p)
+    assert np.isnan(ref[0]).any()
+    got, st = attend(ts, p, ts.KERNEL_AUTO if kernel == "auto" else ts.KERNEL_SIMT)
+    assert st == 0
+    check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), 128, dtype, dtype == "bf16")
