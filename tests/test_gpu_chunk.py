@@ -1142,3 +1142,72 @@ def test_a_nan_among_tokens_of_no_weight_is_not_lost(ts, cuda_device, prefix, ne
     got, st = attend(ts, p, ts.KERNEL_AUTO if kernel == "auto" else ts.KERNEL_SIMT)
     assert st == 0
     check_attention(got, *ref, max(a + b for a, b in zip(prefix, new)), 128, dtype, dtype == "bf16")
+
+
+def test_captured_tree_step_over_8bit_pools(ts, cuda_device):
+    """Append, verification and commit of a batch of trees in one graph, replayed over other trees, lengths, values
+    and paths of the same sizes; between replays the same step runs eagerly with a workspace of its own."""
+    rng = np.random.default_rng(161)
+    B, N, hq, hkv, D = 5, 20, 16, 2, 128
+    p = make_8bit(cuda_device, [900, 30, 0, 400, 77], [N] * B, hq, hkv, D, seed=161)
+    for t in (p.k_pages, p.v_pages):
+        t.view(torch.uint8)[t.view(torch.uint8) == 0x7f] = 0
+    for t in (p.k_scales, p.v_scales):
+        t.nan_to_num_(0.01)
+    qkv = torch.randn((B * N, hq + 2 * hkv, D), device=cuda_device).to(torch.bfloat16)
+    f = (10000.0 ** (-torch.arange(0, D, 2, device=cuda_device) / D)).float()
+    offsets = ints(np.arange(B + 1) * N, cuda_device)
+    parents, pos = ints(np.zeros((B, N)), cuda_device), ints(np.zeros(B * N), cuda_device)
+    path, length, lens = ints(np.zeros((B, N)), cuda_device), ints(np.zeros(B), cuda_device), ints(np.zeros(B), cuda_device)
+    q = torch.empty((B * N, hq, D), dtype=torch.bfloat16, device=cuda_device)
+    out = torch.empty((B, N, hq, D), dtype=torch.bfloat16, device=cuda_device)
+    size = ts.attn_e4m3_workspace_bytes(ts.attn_problem(out, p.k_pages, p.page_table))
+    spaces = [torch.empty(size, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+
+    def step(ws):
+        ts.tree_chunk_append(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], p.k_pages, p.v_pages, p.page_table,
+                             p.prefix_lens, offsets, q, positions=pos, inv_freq=f, workspace=ws, **p.scales())
+        ts.tree_attn_verify_e4m3(q.view(B, N, hq, D), p.k_pages, p.v_pages, p.k_scales, p.v_scales, p.page_table,
+                                 p.prefix_lens, parents, out, workspace=ws)
+        ts.tree_kv_commit_e4m3(p.k_pages, p.v_pages, p.k_scales, p.v_scales, p.page_table, p.prefix_lens, path, length, lens,
+                               workspace=ws)
+
+    def fill():
+        sizes = [int(n) for n in rng.integers(1, N + 1, B)]
+        tree = trees.padded([trees.random_recursive(rng, n) for n in sizes], N)
+        depth, way, steps = np.full((B, N), -1), np.full((B, N), -1), []
+        prefix = [int(rng.integers(0, m + 1)) for m in (900, 30, 0, 400, 77)]
+        for b, n in enumerate(sizes):
+            for i in range(n):
+                depth[b, i] = prefix[b] if i == 0 else depth[b, tree[b, i]] + 1
+            chain, node = [], int(rng.integers(n))
+            while node > 0:
+                chain.append(node)
+                node = int(tree[b, node])
+            way[b, :len(chain)] = chain[::-1]
+            steps.append(len(chain))
+        for t, a in ((parents, tree), (pos, depth.reshape(-1)), (path, way), (length, steps), (p.prefix_lens, prefix)):
+            t.copy_(ints(a, cuda_device))
+        qkv.normal_()
+
+    state = lambda: [t.clone() for t in (p.k_pages.view(torch.uint8), p.v_pages.view(torch.uint8), p.k_scales, p.v_scales)]  # noqa: E731
+    fill()
+    step(spaces[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(spaces[0])
+    for _ in range(4):
+        fill()
+        before = state()
+        g.replay()
+        torch.cuda.synchronize()
+        assert ts.read_status(spaces[0]) == 0
+        by_graph = [out.clone(), lens.clone(), *state()]
+        for t, old in zip((p.k_pages.view(torch.uint8), p.v_pages.view(torch.uint8), p.k_scales, p.v_scales), before):
+            t.copy_(old)
+        out.fill_(float("nan"))
+        step(spaces[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip([out, lens, *state()], by_graph))
+        assert torch.isfinite(out).all()
