@@ -96,7 +96,7 @@ struct Cfg {
     static constexpr int kOffMisc = kOffBar + int(sizeof(Bars));
     static constexpr int kOffEnds = kOffMisc + 16;        // the two ends of the CTA's range
     static constexpr int kOffWarp = kOffEnds + 3 * 16;    // scratch of the scan
-    static constexpr int kOffTiles = kOffWarp + 16 * 16;  // [kChunkMaxBatch + 1] tiles before a sequence, one kv head
+    static constexpr int kOffTiles = kOffWarp + 16 * 24;  // [kChunkMaxBatch + 1] tiles before a sequence, one kv head
     static constexpr int kOffUnits = kOffTiles + (kChunkMaxBatch + 1) * 8;   // and units
     static constexpr int kSmemBytes = kOffUnits + (kChunkMaxBatch + 1) * 4;
     static_assert(kSmemBytes <= 232448, "shared memory budget");
@@ -951,15 +951,18 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
 
     // ---- the sequences' tiles and units, and this CTA's range
     {
-        long long* wt = reinterpret_cast<long long*>(sm + C::kOffWarp);   // [16 warps] {tiles, units}
+        long long* wt = reinterpret_cast<long long*>(sm + C::kOffWarp);   // [16 warps] {tiles, units, rows}
         const int per = (p.B + C::kThreads - 1) / C::kThreads;
         const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
         long long nt = 0;
-        int nu = 0, top = 0;
+        int nu = 0, top = 0, rows_lo = 0, rows_hi = 0;     // rows in 16-bit halves: sums of 96 sequences fit
         bool bad = false;
         for (int b = b0; b < b1; ++b) {
-            const SeqUnits u = seq_units(p, seq_rows(p, b));
+            const SeqRows r = seq_rows(p, b);
+            const SeqUnits u = seq_units(p, r);
             bad |= !seq_ok(p, b);
+            rows_lo += r.n & 0xffff;
+            rows_hi += r.n >> 16;
             tiles_s[b] = nt;                               // relative to the thread's first
             units_s[b] = nu;
             nt += u.np == 1 ? u.tiles(0) : u.tiles_before(u.np);
@@ -979,25 +982,30 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             }
         }
         if (lane == 31) {
-            wt[2 * warp] = it;
-            wt[2 * warp + 1] = iu;
+            wt[3 * warp] = it;
+            wt[3 * warp + 1] = iu;
         }
+        const long long warp_rows = (long long)__reduce_add_sync(0xffffffffu, rows_hi) * 65536 +
+                                    __reduce_add_sync(0xffffffffu, rows_lo);
+        if (lane == 0) wt[3 * warp + 2] = warp_rows;
         __syncthreads();
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) atomicMax(longest, top);
-        long long bt = it - nt;
-        int bu = iu - nu;
+        long long bt = it - nt, bu = iu - nu, rows = warp_rows;   // a warp's units fit 31 bits
         for (int w = 0; w < warp; ++w) {
-            bt += wt[2 * w];
-            bu += int(wt[2 * w + 1]);
+            bt += wt[3 * w];
+            bu += wt[3 * w + 1];
+            rows += wt[3 * w + 2];
         }
         for (int b = b0; b < b1; ++b) {
             tiles_s[b] += bt;
-            units_s[b] += bu;
+            units_s[b] += int(bu);
         }
         if (tid == C::kThreads - 1) {
-            tiles_s[p.B] = bt + nt;
-            units_s[p.B] = bu + nu;
+            // Sequences that share rows (offsets out of order) may have more units than 32 bits count:
+            // no row is computed then
+            tiles_s[p.B] = rows > p.T ? 0 : bt + nt;
+            units_s[p.B] = rows > p.T ? 0 : int(bu + nu);
         }
         __syncthreads();
     }

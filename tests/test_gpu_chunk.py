@@ -1211,3 +1211,21 @@ def test_captured_tree_step_over_8bit_pools(ts, cuda_device):
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip([out, lens, *state()], by_graph))
         assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("kernel", ["tc", "simt"])
+def test_offsets_that_give_rows_to_two_sequences(ts, cuda_device, kernel, e4m3):
+    """0, 64, 0, 64, ...: every second sequence owns all rows.  The call is flagged and touches nothing but the rows;
+    the tensor-core form, whose sums over the sequences could not hold such counts, computes none."""
+    p = make(cuda_device, [40] * 300, [1] * 300, 8, 2, 128, "bf16", e4m3, seed=171, extra_pages=5)
+    p.q = torch.randn((64, 8, 128), device=cuda_device).to(torch.bfloat16)
+    p.chunk_offsets[0::2] = 0
+    p.chunk_offsets[1::2] = 64
+    room = torch.full((64 + 32, 8, 128), 3.0, dtype=torch.bfloat16, device=cuda_device)
+    k = ts.KERNEL_TC_STREAM if kernel == "tc" else ts.KERNEL_SIMT
+    _, st = attend(ts, p, k, out=room[16:80])
+    assert st & BAD_LENGTH
+    assert (room[:16] == 3.0).all() and (room[80:] == 3.0).all()
+    if kernel == "tc":
+        assert (room == 3.0).all()
