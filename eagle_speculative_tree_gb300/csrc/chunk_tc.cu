@@ -29,8 +29,8 @@
 //
 // A value that a row may not see must not reach it.  S is masked by selection, but P V
 // multiplies a masked token's V by zero, and 0 x NaN is NaN.  A row whose O comes out
-// non-finite is therefore recomputed from the visible tokens alone, on CUDA cores: rare and
-// slow, and no cost to the others but a test in the epilogue.  It is done behind the CTA's last
+// non-finite, and does not see what makes it so, is therefore recomputed from the visible tokens
+// alone, on CUDA cores: rare and slow, and no cost to the others but a test in the epilogue.  It is done behind the CTA's last
 // segment, where no hand-off of the pipeline, whose waits are bounded, depends on its time.
 //
 // Every mbarrier wait is bounded; on expiry the CTA records TREESPEC_STATUS_TIMEOUT, drains
@@ -112,7 +112,8 @@ __device__ __forceinline__ long long div_pos(long long a, long long b) {
     return a / b;
 }
 
-// sum over i = 0 .. n - 1 of floor((a i + b) / m); all terms and the sum within 32 bits / 64 bits
+// sum over i = 0 .. n - 1 of floor((a i + b) / m), by the Euclidean reduction of (a, m) that counts the
+// lattice points under a line; all terms and the sum within 32 bits / 64 bits
 __device__ __forceinline__ long long floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
     long long ans = 0;
     while (n) {

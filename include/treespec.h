@@ -379,7 +379,8 @@ int tree_rerank_pool(const int32_t *node_parent, const int32_t *node_token, cons
  * chunk_offsets has batch + 1 entries that do not decrease and lie in [0, num_tokens];
  * rows before the first and behind the last sequence belong to none and are left alone.
  * Offsets out of order or range set BAD_LENGTH: a sequence with such offsets has no rows,
- * and those of others may be left out too; nothing outside the call's buffers is touched.
+ * and those of others may be left out too (all, where sequences come to share rows); nothing
+ * outside the call's buffers is touched.
  *
  * A workspace serves one call at a time: calls that may run at the same time (on two
  * streams, or as two graphs in flight) need one each.
@@ -449,11 +450,12 @@ size_t treespec_append_workspace_bytes(void);
  *      no other overlap is allowed.
  *   k_pages, v_pages in shape->kv_dtype, written in place; k_scales, v_scales NULL unless
  *      8-bit.
- * A row with a negative position is padding: nothing of it is read or written.  A row
- * whose slot lies outside its page table (BAD_LENGTH) or whose page lies outside the pool
- * (BAD_PAGE) is left out in the same way.  New tokens of two sequences must not share a
- * slot: what it holds afterwards is not defined.  (Pages that hold cached tokens may be
- * shared by any number of sequences, here and in the attention calls.)
+ * A row with a negative position is padding: what it holds does not matter (its inputs are
+ * loaded all the same) and nothing of it is written.  A row whose slot lies outside its
+ * page table (BAD_LENGTH) or whose page lies outside the pool (BAD_PAGE) is left out in the
+ * same way.  New tokens of two sequences must not share a slot: what it holds afterwards is
+ * not defined.  (Pages that hold cached tokens may be shared by any number of sequences,
+ * here and in the attention calls.)
  */
 int tree_chunk_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                       int64_t v_stride, void *q_out, void *k_pages, void *v_pages, float *k_scales, float *v_scales,
@@ -475,7 +477,11 @@ size_t treespec_chunk_attn_workspace_bytes(const treespec_chunk_shape *shape);
  *   q, out [T][Hq][D] contiguous, in shape->dtype; out overlaps nothing else.  Pools and
  *   scales as above.
  * Tokens that a row may not see, and slots behind a sequence's last token, do not reach
- * the row's result, whatever they hold (NaN and infinities included).
+ * the row's result, whatever they hold (NaN and infinities included).  On tensor cores a
+ * row is recomputed where that takes it: rows of the 2 floor(128 / G) tokens around a hidden
+ * NaN, about 1 us per row and token of context, some hundreds of rows at a time.  A score of
+ * -inf weighs 0; a NaN in K that a row sees makes the row NaN, a NaN or an infinity in V its
+ * own element (a NaN where the weight of an infinity is below 2^-126).
  * The rows of a sequence with prefix_len < 0 or prefix_len + n_b > max_pages * 16 are
  * zeros (BAD_LENGTH).  A page id outside the pool sets BAD_PAGE; its tokens count as zeros.
  * All tensors 16-byte aligned.  Results do not depend on timing: the same call gives the

@@ -173,6 +173,8 @@ def causal64(p):
     parts = []
     offsets = p.chunk_offsets.tolist()
     for b, (S, n) in enumerate(zip(p.prefix, p.new)):
+        if n == 0:
+            continue
         t = torch.arange(S + n, device=p.q.device)
         i = torch.arange(n, device=p.q.device)
         parts.append(attend64(p, p.q[offsets[b]:offsets[b] + n], b, t[None] <= S + i[:, None]))
