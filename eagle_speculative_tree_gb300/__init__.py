@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import re
 from dataclasses import dataclass
@@ -99,6 +100,25 @@ _lib.tree_attn_verify_e4m3.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnShape), _v
 _lib.tree_attn_verify_e4m3.restype = ctypes.c_int
 _lib.tree_kv_commit_e4m3.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnShape), _vp, ctypes.c_size_t, _vp]
 _lib.tree_kv_commit_e4m3.restype = ctypes.c_int
+_lib.treespec_chunk_window_workspace_bytes.argtypes = [ctypes.POINTER(ChunkShape)] + [ctypes.c_int32] * 2
+_lib.treespec_chunk_window_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_chunk_attn_window.argtypes = [_vp] * 9 + [ctypes.POINTER(ChunkShape)] + [ctypes.c_int32] * 2 + \
+    [_vp, ctypes.c_size_t, _vp]
+_lib.tree_chunk_attn_window.restype = ctypes.c_int
+_lib.treespec_attn_window_workspace_bytes.argtypes = [ctypes.POINTER(AttnShape)] + [ctypes.c_int32] * 3
+_lib.treespec_attn_window_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_attn_verify_window.argtypes = [_vp] * 9 + [ctypes.POINTER(AttnShape)] + [ctypes.c_int32] * 3 + \
+    [_vp, ctypes.c_size_t, _vp]
+_lib.tree_attn_verify_window.restype = ctypes.c_int
+_lib.treespec_chunk_shared_workspace_bytes.argtypes = [ctypes.POINTER(ChunkShape), ctypes.c_int32]
+_lib.treespec_chunk_shared_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_chunk_attn_shared.argtypes = [_vp] * 11 + [ctypes.POINTER(ChunkShape), ctypes.c_int32, _vp, ctypes.c_size_t, _vp]
+_lib.tree_chunk_attn_shared.restype = ctypes.c_int
+_lib.treespec_attn_shared_workspace_bytes.argtypes = [ctypes.POINTER(AttnShape)] + [ctypes.c_int32] * 2
+_lib.treespec_attn_shared_workspace_bytes.restype = ctypes.c_size_t
+_lib.tree_attn_verify_shared.argtypes = [_vp] * 11 + [ctypes.POINTER(AttnShape)] + [ctypes.c_int32] * 2 + \
+    [_vp, ctypes.c_size_t, _vp]
+_lib.tree_attn_verify_shared.restype = ctypes.c_int
 _lib.treespec_read_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.treespec_read_status.restype = ctypes.c_int
 _lib.treespec_error_string.argtypes = [ctypes.c_int]
@@ -615,6 +635,35 @@ def chunk_attn_workspace_bytes(prob: ChunkProblem) -> int:
     return int(n)
 
 
+def _attend_chunks(fn, need, q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales,
+                   kernel, workspace, stream, groups=(), more=()) -> torch.Tensor:
+    """An attention call over packed chunks: `need` gives the workspace bytes of a problem, `groups`
+    are (group_offsets, shared_lens), `more` the call's whole numbers behind the shape."""
+    dt = getattr(q, "dtype", None)
+    if dt is not _BF16 and dt is not _F32:
+        raise _float_type_error(q)
+    index = _index_of(q, "q")
+    sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel)
+    B = sizes[0]
+    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
+             (page_table, "page_table", _I32, (B, sizes[6])), (prefix_lens, "prefix_lens", _I32, (B,)),
+             (chunk_offsets, "chunk_offsets", _I32, (B + 1,))]
+    if groups:
+        wants += _group_wants(*groups)
+    if out is None:
+        out = _fresh(q.shape, dt, q.device, stream)
+    else:
+        wants.append((out, "out", dt, q.shape))
+    _need_all(index, *wants)
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, need(ChunkProblem(*sizes)), index, q.device, stream)
+    _launch(index, stream, fn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
+            _ptr(v_scales), page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(),
+            *[t.data_ptr() for t in groups], out.data_ptr(), _chunk_struct(*sizes), *more, workspace.data_ptr(),
+            workspace.nbytes)
+    return out
+
+
 def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, out=None, *, k_scales=None,
                     v_scales=None, kernel: int = KERNEL_AUTO, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
@@ -626,26 +675,8 @@ def tree_chunk_attn(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets,
     prefix_lens [B], chunk_offsets [B + 1] int32.  Returns out [T][Hq][D] in q's dtype; rows
     that belong to no sequence are left as they are in `out` (and hold nothing of use in a
     new one)."""
-    dt = getattr(q, "dtype", None)
-    if dt is not _BF16 and dt is not _F32:
-        raise _float_type_error(q)
-    index = _index_of(q, "q")
-    sizes = _chunk_sizes(q, k_pages, page_table, chunk_offsets, kernel)
-    B = sizes[0]
-    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
-             (page_table, "page_table", _I32, (B, sizes[6])), (prefix_lens, "prefix_lens", _I32, (B,)),
-             (chunk_offsets, "chunk_offsets", _I32, (B + 1,))]
-    if out is None:
-        out = _fresh(q.shape, dt, q.device, stream)
-    else:
-        wants.append((out, "out", dt, q.shape))
-    _need_all(index, *wants)
-    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        workspace = _workspace_for(workspace, chunk_attn_workspace_bytes(ChunkProblem(*sizes)), index, q.device, stream)
-    _launch(index, stream, _lib.tree_chunk_attn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
-            _ptr(v_scales), page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(), out.data_ptr(),
-            _chunk_struct(*sizes), workspace.data_ptr(), workspace.nbytes)
-    return out
+    return _attend_chunks(_lib.tree_chunk_attn, chunk_attn_workspace_bytes, q, k_pages, v_pages, page_table, prefix_lens,
+                          chunk_offsets, out, k_scales, v_scales, kernel, workspace, stream)
 
 
 def attn_e4m3_workspace_bytes(prob: AttnProblem) -> int:
@@ -653,6 +684,42 @@ def attn_e4m3_workspace_bytes(prob: AttnProblem) -> int:
     if n == 0:
         raise ValueError(f"unsupported attention shape {prob}")
     return int(n)
+
+
+def _attend_trees(fn, need, q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel,
+                  workspace, stream, groups=(), more=()) -> torch.Tensor:
+    """A verification call over any pools; arguments as for _attend_chunks."""
+    dt = getattr(q, "dtype", None)
+    if dt is not _BF16 and dt is not _F32:
+        raise _float_type_error(q)
+    index = _index_of(q, "q")
+    if not isinstance(k_pages, torch.Tensor) or not isinstance(page_table, torch.Tensor) or q.dim() != 4 or \
+            page_table.dim() != 2:
+        _need_tensors(k_pages=k_pages, page_table=page_table)
+        raise ValueError("q is [batch][nodes][heads][head_dim], page_table [batch][pages]")
+    B, N, Hq, D = q.shape
+    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
+             (page_table, "page_table", _I32, (B, page_table.shape[1])), (prefix_lens, "prefix_lens", _I32, (B,)),
+             (tree_parents, "tree_parents", _I32, (B, N))]
+    if groups:
+        wants += _group_wants(*groups)
+    if out is None:
+        out = _fresh(q.shape, dt, q.device, stream)
+    else:
+        wants.append((out, "out", dt, q.shape))
+    _need_all(index, *wants)
+    P, ps, Hkv, D2 = k_pages.shape
+    if D2 != D:
+        raise ValueError("head_dim of q and k_pages differ")
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        workspace = _workspace_for(workspace, need(attn_problem(q, k_pages, page_table, kernel=kernel)), index, q.device,
+                                   stream)
+    _launch(index, stream, fn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
+            page_table.data_ptr(), prefix_lens.data_ptr(), tree_parents.data_ptr(), *[t.data_ptr() for t in groups],
+            out.data_ptr(), _attn_struct(B, N, Hq, Hkv, D, ps, page_table.shape[1], P,
+                                         DTYPE_BF16 if dt is _BF16 else DTYPE_F32, kernel, 0),
+            *more, workspace.data_ptr(), workspace.nbytes)
+    return out
 
 
 def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out=None, *,
@@ -666,33 +733,11 @@ def tree_attn_verify_e4m3(q, k_pages, v_pages, k_scales, v_scales, page_table, p
     dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
         raise _float_type_error(q)
-    index = _index_of(q, "q")
+    _index_of(q, "q")
     if getattr(k_pages, "dtype", None) is not _E4M3:
         raise _code_type_error(k_pages)
-    if not isinstance(page_table, torch.Tensor) or q.dim() != 4 or page_table.dim() != 2:
-        _need_tensors(page_table=page_table)
-        raise ValueError("q is [batch][nodes][heads][head_dim], page_table [batch][pages]")
-    B, N, Hq, D = q.shape
-    wants = [(q, "q", dt, q.shape), *_pool_wants(dt, k_pages, v_pages, k_scales, v_scales),
-             (page_table, "page_table", _I32, (B, page_table.shape[1])), (prefix_lens, "prefix_lens", _I32, (B,)),
-             (tree_parents, "tree_parents", _I32, (B, N))]
-    if out is None:
-        out = _fresh(q.shape, dt, q.device, stream)
-    else:
-        wants.append((out, "out", dt, q.shape))
-    _need_all(index, *wants)
-    P, ps, Hkv, D2 = k_pages.shape
-    if D2 != D:
-        raise ValueError("head_dim of q and k_pages differ")
-    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        workspace = _workspace_for(workspace, attn_e4m3_workspace_bytes(attn_problem(q, k_pages, page_table, kernel=kernel)),
-                                   index, q.device, stream)
-    _launch(index, stream, _lib.tree_attn_verify_e4m3, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            k_scales.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), prefix_lens.data_ptr(), tree_parents.data_ptr(),
-            out.data_ptr(), _attn_struct(B, N, Hq, Hkv, D, ps, page_table.shape[1], P,
-                                         DTYPE_BF16 if dt is _BF16 else DTYPE_F32, kernel, 0),
-            workspace.data_ptr(), workspace.nbytes)
-    return out
+    return _attend_trees(_lib.tree_attn_verify_e4m3, attn_e4m3_workspace_bytes, q, k_pages, v_pages, k_scales, v_scales,
+                         page_table, prefix_lens, tree_parents, out, kernel, workspace, stream)
 
 
 def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, accept_path, accept_len,
@@ -725,6 +770,112 @@ def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix
             _attn_struct(B, N, Hkv, Hkv, D, ps, page_table.shape[1], P, DTYPE_BF16, KERNEL_AUTO, 0),
             workspace.data_ptr(), workspace.nbytes)
     return new_prefix_lens
+
+
+# --------------------------------------------- sliding windows and shared prefixes
+
+def _group_wants(group_offsets, shared_lens) -> tuple:
+    _need_tensors(group_offsets=group_offsets, shared_lens=shared_lens)
+    if shared_lens.dim() != 1 or shared_lens.shape[0] < 1:
+        raise ValueError("shared_lens must have shape [groups], with one group at least")
+    return ((group_offsets, "group_offsets", _I32, (shared_lens.shape[0] + 1,)),
+            (shared_lens, "shared_lens", _I32, shared_lens.shape))
+
+
+def _window_of(window, sinks) -> tuple:
+    """window >= 1 and sinks >= 0 as the C calls take them: 2^30 reaches every token."""
+    window, sinks = operator.index(window), operator.index(sinks)
+    if window < 1:
+        raise ValueError(f"window must be at least 1, got {window}")
+    if sinks < 0:
+        raise ValueError(f"sinks must not be negative, got {sinks}")
+    return min(window, 1 << 30), min(sinks, 1 << 30)
+
+
+def _kv_dtype(q, k_pages) -> int:
+    return DTYPE_E4M3 if getattr(k_pages, "dtype", None) is _E4M3 else DTYPE_BF16 if getattr(q, "dtype", None) is _BF16 \
+        else DTYPE_F32
+
+
+def _bytes_or_error(n: int, prob, *more) -> int:
+    if n == 0:
+        raise ValueError(f"unsupported attention shape {prob} {more}")
+    return int(n)
+
+
+def chunk_window_workspace_bytes(prob: ChunkProblem, window: int, sinks: int = 0) -> int:
+    w = _window_of(window, sinks)
+    return _bytes_or_error(_lib.treespec_chunk_window_workspace_bytes(prob.c_shape(), *w), prob, *w)
+
+
+def attn_window_workspace_bytes(prob: AttnProblem, kv_dtype: int, window: int, sinks: int = 0) -> int:
+    w = _window_of(window, sinks)
+    return _bytes_or_error(_lib.treespec_attn_window_workspace_bytes(prob.c_shape(), kv_dtype, *w), prob, kv_dtype, *w)
+
+
+def chunk_shared_workspace_bytes(prob: ChunkProblem, num_groups: int) -> int:
+    return _bytes_or_error(_lib.treespec_chunk_shared_workspace_bytes(prob.c_shape(), num_groups), prob, num_groups)
+
+
+def attn_shared_workspace_bytes(prob: AttnProblem, kv_dtype: int, num_groups: int) -> int:
+    return _bytes_or_error(_lib.treespec_attn_shared_workspace_bytes(prob.c_shape(), kv_dtype, num_groups), prob, kv_dtype,
+                           num_groups)
+
+
+def tree_chunk_attn_window(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, window: int, sinks: int = 0,
+                           out=None, *, k_scales=None, v_scales=None, kernel: int = KERNEL_AUTO,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tree_chunk_attn where a row sees itself, the window - 1 tokens before it and the sequence's
+    first `sinks` tokens; see include/treespec.h.  Pages that no row sees are not read, and their
+    entries in page_table may hold anything."""
+    w = _window_of(window, sinks)
+    return _attend_chunks(_lib.tree_chunk_attn_window, lambda prob: chunk_window_workspace_bytes(prob, *w), q, k_pages,
+                          v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace,
+                          stream, (), w)
+
+
+def tree_attn_verify_window(q, k_pages, v_pages, page_table, prefix_lens, tree_parents, window: int, sinks: int = 0,
+                            out=None, *, k_scales=None, v_scales=None, kernel: int = KERNEL_AUTO,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tree verification where a node sees, of its prefix and its ancestors, those fewer than
+    `window` positions before it and those at the first `sinks` positions; a node's position is
+    the prefix length plus its depth.  See include/treespec.h.
+
+    q [B][N][Hq][D], k_pages / v_pages in the same type or float8_e4m3fn with k_scales /
+    v_scales, the rest as for tree_attn_verify."""
+    w = _window_of(window, sinks)
+    kv = _kv_dtype(q, k_pages)
+    return _attend_trees(_lib.tree_attn_verify_window, lambda prob: attn_window_workspace_bytes(prob, kv, *w), q, k_pages,
+                         v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel, workspace, stream,
+                         (), (kv, *w))
+
+
+def tree_chunk_attn_shared(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, group_offsets, shared_lens,
+                           out=None, *, k_scales=None, v_scales=None, kernel: int = KERNEL_AUTO,
+                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tree_chunk_attn of a batch whose sequences share prefixes, each read and multiplied once: the
+    sequences group_offsets[g] .. group_offsets[g + 1] - 1 have their first shared_lens[g] tokens
+    in common.  group_offsets [groups + 1] and shared_lens [groups] int32 on the device; see
+    include/treespec.h."""
+    groups = (group_offsets, shared_lens)
+    _group_wants(*groups)
+    n = shared_lens.shape[0]
+    return _attend_chunks(_lib.tree_chunk_attn_shared, lambda prob: chunk_shared_workspace_bytes(prob, n), q, k_pages,
+                          v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace,
+                          stream, groups, (n,))
+
+
+def tree_attn_verify_shared(q, k_pages, v_pages, page_table, prefix_lens, tree_parents, group_offsets, shared_lens,
+                            out=None, *, k_scales=None, v_scales=None, kernel: int = KERNEL_AUTO,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tree verification of a batch whose sequences share prefixes; groups as for
+    tree_chunk_attn_shared, pools as for tree_attn_verify_window.  See include/treespec.h."""
+    groups = (group_offsets, shared_lens)
+    _group_wants(*groups)
+    n, kv = shared_lens.shape[0], _kv_dtype(q, k_pages)
+    return _attend_trees(_lib.tree_attn_verify_shared, lambda prob: attn_shared_workspace_bytes(prob, kv, n), q, k_pages,
+                         v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel, workspace, stream,
+                         groups, (kv, n))
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

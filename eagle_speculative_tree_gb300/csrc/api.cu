@@ -497,10 +497,18 @@ struct ChunkPlan {
     int kernel, num_splits, split_tokens, rows_block, ctas;
 };
 
-// rows: query rows per kv head of the whole batch.  The lengths are on the device, so the
-// plan goes by the page table's width and the mean rows of a sequence.
+// What a call adds to plain causal or tree attention.
+struct ChunkExtra {
+    ChunkMode mode = kChunkPlain;
+    int window = 0, sinks = 0;                           // kChunkWindow
+    int groups = 0;                                      // kChunkShared
+};
+
+// rows: query rows per kv head of the whole batch; tokens: how many a row block may run over.  The
+// lengths are on the device, so the plan goes by the page table's width (or the window's) and the
+// mean rows of a sequence.
 ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long long rows, int Hkv, int D,
-                     int max_pages, int pool_pages, int sms) {
+                     long long tokens, int pool_pages, int sms) {
     ChunkPlan c{};
     if (kernel != TREESPEC_KERNEL_SIMT && chunk_tc_supported(dtype, int(batch), (long long)pool_pages * kPage)) {
         c.kernel = TREESPEC_KERNEL_TC_STREAM;
@@ -515,7 +523,6 @@ ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long 
     // (5 sequences of up to 130 tokens x 4 heads over up to 830 tokens of 64, float32: 59 us
     // with blocks of 64 rows in splits of 256 tokens, 27 us with this rule).
     const long long mean = (rows + batch - 1) / batch;
-    const long long tokens = (long long)max_pages * kPage;
     long long splits = 1;
     // No block smaller than leaves its CTA 8 warps: they share the loads even where only some
     // hold rows.
@@ -536,66 +543,109 @@ ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long 
     return c;
 }
 
-ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long long tree_rows, long long batch) {
+ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long long tree_rows, long long batch,
+                         const ChunkExtra& x) {
     ChunkLayout L{};
     size_t off = 0;
-    L.status = off;                                      // and the persistent kernel's counters behind it
-    off += kWsAlign;
-    off = align_up(off + size_t(c.ctas) * 8 * 4, kWsAlign);
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, kWsAlign);
+        return at;
+    };
+    L.status = take(kWsAlign + size_t(c.ctas) * 8 * 4);  // and the persistent kernel's counters behind it
     L.cleared = off;
-    L.anc = off;
-    off = align_up(off + size_t(tree_rows) * kAncWords * 8, kWsAlign);
-    L.lens = off;
-    off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
-    L.nn = off;
-    off = align_up(off + (tree_rows ? size_t(batch) * 4 : 0), kWsAlign);
-    // SIMT: a row of each split; persistent: two slots of two tiles per CTA
-    const size_t parts = c.ctas ? size_t(2) * c.ctas * 256 : c.num_splits > 1 ? size_t(c.num_splits) * T * Hq : 0;
-    L.ml = off;
-    off = align_up(off + parts * 2 * 4, kWsAlign);
-    L.acc = off;
-    off = align_up(off + parts * D * 4, kWsAlign);
+    L.anc = take(size_t(tree_rows) * kAncWords * 8);
+    L.lens = take(tree_rows ? size_t(batch) * 4 : 0);
+    L.nn = take(tree_rows ? size_t(batch) * 4 : 0);
+    L.depth = take(x.mode == kChunkWindow ? size_t(tree_rows) * 4 : 0);
+    L.gtab = take(size_t(x.groups) * 16);
+    L.skip = take(x.groups ? size_t(batch) * 4 : 0);
+    // SIMT: a row of each split, and of each split of its group's; persistent: two slots of two tiles per CTA
+    const bool shared = x.mode == kChunkShared;
+    const size_t rows = size_t(T) * Hq * (shared ? 2 : 1);
+    const size_t parts = c.ctas ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
+    L.ml = take(parts * 2 * 4);
+    L.acc = take(parts * D * 4);
     L.total = off;
     return L;
 }
 
-ChunkPlan plan_of(const treespec_chunk_shape& s) {
-    return chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch, (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads),
-                      s.num_kv_heads, s.head_dim, s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
+// The most tokens that one row block of a windowed call runs over: the sinks and the window of its
+// first row, both to a page's border, and the rows' own tokens behind that.
+long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
+    if (x.mode != kChunkWindow) return tokens;
+    return std::min(tokens, (long long)x.window + x.sinks + 2 * kPage + std::max(kSharedTile, tree_nodes));
 }
-ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c) {
-    return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch);
+ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
+    return chunk_plan(x.mode == kChunkPlain ? s.kernel : TREESPEC_KERNEL_SIMT, s.dtype, s.kv_dtype, s.batch + x.groups,
+                      (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
+                      window_span((long long)s.max_pages_per_seq * kPage, x, 0), s.num_pool_pages, sm_count_or_default());
+}
+ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c, const ChunkExtra& x = {}) {
+    return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch, x);
 }
 
-int check_e4m3_verify_shape(const treespec_attn_shape* s) {
+int check_extra(const ChunkExtra& x) {
+    if (x.mode == kChunkWindow && (x.window < 1 || x.sinks < 0)) return TREESPEC_ERR_SHAPE;
+    if (x.mode == kChunkShared && (x.groups < 1 || x.groups > kMaxGroups)) return TREESPEC_ERR_SHAPE;
+    return TREESPEC_OK;
+}
+// A window or sinks beyond every sequence's length are all of it: lengths stay below 2^30.
+ChunkExtra window_of(int window, int sinks) {
+    ChunkExtra x;
+    x.mode = kChunkWindow;
+    x.window = std::min(window, 1 << 30);
+    x.sinks = std::min(sinks, 1 << 30);
+    return x;
+}
+ChunkExtra groups_of(int groups) {
+    ChunkExtra x;
+    x.mode = kChunkShared;
+    x.groups = groups;
+    return x;
+}
+
+int check_chunk_call(const treespec_chunk_shape* s, const ChunkExtra& x) {
+    const int rc = check_chunk_shape(s, true);
+    if (rc != TREESPEC_OK) return rc;
+    if (const int rx = check_extra(x); rx != TREESPEC_OK) return rx;
+    if (x.groups && s->kernel == TREESPEC_KERNEL_TC_STREAM &&
+        !chunk_tc_supported(s->dtype, s->batch + x.groups, (long long)s->num_pool_pages * kPage))
+        return TREESPEC_ERR_SHAPE;
+    return TREESPEC_OK;
+}
+
+int check_tree_call(const treespec_attn_shape* s, int kv_dtype, const ChunkExtra& x) {
     if (!s) return TREESPEC_ERR_NULL_POINTER;
     treespec_attn_shape t = *s;
     if (t.kernel != TREESPEC_KERNEL_AUTO && t.kernel != TREESPEC_KERNEL_SIMT && t.kernel != TREESPEC_KERNEL_TC_STREAM)
         return TREESPEC_ERR_SHAPE;
     if (t.kernel == TREESPEC_KERNEL_TC_STREAM) {
         if (t.dtype != TREESPEC_DTYPE_BF16) return TREESPEC_ERR_DTYPE;
-        if (!chunk_tc_supported(t.dtype, t.batch, (long long)t.num_pool_pages * kPage)) return TREESPEC_ERR_SHAPE;
+        if (!chunk_tc_supported(t.dtype, t.batch + x.groups, (long long)t.num_pool_pages * kPage)) return TREESPEC_ERR_SHAPE;
     }
     t.kernel = TREESPEC_KERNEL_SIMT;                     // the limits of the tensor-core kernels are checked by the plan
     const int rc = check_attn_shape(&t);
     if (rc != TREESPEC_OK) return rc;
+    if (kv_dtype != t.dtype && kv_dtype != TREESPEC_DTYPE_E4M3) return TREESPEC_ERR_DTYPE;
     if (t.num_q_heads / t.num_kv_heads > 128) return TREESPEC_ERR_SHAPE;
     if ((long long)t.batch * t.num_nodes * t.num_q_heads >= (1ll << 31)) return TREESPEC_ERR_SHAPE;
-    return TREESPEC_OK;
+    return check_extra(x);
 }
-ChunkPlan plan_of(const treespec_attn_shape& s) {
-    return chunk_plan(s.kernel, s.dtype, TREESPEC_DTYPE_E4M3, s.batch,
+ChunkPlan plan_of(const treespec_attn_shape& s, int kv_dtype, const ChunkExtra& x) {
+    return chunk_plan(x.mode == kChunkPlain ? s.kernel : TREESPEC_KERNEL_SIMT, s.dtype, kv_dtype, s.batch + x.groups,
                       (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
-                      s.max_pages_per_seq, s.num_pool_pages, sm_count_or_default());
+                      window_span((long long)s.max_pages_per_seq * kPage, x, s.num_nodes), s.num_pool_pages,
+                      sm_count_or_default());
 }
-ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c) {
+ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const ChunkExtra& x) {
     const long long rows = (long long)s.batch * s.num_nodes;
-    return chunk_layout(c, rows, s.num_q_heads, s.head_dim, rows, s.batch);
+    return chunk_layout(c, rows, s.num_q_heads, s.head_dim, rows, s.batch, x);
 }
 
-// What the two attention calls share once their arguments are checked.
-int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsigned char* ws, int dtype, int kv_dtype,
-              cudaStream_t st) {
+// What the attention calls share once their arguments are checked and the status word is cleared.
+int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const ChunkExtra& x, GroupParams g,
+              unsigned char* ws, int dtype, int kv_dtype, cudaStream_t st) {
     p.status = reinterpret_cast<uint32_t*>(ws + lay.status);
     p.counters = reinterpret_cast<int32_t*>(ws + lay.status + kWsAlign);
     p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
@@ -610,16 +660,138 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, unsign
     p.inv_g = (65536 + p.G - 1) / p.G;
     p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.D)));
     p.wait_ns = g_wait_ns.load();
-    cudaError_t e = c.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_chunk_tc(p, kv_dtype, st)
-                                                          : launch_chunk_simt(p, dtype, kv_dtype, st);
+    p.window = x.window;
+    p.sinks = x.sinks;
+    p.groups = x.groups;
+    p.gtab = g.gtab = reinterpret_cast<int4*>(ws + lay.gtab);
+    p.skip = g.skip = reinterpret_cast<int32_t*>(ws + lay.skip);
+    cudaError_t e;
+    if (x.mode == kChunkShared) {
+        e = launch_group_prologue(p, g, st);
+        if (e != cudaSuccess) return launch_failed(e);
+        g_launches++;
+    }
+    e = c.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_chunk_tc(p, kv_dtype, st)
+        : x.mode == kChunkWindow              ? launch_chunk_simt<kChunkWindow>(p, dtype, kv_dtype, st)
+        : x.mode == kChunkShared              ? launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st)
+                                              : launch_chunk_simt<kChunkPlain>(p, dtype, kv_dtype, st);
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;
-    if (c.num_splits > 1) {
-        e = launch_chunk_merge(p, dtype, st);
+    if (c.num_splits > 1 || x.mode == kChunkShared) {
+        e = launch_chunk_merge(p, x.mode, dtype, st);
         if (e != cudaSuccess) return launch_failed(e);
         g_launches++;
     }
     return TREESPEC_OK;
+}
+
+// An attention call over packed chunks, whatever its form.
+int attend_chunks(const void* q, const void* k_pages, const void* v_pages, const float* k_scales, const float* v_scales,
+                  const int32_t* page_table, const int32_t* prefix_lens, const int32_t* chunk_offsets, void* out,
+                  const treespec_chunk_shape* shape, const ChunkExtra& x, const GroupParams& g, void* workspace,
+                  size_t workspace_bytes, treespec_stream_t stream) {
+    int rc = check_chunk_call(shape, x);
+    if (rc != TREESPEC_OK) return rc;
+    if (!q || !k_pages || !v_pages || !page_table || !prefix_lens || !chunk_offsets || !out)
+        return TREESPEC_ERR_NULL_POINTER;
+    if (x.groups && (!g.group_offsets || !g.shared_lens)) return TREESPEC_ERR_NULL_POINTER;
+    const treespec_chunk_shape& s = *shape;
+    const bool q8 = s.kv_dtype == TREESPEC_DTYPE_E4M3;
+    if (q8 && (!k_scales || !v_scales)) return TREESPEC_ERR_NULL_POINTER;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        (q8 && (!aligned16(k_scales) || !aligned16(v_scales))))
+        return TREESPEC_ERR_ALIGNMENT;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
+    rc = check_device();
+    if (rc != TREESPEC_OK) return rc;
+    const ChunkPlan plan = plan_of(s, x);
+    const ChunkLayout lay = layout_of(s, plan, x);
+    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
+    ChunkParams p{};
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.k_scales = q8 ? k_scales : nullptr;
+    p.v_scales = q8 ? v_scales : nullptr;
+    p.page_table = page_table;
+    p.prefix_lens = prefix_lens;
+    p.offsets = chunk_offsets;
+    p.out = out;
+    p.B = s.batch;
+    p.T = s.num_tokens;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.D = s.head_dim;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
+    return run_chunk(p, plan, lay, x, g, ws, s.dtype, s.kv_dtype, st);
+}
+
+// A verification of trees by the same kernels, whatever its form.
+int attend_trees(const void* q, const void* k_pages, const void* v_pages, const float* k_scales, const float* v_scales,
+                 const int32_t* page_table, const int32_t* prefix_lens, const int32_t* tree_parents, void* out,
+                 const treespec_attn_shape* shape, int kv_dtype, const ChunkExtra& x, const GroupParams& g,
+                 void* workspace, size_t workspace_bytes, treespec_stream_t stream) {
+    int rc = check_tree_call(shape, kv_dtype, x);
+    if (rc != TREESPEC_OK) return rc;
+    const bool q8 = kv_dtype == TREESPEC_DTYPE_E4M3;
+    if (!q || !k_pages || !v_pages || !page_table || !prefix_lens || !tree_parents || !out || (q8 && (!k_scales || !v_scales)))
+        return TREESPEC_ERR_NULL_POINTER;
+    if (x.groups && (!g.group_offsets || !g.shared_lens)) return TREESPEC_ERR_NULL_POINTER;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+        (q8 && (!aligned16(k_scales) || !aligned16(v_scales))))
+        return TREESPEC_ERR_ALIGNMENT;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
+    rc = check_device();
+    if (rc != TREESPEC_OK) return rc;
+    const treespec_attn_shape& s = *shape;
+    const ChunkPlan plan = plan_of(s, kv_dtype, x);
+    const ChunkLayout lay = layout_of(s, plan, x);
+    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    ChunkParams p{};
+    p.q = q;
+    p.k = k_pages;
+    p.v = v_pages;
+    p.k_scales = q8 ? k_scales : nullptr;
+    p.v_scales = q8 ? v_scales : nullptr;
+    p.page_table = page_table;
+    p.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
+    p.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
+    p.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
+    p.depth = x.mode == kChunkWindow ? reinterpret_cast<int32_t*>(ws + lay.depth) : nullptr;
+    p.out = out;
+    p.B = s.batch;
+    p.T = s.batch * s.num_nodes;
+    p.N = s.num_nodes;
+    p.Hq = s.num_q_heads;
+    p.Hkv = s.num_kv_heads;
+    p.D = s.head_dim;
+    p.max_pages = s.max_pages_per_seq;
+    p.num_pool_pages = s.num_pool_pages;
+    AttnParams a{};                                      // what the tree prologue reads and writes
+    a.parents = tree_parents;
+    a.prefix_lens = prefix_lens;
+    a.status = reinterpret_cast<uint32_t*>(ws + lay.status);
+    a.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
+    a.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
+    a.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
+    a.depth = const_cast<int32_t*>(p.depth);
+    a.window = x.window;
+    a.sinks = x.sinks;
+    a.B = s.batch;
+    a.N = s.num_nodes;
+    a.max_pages = s.max_pages_per_seq;
+    a.ps = kPage;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
+    const cudaError_t e = launch_tree_prologue(a, st);
+    if (e != cudaSuccess) return launch_failed(e);
+    g_launches++;
+    return run_chunk(p, plan, lay, x, g, ws, s.dtype, kv_dtype, st);
 }
 
 }  // namespace
@@ -708,105 +880,87 @@ extern "C" int tree_chunk_attn(const void* q, const void* k_pages, const void* v
                                const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
                                const int32_t* chunk_offsets, void* out, const treespec_chunk_shape* shape,
                                void* workspace, size_t workspace_bytes, treespec_stream_t stream) {
-    int rc = check_chunk_shape(shape, true);
-    if (rc != TREESPEC_OK) return rc;
-    if (!q || !k_pages || !v_pages || !page_table || !prefix_lens || !chunk_offsets || !out)
-        return TREESPEC_ERR_NULL_POINTER;
-    const treespec_chunk_shape& s = *shape;
-    const bool q8 = s.kv_dtype == TREESPEC_DTYPE_E4M3;
-    if (q8 && (!k_scales || !v_scales)) return TREESPEC_ERR_NULL_POINTER;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
-        (q8 && (!aligned16(k_scales) || !aligned16(v_scales))))
-        return TREESPEC_ERR_ALIGNMENT;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
-    rc = check_device();
-    if (rc != TREESPEC_OK) return rc;
-    const ChunkPlan plan = plan_of(s);
-    const ChunkLayout lay = layout_of(s, plan);
-    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
-    ChunkParams p{};
-    p.q = q;
-    p.k = k_pages;
-    p.v = v_pages;
-    p.k_scales = q8 ? k_scales : nullptr;
-    p.v_scales = q8 ? v_scales : nullptr;
-    p.page_table = page_table;
-    p.prefix_lens = prefix_lens;
-    p.offsets = chunk_offsets;
-    p.out = out;
-    p.B = s.batch;
-    p.T = s.num_tokens;
-    p.Hq = s.num_q_heads;
-    p.Hkv = s.num_kv_heads;
-    p.D = s.head_dim;
-    p.max_pages = s.max_pages_per_seq;
-    p.num_pool_pages = s.num_pool_pages;
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
-    return run_chunk(p, plan, lay, ws, s.dtype, s.kv_dtype, st);
+    return attend_chunks(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, chunk_offsets, out, shape, {}, {},
+                         workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t treespec_attn_e4m3_workspace_bytes(const treespec_attn_shape* shape) {
-    if (check_e4m3_verify_shape(shape) != TREESPEC_OK) return 0;
-    return layout_of(*shape, plan_of(*shape)).total;
+    if (check_tree_call(shape, TREESPEC_DTYPE_E4M3, {}) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape, TREESPEC_DTYPE_E4M3, {}), {}).total;
 }
 
 extern "C" int tree_attn_verify_e4m3(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
                                      const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
                                      const int32_t* tree_parents, void* out, const treespec_attn_shape* shape,
                                      void* workspace, size_t workspace_bytes, treespec_stream_t stream) {
-    int rc = check_e4m3_verify_shape(shape);
-    if (rc != TREESPEC_OK) return rc;
-    if (!q || !k_pages || !v_pages || !k_scales || !v_scales || !page_table || !prefix_lens || !tree_parents || !out)
-        return TREESPEC_ERR_NULL_POINTER;
-    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(k_scales) ||
-        !aligned16(v_scales))
-        return TREESPEC_ERR_ALIGNMENT;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) % kWsAlign)) return TREESPEC_ERR_WORKSPACE;
-    rc = check_device();
-    if (rc != TREESPEC_OK) return rc;
-    const treespec_attn_shape& s = *shape;
-    const ChunkPlan plan = plan_of(s);
-    const ChunkLayout lay = layout_of(s, plan);
-    if (workspace_bytes < lay.total) return TREESPEC_ERR_WORKSPACE;
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
-    ChunkParams p{};
-    p.q = q;
-    p.k = k_pages;
-    p.v = v_pages;
-    p.k_scales = k_scales;
-    p.v_scales = v_scales;
-    p.page_table = page_table;
-    p.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
-    p.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
-    p.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
-    p.out = out;
-    p.B = s.batch;
-    p.T = s.batch * s.num_nodes;
-    p.N = s.num_nodes;
-    p.Hq = s.num_q_heads;
-    p.Hkv = s.num_kv_heads;
-    p.D = s.head_dim;
-    p.max_pages = s.max_pages_per_seq;
-    p.num_pool_pages = s.num_pool_pages;
-    AttnParams a{};                                      // what the tree prologue reads and writes
-    a.parents = tree_parents;
-    a.prefix_lens = prefix_lens;
-    a.status = reinterpret_cast<uint32_t*>(ws + lay.status);
-    a.anc = reinterpret_cast<uint64_t*>(ws + lay.anc);
-    a.lens = reinterpret_cast<int32_t*>(ws + lay.lens);
-    a.nn = reinterpret_cast<int32_t*>(ws + lay.nn);
-    a.B = s.batch;
-    a.N = s.num_nodes;
-    a.max_pages = s.max_pages_per_seq;
-    a.ps = kPage;
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
-    const cudaError_t e = launch_tree_prologue(a, st);
-    if (e != cudaSuccess) return launch_failed(e);
-    g_launches++;
-    return run_chunk(p, plan, lay, ws, s.dtype, TREESPEC_DTYPE_E4M3, st);
+    return attend_trees(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, shape,
+                        TREESPEC_DTYPE_E4M3, {}, {}, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t treespec_chunk_window_workspace_bytes(const treespec_chunk_shape* shape, int32_t window, int32_t sinks) {
+    const ChunkExtra x = window_of(window, sinks);
+    if (check_chunk_call(shape, x) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape, x), x).total;
+}
+
+extern "C" int tree_chunk_attn_window(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                      const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                      const int32_t* chunk_offsets, void* out, const treespec_chunk_shape* shape,
+                                      int32_t window, int32_t sinks, void* workspace, size_t workspace_bytes,
+                                      treespec_stream_t stream) {
+    return attend_chunks(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, chunk_offsets, out, shape,
+                         window_of(window, sinks), {}, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t treespec_attn_window_workspace_bytes(const treespec_attn_shape* shape, int32_t kv_dtype, int32_t window,
+                                                       int32_t sinks) {
+    const ChunkExtra x = window_of(window, sinks);
+    if (check_tree_call(shape, kv_dtype, x) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape, kv_dtype, x), x).total;
+}
+
+extern "C" int tree_attn_verify_window(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                       const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                       const int32_t* tree_parents, void* out, const treespec_attn_shape* shape,
+                                       int32_t kv_dtype, int32_t window, int32_t sinks, void* workspace,
+                                       size_t workspace_bytes, treespec_stream_t stream) {
+    return attend_trees(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, shape, kv_dtype,
+                        window_of(window, sinks), {}, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t treespec_chunk_shared_workspace_bytes(const treespec_chunk_shape* shape, int32_t num_groups) {
+    const ChunkExtra x = groups_of(num_groups);
+    if (check_chunk_call(shape, x) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape, x), x).total;
+}
+
+extern "C" int tree_chunk_attn_shared(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                      const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                      const int32_t* chunk_offsets, const int32_t* group_offsets,
+                                      const int32_t* shared_lens, void* out, const treespec_chunk_shape* shape,
+                                      int32_t num_groups, void* workspace, size_t workspace_bytes,
+                                      treespec_stream_t stream) {
+    return attend_chunks(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, chunk_offsets, out, shape,
+                         groups_of(num_groups), GroupParams{group_offsets, shared_lens, nullptr, nullptr}, workspace,
+                         workspace_bytes, stream);
+}
+
+extern "C" size_t treespec_attn_shared_workspace_bytes(const treespec_attn_shape* shape, int32_t kv_dtype,
+                                                       int32_t num_groups) {
+    const ChunkExtra x = groups_of(num_groups);
+    if (check_tree_call(shape, kv_dtype, x) != TREESPEC_OK) return 0;
+    return layout_of(*shape, plan_of(*shape, kv_dtype, x), x).total;
+}
+
+extern "C" int tree_attn_verify_shared(const void* q, const void* k_pages, const void* v_pages, const float* k_scales,
+                                       const float* v_scales, const int32_t* page_table, const int32_t* prefix_lens,
+                                       const int32_t* tree_parents, const int32_t* group_offsets,
+                                       const int32_t* shared_lens, void* out, const treespec_attn_shape* shape,
+                                       int32_t kv_dtype, int32_t num_groups, void* workspace, size_t workspace_bytes,
+                                       treespec_stream_t stream) {
+    return attend_trees(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, shape, kv_dtype,
+                        groups_of(num_groups), GroupParams{group_offsets, shared_lens, nullptr, nullptr}, workspace,
+                        workspace_bytes, stream);
 }
 
 extern "C" size_t treespec_draft_workspace_bytes(int32_t batch, int32_t frontier, int32_t topk) {

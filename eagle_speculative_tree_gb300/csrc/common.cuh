@@ -111,6 +111,8 @@ struct AttnParams {
     int32_t* stream_flags;        // persistent two-tile kernel: [2 * CTAs][2] a piece's partial is written
                                   // (slot, query tile); zeroed by the prologue
     uint64_t wait_ns;             // bound of the tensor-core kernels' pipeline waits (kDefaultWaitNs unless a test shortens it)
+    int32_t* depth;               // [B][N] depth of each node, and ancestor sets within the window alone; NULL: no window
+    int window, sinks;
 };
 
 // ------------------------------------------------------------------ accept
@@ -215,8 +217,16 @@ cudaError_t launch_chunk_append(const AppendParams& p, int dtype, int kv_dtype, 
 constexpr int kPage = 16;                     // tokens per page
 constexpr int kChunkMaxBatch = 1024;          // persistent tensor-core form: sequences per call
 constexpr int kChunkMaxCtas = 1024;           // persistent tensor-core form: CTAs
+constexpr int kMaxGroups = 1024;              // groups of sequences that share a prefix, per call
+constexpr int kSharedTile = 64;               // shared prefixes are taken in whole KV tiles of this many tokens
+enum ChunkMode {
+    kChunkPlain,
+    kChunkWindow,                             // a row sees the last `window` tokens and the first `sinks`
+    kChunkShared,                             // groups of sequences share their first tokens
+};
 struct ChunkLayout {
-    size_t status, cleared, anc, lens, nn, ml, acc, total;   // [status, cleared): zeroed before every call
+    // [status, cleared): zeroed before every call
+    size_t status, cleared, anc, lens, nn, depth, gtab, skip, ml, acc, rows_ml, rows_acc, total;
 };
 struct ChunkParams {
     const void* q;
@@ -241,13 +251,29 @@ struct ChunkParams {
     int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
     float scale_log2;
     uint64_t wait_ns;
+    int window, sinks;                        // kChunkWindow: >= 1, >= 0, both at most 2^30
+    const int32_t* depth;                     //               trees: [B][N] of the prologue
+    int groups;                               // kChunkShared: >= 1
+    const int4* gtab;                         //               [groups] of the group prologue: the first row, the rows,
+                                              //               the shared tokens (whole KV tiles; 0 with 0 rows where
+                                              //               nothing is shared), the sequence whose pages are read
+    const int32_t* skip;                      //               [B] shared tokens of each sequence
 };
+// Groups of sequences (kChunkShared): what the group prologue reads and writes.
+struct GroupParams {
+    const int32_t* group_offsets;             // [groups + 1]
+    const int32_t* shared_lens;               // [groups]
+    int4* gtab;
+    int32_t* skip;
+};
+cudaError_t launch_group_prologue(const ChunkParams& p, const GroupParams& g, cudaStream_t s);
+template <ChunkMode M>
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
 // the smallest row block whose CTA still has 8 warps, `elem` bytes per K/V element
 int chunk_simt_min_rows(int D, int elem);
 cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s);
 bool chunk_tc_supported(int dtype, int batch, long long pool_tokens);
-cudaError_t launch_chunk_merge(const ChunkParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s);
 
 // Rows of a sequence's new tokens: the first row, the rows, those of them that hold a
 // token (a padded tree's other rows are zeros), and the prefix length (-1: the sequence is
@@ -277,6 +303,24 @@ __device__ __forceinline__ bool seq_ok(const ChunkParams& p, int b) {
     if (!p.offsets) return true;
     const int o0 = p.offsets[b], o1 = p.offsets[b + 1], S = p.prefix_lens[b];
     return o0 >= 0 && o1 >= o0 && o1 <= p.T && S >= 0 && (long long)S + (o1 - o0) <= (long long)p.max_pages * kPage;
+}
+
+// The entries of a batch: its sequences; with shared prefixes, the groups and then the sequences.  A
+// group's rows are all new tokens of its sequences, over a "prefix" of the shared tokens alone.
+template <ChunkMode M>
+__device__ __forceinline__ int chunk_entries(const ChunkParams& p) {
+    return M == kChunkShared ? p.groups + p.B : p.B;
+}
+template <ChunkMode M>
+__device__ __forceinline__ SeqRows entry_rows(const ChunkParams& p, int v) {
+    if constexpr (M == kChunkShared) {
+        if (v < p.groups) {
+            const int4 g = p.gtab[v];
+            return SeqRows{g.x, g.y, g.y, g.z};
+        }
+        return seq_rows(p, v - p.groups);
+    }
+    return seq_rows(p, v);
 }
 
 // two e4m3 codes -> two floats (exact; NaN codes give NaN)

@@ -15,6 +15,10 @@
 
 namespace treespec {
 
+//
+// With a window (kWindow) the sets hold only what the window leaves of them: a node sees its
+// ancestors fewer than `window` steps above it, and those whose position S + depth is a sink's.
+template <bool kWindow>
 __global__ void __launch_bounds__(kMaxNodes) tree_prologue_kernel(AttnParams p) {
     __shared__ int par[kMaxNodes];
     __shared__ int bad, first_pad;
@@ -45,8 +49,16 @@ __global__ void __launch_bounds__(kMaxNodes) tree_prologue_kernel(AttnParams p) 
     if (i < N) {
         static_assert(kAncWords == 2, "two words per node");
         uint64_t w0 = 0, w1 = 0;                                  // nodes 0..63, 64..127
+        int depth = 0;
+        if (kWindow) {
+            for (int j = i < nb ? par[i] : -1; j >= 0; j = par[j]) ++depth;
+            p.depth[(size_t)b * N + i] = depth;
+        }
         if (i < nb) {
-            for (int j = i; j >= 0; j = par[j]) {                 // i, then its parent chain (par[j] < j)
+            const long long S = kWindow ? p.prefix_lens[b] : 0;
+            int up = 0;
+            for (int j = i; j >= 0; j = par[j], ++up) {           // i, then its parent chain (par[j] < j)
+                if (kWindow && up >= p.window && S + depth - up >= p.sinks) continue;
                 if (j < 64) w0 |= 1ull << j;
                 else w1 |= 1ull << (j - 64);
             }
@@ -68,7 +80,8 @@ __global__ void __launch_bounds__(kMaxNodes) tree_prologue_kernel(AttnParams p) 
 }
 
 cudaError_t launch_tree_prologue(const AttnParams& p, cudaStream_t s) {
-    tree_prologue_kernel<<<p.B, kMaxNodes, 0, s>>>(p);
+    if (p.depth) tree_prologue_kernel<true><<<p.B, kMaxNodes, 0, s>>>(p);
+    else tree_prologue_kernel<false><<<p.B, kMaxNodes, 0, s>>>(p);
     return cudaGetLastError();
 }
 

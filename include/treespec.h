@@ -515,6 +515,80 @@ int tree_kv_commit_e4m3(void *k_pages, void *v_pages, float *k_scales, float *v_
                         const int32_t *accept_len, int32_t *new_prefix_lens, const treespec_attn_shape *shape,
                         void *workspace, size_t workspace_bytes, treespec_stream_t stream);
 
+/* --------------------------------------------- sliding windows and shared prefixes */
+
+/*
+ * The calls below are tree_chunk_attn and the tree verification with one thing added.  Layouts,
+ * packed rows, pools, alignment, the treatment of values that are not finite and of bad
+ * lengths, offsets and pages are those of tree_chunk_attn and tree_attn_verify /
+ * tree_attn_verify_e4m3.  Of the tree calls, shape->dtype is that of q and out and kv_dtype that
+ * of the pools (the same, or TREESPEC_DTYPE_E4M3 with scales; else the scales are not used);
+ * shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q), num_splits is not used.
+ */
+
+/* Workspace bytes of the two window calls (0 if the arguments are invalid). */
+size_t treespec_chunk_window_workspace_bytes(const treespec_chunk_shape *shape, int32_t window, int32_t sinks);
+size_t treespec_attn_window_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t window,
+                                            int32_t sinks);
+
+/*
+ * tree_chunk_attn_window, tree_attn_verify_window -- attention with a sliding window and sinks: of
+ * the tokens that the plain call lets a row see, the row at position P (a chunk: prefix_lens[b] +
+ * i; a tree: prefix_lens[b] + the node's depth) sees those at positions p with
+ *     P - p < window   or   p < sinks
+ * (a cached or chunk token's position is its logical index, a tree node's prefix_lens[b] + its
+ * depth).  window >= 1: the row itself and the window - 1 positions before it; sinks >= 0.  A
+ * window that reaches every token gives the plain call's result.
+ * Pages that hold no token that a row of the call sees are not read, and their entries in the page
+ * table may hold anything: a program may give them back while the sequence goes on.  (A page's
+ * tokens outside the window may be read where the page holds one inside; they do not reach any
+ * row that does not see them.  In a tree, the root's window counts as seen by all nodes here.)
+ */
+int tree_chunk_attn_window(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                           const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                           const int32_t *chunk_offsets, void *out, const treespec_chunk_shape *shape,
+                           int32_t window, int32_t sinks, void *workspace, size_t workspace_bytes,
+                           treespec_stream_t stream);
+int tree_attn_verify_window(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                            const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                            const int32_t *tree_parents, void *out, const treespec_attn_shape *shape,
+                            int32_t kv_dtype, int32_t window, int32_t sinks, void *workspace,
+                            size_t workspace_bytes, treespec_stream_t stream);
+
+/* Workspace bytes of the two calls over shared prefixes (0 if the arguments are invalid). */
+size_t treespec_chunk_shared_workspace_bytes(const treespec_chunk_shape *shape, int32_t num_groups);
+size_t treespec_attn_shared_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t num_groups);
+
+/*
+ * tree_chunk_attn_shared, tree_attn_verify_shared -- attention of a batch whose sequences share
+ * long prefixes (one system prompt for many requests, several samples of one prompt): the shared
+ * tokens are read and multiplied once for all rows of a group.
+ *
+ * Group g is the sequences group_offsets[g] .. group_offsets[g+1]-1, whose logical tokens
+ * 0 .. shared_lens[g]-1 are the same: their page tables name the same pages there, or pages of
+ * the same content.  (Which of these pages a call reads is not defined, so every entry has to be
+ * valid.)  The result is the plain call's.
+ *   group_offsets [num_groups + 1]  int32 device, not decreasing, within [0, batch]; sequences
+ *                                   before the first and behind the last group share nothing
+ *   shared_lens   [num_groups]      int32 device, 0 <= shared_lens[g] <= the prefix length of
+ *                                   every sequence of the group that has new tokens
+ * Shared lengths that do not hold to that, and group offsets out of order or range, set BAD_LENGTH
+ * and the group (all groups, in case of offsets) is computed as if it shared nothing; so it is,
+ * without a status, where chunk_offsets are out of order.
+ * 1 <= num_groups <= 1024 (TREESPEC_KERNEL_TC_STREAM: batch + num_groups <= 1024).
+ * A tree's padding rows are zeros; what their q holds does not matter.
+ */
+int tree_chunk_attn_shared(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                           const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                           const int32_t *chunk_offsets, const int32_t *group_offsets, const int32_t *shared_lens,
+                           void *out, const treespec_chunk_shape *shape, int32_t num_groups, void *workspace,
+                           size_t workspace_bytes, treespec_stream_t stream);
+int tree_attn_verify_shared(const void *q, const void *k_pages, const void *v_pages, const float *k_scales,
+                            const float *v_scales, const int32_t *page_table, const int32_t *prefix_lens,
+                            const int32_t *tree_parents, const int32_t *group_offsets, const int32_t *shared_lens,
+                            void *out, const treespec_attn_shape *shape, int32_t kv_dtype, int32_t num_groups,
+                            void *workspace, size_t workspace_bytes, treespec_stream_t stream);
+
 /* ------------------------------------------------------------------------- helpers */
 
 /* Synchronise `stream` and copy the status word of a workspace used by the last call
