@@ -566,6 +566,8 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
     const size_t parts = c.ctas ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
     L.ml = take(parts * 2 * 4);
     L.acc = take(parts * D * 4);
+    L.rows_ml = take(c.ctas && shared ? rows * 2 * 4 : 0);
+    L.rows_acc = take(c.ctas && shared ? rows * D * 4 : 0);
     L.total = off;
     return L;
 }
@@ -577,7 +579,7 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
     return std::min(tokens, (long long)x.window + x.sinks + 2 * kPage + std::max(kSharedTile, tree_nodes));
 }
 ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
-    return chunk_plan(x.mode == kChunkPlain ? s.kernel : TREESPEC_KERNEL_SIMT, s.dtype, s.kv_dtype, s.batch + x.groups,
+    return chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch + x.groups,
                       (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
                       window_span((long long)s.max_pages_per_seq * kPage, x, 0), s.num_pool_pages, sm_count_or_default());
 }
@@ -633,7 +635,7 @@ int check_tree_call(const treespec_attn_shape* s, int kv_dtype, const ChunkExtra
     return check_extra(x);
 }
 ChunkPlan plan_of(const treespec_attn_shape& s, int kv_dtype, const ChunkExtra& x) {
-    return chunk_plan(x.mode == kChunkPlain ? s.kernel : TREESPEC_KERNEL_SIMT, s.dtype, kv_dtype, s.batch + x.groups,
+    return chunk_plan(s.kernel, s.dtype, kv_dtype, s.batch + x.groups,
                       (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
                       window_span((long long)s.max_pages_per_seq * kPage, x, s.num_nodes), s.num_pool_pages,
                       sm_count_or_default());
@@ -665,19 +667,33 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
     p.groups = x.groups;
     p.gtab = g.gtab = reinterpret_cast<int4*>(ws + lay.gtab);
     p.skip = g.skip = reinterpret_cast<int32_t*>(ws + lay.skip);
-    cudaError_t e;
+    p.rows_ml = reinterpret_cast<float*>(ws + lay.rows_ml);
+    p.rows_acc = reinterpret_cast<float*>(ws + lay.rows_acc);
+    cudaError_t e = cudaSuccess;
     if (x.mode == kChunkShared) {
         e = launch_group_prologue(p, g, st);
         if (e != cudaSuccess) return launch_failed(e);
         g_launches++;
     }
-    e = c.kernel == TREESPEC_KERNEL_TC_STREAM ? launch_chunk_tc(p, kv_dtype, st)
-        : x.mode == kChunkWindow              ? launch_chunk_simt<kChunkWindow>(p, dtype, kv_dtype, st)
-        : x.mode == kChunkShared              ? launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st)
-                                              : launch_chunk_simt<kChunkPlain>(p, dtype, kv_dtype, st);
+    const bool tc = c.kernel == TREESPEC_KERNEL_TC_STREAM;
+    switch (x.mode) {
+        case kChunkPlain:
+            e = tc ? launch_chunk_tc<kChunkPlain>(p, kv_dtype, st) : launch_chunk_simt<kChunkPlain>(p, dtype, kv_dtype, st);
+            break;
+        case kChunkWindow:
+            e = tc ? launch_chunk_tc<kChunkWindow>(p, kv_dtype, st) : launch_chunk_simt<kChunkWindow>(p, dtype, kv_dtype, st);
+            break;
+        case kChunkShared:
+            e = tc ? launch_chunk_tc<kChunkShared>(p, kv_dtype, st) : launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st);
+            break;
+    }
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;
     if (c.num_splits > 1 || x.mode == kChunkShared) {
+        if (tc) {                                        // the merge reads the rows' parts as it does splits
+            p.part_ml = p.rows_ml;
+            p.part_acc = p.rows_acc;
+        }
         e = launch_chunk_merge(p, x.mode, dtype, st);
         if (e != cudaSuccess) return launch_failed(e);
         g_launches++;

@@ -40,9 +40,10 @@ struct ProducerArgs {
     uint64_t* empty;              // [nst]
     int nst, stage_bytes, panel_bytes;
     int pg0, npg, dp0, ndp;
+    int low, sinks;               // kWindow: pages that hold no token at or behind `low` or below `sinks` count as zeros
 };
 
-template <int TILE, int DIM = kD, class Params>
+template <int TILE, int DIM = kD, bool kWindow = false, class Params>
 __device__ __forceinline__ bool produce_pages(const Params& p, const ProducerArgs& a, int b, int h, int t0,
                                               int t1, int L, int ntiles, int& g, volatile uint32_t* abort_flag) {
     constexpr int kPPT = TILE / 16;                    // pages per tile
@@ -72,7 +73,7 @@ __device__ __forceinline__ bool produce_pages(const Params& p, const ProducerArg
         int kind = 0;
         if (lane < a.npg) {
             kind = 2;
-            if (pos0 < t1) {
+            if (pos0 < t1 && (!kWindow || pos0 + 16 > a.low || pos0 < a.sinks)) {
                 const bool ok = page >= 0 && page < p.num_pool_pages;
                 if (!ok) atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
                 if (ok && pos0 + 16 <= L) kind = 1;

@@ -258,6 +258,8 @@ struct ChunkParams {
                                               //               the shared tokens (whole KV tiles; 0 with 0 rows where
                                               //               nothing is shared), the sequence whose pages are read
     const int32_t* skip;                      //               [B] shared tokens of each sequence
+    float* rows_ml;                           //               persistent: the rows' two parts for the merge,
+    float* rows_acc;                          //               [2][T][Hq][2] and [2][T][Hq][D]
 };
 // Groups of sequences (kChunkShared): what the group prologue reads and writes.
 struct GroupParams {
@@ -271,8 +273,10 @@ template <ChunkMode M>
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
 // the smallest row block whose CTA still has 8 warps, `elem` bytes per K/V element
 int chunk_simt_min_rows(int D, int elem);
+template <ChunkMode M>
 cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s);
-bool chunk_tc_supported(int dtype, int batch, long long pool_tokens);
+// entries: sequences and groups of them
+bool chunk_tc_supported(int dtype, int entries, long long pool_tokens);
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s);
 
 // Rows of a sequence's new tokens: the first row, the rows, those of them that hold a

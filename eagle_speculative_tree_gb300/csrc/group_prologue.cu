@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(kThreads) group_prologue_kernel(const ChunkPar
     __shared__ int first[kMaxGroups], count[kMaxGroups], least[kMaxGroups];   // of the group's sequences with rows
     __shared__ int off[kMaxGroups + 1], share[kMaxGroups];
     __shared__ int bad_groups, bad_chunks;
+    grid_dep_release();                                    // the attention kernel may launch; it waits for this grid
     const int tid = threadIdx.x, NG = p.groups;
     if (tid == 0) bad_groups = bad_chunks = 0;
     for (int k = tid; k <= NG; k += kThreads) off[k] = g.group_offsets[k];
