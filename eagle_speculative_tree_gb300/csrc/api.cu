@@ -494,7 +494,9 @@ int check_chunk_shape(const treespec_chunk_shape* s, bool attn) {
 }
 
 struct ChunkPlan {
-    int kernel, num_splits, split_tokens, rows_block, ctas;
+    int kernel, num_splits, split_tokens, rows_block;
+    int ctas;                                            // tensor cores: CTAs over units of 256 rows, 0: none
+    int few_ctas, row_tiles;                             // CTAs over units of 16 row_tiles rows, 0: none
 };
 
 // What a call adds to plain causal or tree attention.
@@ -552,7 +554,9 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
         off = align_up(off + bytes, kWsAlign);
         return at;
     };
-    L.status = take(kWsAlign + size_t(c.ctas) * 8 * 4);  // and the persistent kernel's counters behind it
+    L.status = take(kWsAlign);
+    L.counters = take(size_t(c.ctas) * 8 * 4);
+    L.few_counters = take(size_t(c.few_ctas) * 8 * 4);
     L.cleared = off;
     L.anc = take(size_t(tree_rows) * kAncWords * 8);
     L.lens = take(tree_rows ? size_t(batch) * 4 : 0);
@@ -560,14 +564,17 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
     L.depth = take(x.mode == kChunkWindow ? size_t(tree_rows) * 4 : 0);
     L.gtab = take(size_t(x.groups) * 16);
     L.skip = take(x.groups ? size_t(batch) * 4 : 0);
-    // SIMT: a row of each split, and of each split of its group's; persistent: two slots of two tiles per CTA
-    const bool shared = x.mode == kChunkShared;
+    // SIMT: a row of each split, and of each split of its group's; persistent: two slots of a unit's rows per CTA
+    const bool shared = x.mode == kChunkShared, tc = c.kernel == TREESPEC_KERNEL_TC_STREAM;
     const size_t rows = size_t(T) * Hq * (shared ? 2 : 1);
-    const size_t parts = c.ctas ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
+    const size_t parts = tc ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
+    const size_t few = size_t(2) * c.few_ctas * 64;
     L.ml = take(parts * 2 * 4);
     L.acc = take(parts * D * 4);
-    L.rows_ml = take(c.ctas && shared ? rows * 2 * 4 : 0);
-    L.rows_acc = take(c.ctas && shared ? rows * D * 4 : 0);
+    L.few_ml = take(few * 2 * 4);
+    L.few_acc = take(few * D * 4);
+    L.rows_ml = take(tc && shared ? rows * 2 * 4 : 0);
+    L.rows_acc = take(tc && shared ? rows * D * 4 : 0);
     L.total = off;
     return L;
 }
@@ -578,10 +585,24 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
     if (x.mode != kChunkWindow) return tokens;
     return std::min(tokens, (long long)x.window + x.sinks + 2 * kPage + std::max(kSharedTile, tree_nodes));
 }
+// With a window or shared prefixes, batches of few rows per sequence take the kernel made for them
+// (chunk_few.cuh), unless the call names the other; the lengths are on the device, so the mean
+// counts.
+ChunkPlan few_plan(ChunkPlan c, int kernel, const ChunkExtra& x, long long batch, long long rows, int G, int sms) {
+    if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain) return c;
+    const long long mean = std::max<long long>((rows + batch - 1) / batch, G);
+    if (mean > 64) return c;
+    c.row_tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    c.few_ctas = std::min(2 * sms, kChunkMaxCtas);
+    if (x.mode == kChunkWindow || rows <= 64) c.ctas = 0;   // else the groups' units are of 256 rows
+    return c;
+}
 ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
-    return chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch + x.groups,
-                      (long long)s.num_tokens * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
-                      window_span((long long)s.max_pages_per_seq * kPage, x, 0), s.num_pool_pages, sm_count_or_default());
+    const int G = s.num_q_heads / s.num_kv_heads, sms = sm_count_or_default();
+    const long long rows = (long long)s.num_tokens * G;
+    return few_plan(chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch + x.groups, rows, s.num_kv_heads, s.head_dim,
+                               window_span((long long)s.max_pages_per_seq * kPage, x, 0), s.num_pool_pages, sms),
+                    s.kernel, x, s.batch, rows, G, sms);
 }
 ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c, const ChunkExtra& x = {}) {
     return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch, x);
@@ -635,10 +656,11 @@ int check_tree_call(const treespec_attn_shape* s, int kv_dtype, const ChunkExtra
     return check_extra(x);
 }
 ChunkPlan plan_of(const treespec_attn_shape& s, int kv_dtype, const ChunkExtra& x) {
-    return chunk_plan(s.kernel, s.dtype, kv_dtype, s.batch + x.groups,
-                      (long long)s.batch * s.num_nodes * (s.num_q_heads / s.num_kv_heads), s.num_kv_heads, s.head_dim,
-                      window_span((long long)s.max_pages_per_seq * kPage, x, s.num_nodes), s.num_pool_pages,
-                      sm_count_or_default());
+    const int G = s.num_q_heads / s.num_kv_heads, sms = sm_count_or_default();
+    const long long rows = (long long)s.batch * s.num_nodes * G;
+    return few_plan(chunk_plan(s.kernel, s.dtype, kv_dtype, s.batch + x.groups, rows, s.num_kv_heads, s.head_dim,
+                               window_span((long long)s.max_pages_per_seq * kPage, x, s.num_nodes), s.num_pool_pages, sms),
+                    s.kernel, x, s.batch, rows, G, sms);
 }
 ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const ChunkExtra& x) {
     const long long rows = (long long)s.batch * s.num_nodes;
@@ -649,7 +671,7 @@ ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const Ch
 int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const ChunkExtra& x, GroupParams g,
               unsigned char* ws, int dtype, int kv_dtype, cudaStream_t st) {
     p.status = reinterpret_cast<uint32_t*>(ws + lay.status);
-    p.counters = reinterpret_cast<int32_t*>(ws + lay.status + kWsAlign);
+    p.counters = reinterpret_cast<int32_t*>(ws + lay.counters);
     p.part_ml = reinterpret_cast<float*>(ws + lay.ml);
     p.part_acc = reinterpret_cast<float*>(ws + lay.acc);
     p.ps = kPage;
@@ -659,12 +681,15 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
     p.rows_block = c.rows_block;
     p.ctas = c.ctas;
     p.tpq = 128 / p.G;
+    p.tpu = 2 * p.tpq;
     p.inv_g = (65536 + p.G - 1) / p.G;
     p.scale_log2 = float(1.4426950408889634 / std::sqrt(double(p.D)));
     p.wait_ns = g_wait_ns.load();
     p.window = x.window;
     p.sinks = x.sinks;
     p.groups = x.groups;
+    p.entry0 = 0;
+    p.entries = x.groups + p.B;
     p.gtab = g.gtab = reinterpret_cast<int4*>(ws + lay.gtab);
     p.skip = g.skip = reinterpret_cast<int32_t*>(ws + lay.skip);
     p.rows_ml = reinterpret_cast<float*>(ws + lay.rows_ml);
@@ -675,28 +700,42 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
         if (e != cudaSuccess) return launch_failed(e);
         g_launches++;
     }
-    const bool tc = c.kernel == TREESPEC_KERNEL_TC_STREAM;
-    switch (x.mode) {
-        case kChunkPlain:
-            e = tc ? launch_chunk_tc<kChunkPlain>(p, kv_dtype, st) : launch_chunk_simt<kChunkPlain>(p, dtype, kv_dtype, st);
-            break;
-        case kChunkWindow:
-            e = tc ? launch_chunk_tc<kChunkWindow>(p, kv_dtype, st) : launch_chunk_simt<kChunkWindow>(p, dtype, kv_dtype, st);
-            break;
-        case kChunkShared:
-            e = tc ? launch_chunk_tc<kChunkShared>(p, kv_dtype, st) : launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st);
-            break;
+    const bool tc = c.kernel == TREESPEC_KERNEL_TC_STREAM, shared = x.mode == kChunkShared;
+    auto launch = [&](cudaError_t err) {
+        if (err == cudaSuccess) g_launches++;
+        return err;
+    };
+    if (c.few_ctas) {                                    // groups of many rows first, then the sequences
+        ChunkParams few = p;
+        if (shared && c.ctas) {
+            p.entries = p.groups;
+            e = launch(launch_chunk_tc<kChunkShared>(p, kv_dtype, st));
+            few.entry0 = p.groups;
+            few.entries = p.B;
+        }
+        few.ctas = c.few_ctas;
+        few.row_tiles = c.row_tiles;
+        few.tpu = 16 * c.row_tiles / p.G;
+        few.counters = reinterpret_cast<int32_t*>(ws + lay.few_counters);
+        few.part_ml = reinterpret_cast<float*>(ws + lay.few_ml);
+        few.part_acc = reinterpret_cast<float*>(ws + lay.few_acc);
+        if (e == cudaSuccess)
+            e = launch(shared ? launch_chunk_few<kChunkShared>(few, kv_dtype, st) : launch_chunk_few<kChunkWindow>(few, kv_dtype, st));
+    } else if (x.mode == kChunkPlain) {
+        e = launch(tc ? launch_chunk_tc<kChunkPlain>(p, kv_dtype, st) : launch_chunk_simt<kChunkPlain>(p, dtype, kv_dtype, st));
+    } else if (x.mode == kChunkWindow) {
+        e = launch(tc ? launch_chunk_tc<kChunkWindow>(p, kv_dtype, st) : launch_chunk_simt<kChunkWindow>(p, dtype, kv_dtype, st));
+    } else {
+        e = launch(tc ? launch_chunk_tc<kChunkShared>(p, kv_dtype, st) : launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st));
     }
     if (e != cudaSuccess) return launch_failed(e);
-    g_launches++;
-    if (c.num_splits > 1 || x.mode == kChunkShared) {
+    if (c.num_splits > 1 || shared) {
         if (tc) {                                        // the merge reads the rows' parts as it does splits
             p.part_ml = p.rows_ml;
             p.part_acc = p.rows_acc;
         }
-        e = launch_chunk_merge(p, x.mode, dtype, st);
+        e = launch(launch_chunk_merge(p, x.mode, dtype, st));
         if (e != cudaSuccess) return launch_failed(e);
-        g_launches++;
     }
     return TREESPEC_OK;
 }

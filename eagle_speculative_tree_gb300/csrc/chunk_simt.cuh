@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
     }
     __syncthreads();
     const int v = seq_s;
-    const bool group = M == kChunkShared && v < p.groups;
-    const int b = M != kChunkShared ? v : group ? p.gtab[v].w : v - p.groups;   // whose row of the page table is read
+    const bool group = is_group<M>(p, v);
+    const int b = group ? p.gtab[v].w : sequence_of<M>(p, v);   // whose row of the page table is read
     const SeqRows sq = entry_rows<M>(p, v);
     const int skip = M == kChunkShared && !group ? p.skip[b] : 0;   // tokens that the group's blocks run over
     const bool partial = p.num_splits > 1 || group || skip > 0;

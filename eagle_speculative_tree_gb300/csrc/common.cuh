@@ -226,7 +226,8 @@ enum ChunkMode {
 };
 struct ChunkLayout {
     // [status, cleared): zeroed before every call
-    size_t status, cleared, anc, lens, nn, depth, gtab, skip, ml, acc, rows_ml, rows_acc, total;
+    size_t status, counters, few_counters, cleared, anc, lens, nn, depth, gtab, skip, ml, acc, few_ml, few_acc, rows_ml,
+        rows_acc, total;
 };
 struct ChunkParams {
     const void* q;
@@ -249,11 +250,14 @@ struct ChunkParams {
     int B, T, N, Hq, Hkv, G, D, ps, max_pages, num_pool_pages;
     int num_splits, split_tokens, rows_block; // SIMT
     int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
+    int tpu;                                  //             tokens per unit
+    int row_tiles;                            // few rows: row tiles of 16 in a unit, 1, 2 or 4
     float scale_log2;
     uint64_t wait_ns;
     int window, sinks;                        // kChunkWindow: >= 1, >= 0, both at most 2^30
     const int32_t* depth;                     //               trees: [B][N] of the prologue
     int groups;                               // kChunkShared: >= 1
+    int entry0, entries;                      //               the entries of this launch
     const int4* gtab;                         //               [groups] of the group prologue: the first row, the rows,
                                               //               the shared tokens (whole KV tiles; 0 with 0 rows where
                                               //               nothing is shared), the sequence whose pages are read
@@ -275,6 +279,8 @@ cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cud
 int chunk_simt_min_rows(int D, int elem);
 template <ChunkMode M>
 cudaError_t launch_chunk_tc(const ChunkParams& p, int kv_dtype, cudaStream_t s);
+template <ChunkMode M>
+cudaError_t launch_chunk_few(const ChunkParams& p, int kv_dtype, cudaStream_t s);
 // entries: sequences and groups of them
 bool chunk_tc_supported(int dtype, int entries, long long pool_tokens);
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s);
@@ -309,22 +315,28 @@ __device__ __forceinline__ bool seq_ok(const ChunkParams& p, int b) {
     return o0 >= 0 && o1 >= o0 && o1 <= p.T && S >= 0 && (long long)S + (o1 - o0) <= (long long)p.max_pages * kPage;
 }
 
-// The entries of a batch: its sequences; with shared prefixes, the groups and then the sequences.  A
-// group's rows are all new tokens of its sequences, over a "prefix" of the shared tokens alone.
+// The entries of a launch: the batch's sequences; with shared prefixes, entries entry0 .. entry0 +
+// entries - 1 of the list of its groups and then its sequences.  A group's rows are all new tokens
+// of its sequences, over a "prefix" of the shared tokens alone.
 template <ChunkMode M>
 __device__ __forceinline__ int chunk_entries(const ChunkParams& p) {
-    return M == kChunkShared ? p.groups + p.B : p.B;
+    return M == kChunkShared ? p.entries : p.B;
+}
+template <ChunkMode M>
+__device__ __forceinline__ bool is_group(const ChunkParams& p, int v) {
+    return M == kChunkShared && v + p.entry0 < p.groups;
+}
+template <ChunkMode M>
+__device__ __forceinline__ int sequence_of(const ChunkParams& p, int v) {
+    return M == kChunkShared ? v + p.entry0 - p.groups : v;
 }
 template <ChunkMode M>
 __device__ __forceinline__ SeqRows entry_rows(const ChunkParams& p, int v) {
-    if constexpr (M == kChunkShared) {
-        if (v < p.groups) {
-            const int4 g = p.gtab[v];
-            return SeqRows{g.x, g.y, g.y, g.z};
-        }
-        return seq_rows(p, v - p.groups);
+    if (is_group<M>(p, v)) {
+        const int4 g = p.gtab[v + p.entry0];
+        return SeqRows{g.x, g.y, g.y, g.z};
     }
-    return seq_rows(p, v);
+    return seq_rows(p, sequence_of<M>(p, v));
 }
 
 // two e4m3 codes -> two floats (exact; NaN codes give NaN)

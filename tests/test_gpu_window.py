@@ -35,9 +35,11 @@ def on_tensor_cores(ts, p, kernel):
     return p.q.dtype == torch.bfloat16 and kernel != ts.KERNEL_SIMT
 
 
-# kernels to run a type on: the CUDA cores take all, the tensor cores bf16 queries
-TYPES = [("f32", False, 0), ("f32", True, 0), ("bf16", False, 0), ("bf16", True, 0), ("bf16", False, 1), ("bf16", True, 1)]
-TYPE_IDS = ["f32", "f32-e4m3", "bf16", "bf16-e4m3", "bf16-simt", "bf16-e4m3-simt"]
+# kernels to run a type on: the CUDA cores take all, the tensor cores bf16 queries (in units of 256 rows, or by
+# their number where the call chooses)
+TYPES = [("f32", False, 0), ("f32", True, 0), ("bf16", False, 0), ("bf16", True, 0), ("bf16", False, 5), ("bf16", True, 5),
+         ("bf16", False, 1), ("bf16", True, 1)]
+TYPE_IDS = ["f32", "f32-e4m3", "bf16", "bf16-e4m3", "bf16-units", "bf16-e4m3-units", "bf16-simt", "bf16-e4m3-simt"]
 types = pytest.mark.parametrize("dtype,e4m3,kernel", TYPES, ids=TYPE_IDS)
 
 
