@@ -496,7 +496,7 @@ int check_chunk_shape(const treespec_chunk_shape* s, bool attn) {
 struct ChunkPlan {
     int kernel, num_splits, split_tokens, rows_block;
     int ctas;                                            // tensor cores: CTAs over units of 256 rows, 0: none
-    int few_ctas, row_tiles;                             // CTAs over units of 16 row_tiles rows, 0: none
+    int few_ctas, rows_tile, row_tiles;                  // CTAs over units of row_tiles tiles of so many rows, 0: none
 };
 
 // What a call adds to plain causal or tree attention.
@@ -545,7 +545,7 @@ ChunkPlan chunk_plan(int kernel, int dtype, int kv_dtype, long long batch, long 
     return c;
 }
 
-ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long long tree_rows, long long batch,
+ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int Hkv, int D, long long tree_rows, long long batch,
                          const ChunkExtra& x) {
     ChunkLayout L{};
     size_t off = 0;
@@ -563,12 +563,17 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int D, long lo
     L.nn = take(tree_rows ? size_t(batch) * 4 : 0);
     L.depth = take(x.mode == kChunkWindow ? size_t(tree_rows) * 4 : 0);
     L.gtab = take(size_t(x.groups) * 16);
-    L.skip = take(x.groups ? size_t(batch) * 4 : 0);
+    L.skip = take(x.groups ? size_t(batch) * 8 : 0);
+    L.group_units = take(size_t(x.groups) * 4);
+    // units of 256 rows: no more than rows fill, and one more for each group
+    L.units = take(x.groups && c.ctas ? size_t(Hkv) * (size_t(T) / (2 * (128 / (Hq / Hkv))) + x.groups) * 8 : 0);
+    L.plan = take(x.mode != kChunkPlain ? size_t(c.ctas) * sizeof(CtaPlan) : 0);
+    L.few_plan = take(size_t(c.few_ctas) * sizeof(CtaPlan));
     // SIMT: a row of each split, and of each split of its group's; persistent: two slots of a unit's rows per CTA
     const bool shared = x.mode == kChunkShared, tc = c.kernel == TREESPEC_KERNEL_TC_STREAM;
     const size_t rows = size_t(T) * Hq * (shared ? 2 : 1);
     const size_t parts = tc ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
-    const size_t few = size_t(2) * c.few_ctas * 64;
+    const size_t few = size_t(2) * c.few_ctas * 32;
     L.ml = take(parts * 2 * 4);
     L.acc = take(parts * D * 4);
     L.few_ml = take(few * 2 * 4);
@@ -591,10 +596,11 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
 ChunkPlan few_plan(ChunkPlan c, int kernel, const ChunkExtra& x, long long batch, long long rows, int G, int sms) {
     if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain) return c;
     const long long mean = std::max<long long>((rows + batch - 1) / batch, G);
-    if (mean > 64) return c;
-    c.row_tiles = mean <= 16 ? 1 : mean <= 32 ? 2 : 4;
+    if (mean > 32) return c;
+    c.rows_tile = mean <= 8 ? 8 : 16;
+    c.row_tiles = mean <= 16 ? 1 : 2;
     c.few_ctas = std::min(2 * sms, kChunkMaxCtas);
-    if (x.mode == kChunkWindow || rows <= 64) c.ctas = 0;   // else the groups' units are of 256 rows
+    if (x.mode == kChunkWindow || rows <= 32) c.ctas = 0;   // else the groups' units are of 256 rows
     return c;
 }
 ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
@@ -605,7 +611,7 @@ ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
                     s.kernel, x, s.batch, rows, G, sms);
 }
 ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c, const ChunkExtra& x = {}) {
-    return chunk_layout(c, s.num_tokens, s.num_q_heads, s.head_dim, 0, s.batch, x);
+    return chunk_layout(c, s.num_tokens, s.num_q_heads, s.num_kv_heads, s.head_dim, 0, s.batch, x);
 }
 
 int check_extra(const ChunkExtra& x) {
@@ -664,11 +670,11 @@ ChunkPlan plan_of(const treespec_attn_shape& s, int kv_dtype, const ChunkExtra& 
 }
 ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const ChunkExtra& x) {
     const long long rows = (long long)s.batch * s.num_nodes;
-    return chunk_layout(c, rows, s.num_q_heads, s.head_dim, rows, s.batch, x);
+    return chunk_layout(c, rows, s.num_q_heads, s.num_kv_heads, s.head_dim, rows, s.batch, x);
 }
 
-// What the attention calls share once their arguments are checked and the status word is cleared.
-int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const ChunkExtra& x, GroupParams g,
+// What the attention calls share once their arguments are checked.
+int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const ChunkExtra& x, const GroupParams& g,
               unsigned char* ws, int dtype, int kv_dtype, cudaStream_t st) {
     p.status = reinterpret_cast<uint32_t*>(ws + lay.status);
     p.counters = reinterpret_cast<int32_t*>(ws + lay.counters);
@@ -690,35 +696,48 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
     p.groups = x.groups;
     p.entry0 = 0;
     p.entries = x.groups + p.B;
-    p.gtab = g.gtab = reinterpret_cast<int4*>(ws + lay.gtab);
-    p.skip = g.skip = reinterpret_cast<int32_t*>(ws + lay.skip);
+    p.gtab = reinterpret_cast<int4*>(ws + lay.gtab);
+    p.skip = reinterpret_cast<int2*>(ws + lay.skip);
+    p.group_units = reinterpret_cast<int32_t*>(ws + lay.group_units);
+    p.units = reinterpret_cast<int2*>(ws + lay.units);
+    p.plan = reinterpret_cast<CtaPlan*>(ws + lay.plan);
     p.rows_ml = reinterpret_cast<float*>(ws + lay.rows_ml);
     p.rows_acc = reinterpret_cast<float*>(ws + lay.rows_acc);
-    cudaError_t e = cudaSuccess;
-    if (x.mode == kChunkShared) {
-        e = launch_group_prologue(p, g, st);
-        if (e != cudaSuccess) return launch_failed(e);
-        g_launches++;
-    }
     const bool tc = c.kernel == TREESPEC_KERNEL_TC_STREAM, shared = x.mode == kChunkShared;
+    ChunkParams few = p;                                 // the launch over units of few rows
+    if (c.few_ctas) {
+        few.plan = reinterpret_cast<CtaPlan*>(ws + lay.few_plan);
+        few.ctas = c.few_ctas;
+        few.rows_tile = c.rows_tile;
+        few.row_tiles = c.row_tiles;
+        few.tpu = c.rows_tile * c.row_tiles / p.G;
+        few.counters = reinterpret_cast<int32_t*>(ws + lay.few_counters);
+        few.part_ml = reinterpret_cast<float*>(ws + lay.few_ml);
+        few.part_acc = reinterpret_cast<float*>(ws + lay.few_acc);
+        if (shared && c.ctas) {                          // groups of many rows in a launch of their own
+            p.entries = p.groups;
+            few.entry0 = p.groups;
+            few.entries = p.B;
+        }
+    }
+    cudaError_t e = cudaSuccess;
     auto launch = [&](cudaError_t err) {
         if (err == cudaSuccess) g_launches++;
         return err;
     };
-    if (c.few_ctas) {                                    // groups of many rows first, then the sequences
-        ChunkParams few = p;
-        if (shared && c.ctas) {
-            p.entries = p.groups;
-            e = launch(launch_chunk_tc<kChunkShared>(p, kv_dtype, st));
-            few.entry0 = p.groups;
-            few.entries = p.B;
-        }
-        few.ctas = c.few_ctas;
-        few.row_tiles = c.row_tiles;
-        few.tpu = 16 * c.row_tiles / p.G;
-        few.counters = reinterpret_cast<int32_t*>(ws + lay.few_counters);
-        few.part_ml = reinterpret_cast<float*>(ws + lay.few_ml);
-        few.part_acc = reinterpret_cast<float*>(ws + lay.few_acc);
+    if (shared || (tc && x.mode == kChunkWindow)) {
+        PlanParams plan{};                               // chunks: also clears the status word and the counters
+        plan.groups = g;
+        plan.launches = !tc ? 0 : c.few_ctas && c.ctas ? 2 : 1;
+        plan.launch[0] = c.few_ctas ? few : p;
+        plan.launch[1] = p;
+        plan.cleared = p.status;
+        plan.clear = p.offsets ? int((lay.cleared - lay.status) / 4) : 0;
+        e = launch(launch_chunk_plan(plan, x.mode, st));
+        if (e != cudaSuccess) return launch_failed(e);
+    }
+    if (c.few_ctas) {
+        if (c.ctas) e = launch(launch_chunk_tc<kChunkShared>(p, kv_dtype, st));
         if (e == cudaSuccess)
             e = launch(shared ? launch_chunk_few<kChunkShared>(few, kv_dtype, st) : launch_chunk_few<kChunkWindow>(few, kv_dtype, st));
     } else if (x.mode == kChunkPlain) {
@@ -729,15 +748,13 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
         e = launch(tc ? launch_chunk_tc<kChunkShared>(p, kv_dtype, st) : launch_chunk_simt<kChunkShared>(p, dtype, kv_dtype, st));
     }
     if (e != cudaSuccess) return launch_failed(e);
-    if (c.num_splits > 1 || shared) {
-        if (tc) {                                        // the merge reads the rows' parts as it does splits
-            p.part_ml = p.rows_ml;
-            p.part_acc = p.rows_acc;
-        }
+    if (tc && shared) {
+        if (!c.ctas) p.units = nullptr;
+        e = launch(launch_group_merge(p, st));
+    } else if (c.num_splits > 1 || shared) {
         e = launch(launch_chunk_merge(p, x.mode, dtype, st));
-        if (e != cudaSuccess) return launch_failed(e);
     }
-    return TREESPEC_OK;
+    return e == cudaSuccess ? TREESPEC_OK : launch_failed(e);
 }
 
 // An attention call over packed chunks, whatever its form.
@@ -781,7 +798,9 @@ int attend_chunks(const void* q, const void* k_pages, const void* v_pages, const
     p.num_pool_pages = s.num_pool_pages;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
+    const bool planned = x.mode == kChunkShared || (x.mode == kChunkWindow && plan.kernel == TREESPEC_KERNEL_TC_STREAM);
+    if (!planned)
+        if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
     return run_chunk(p, plan, lay, x, g, ws, s.dtype, s.kv_dtype, st);
 }
 
@@ -996,7 +1015,7 @@ extern "C" int tree_chunk_attn_shared(const void* q, const void* k_pages, const 
                                       int32_t num_groups, void* workspace, size_t workspace_bytes,
                                       treespec_stream_t stream) {
     return attend_chunks(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, chunk_offsets, out, shape,
-                         groups_of(num_groups), GroupParams{group_offsets, shared_lens, nullptr, nullptr}, workspace,
+                         groups_of(num_groups), GroupParams{group_offsets, shared_lens}, workspace,
                          workspace_bytes, stream);
 }
 
@@ -1014,7 +1033,7 @@ extern "C" int tree_attn_verify_shared(const void* q, const void* k_pages, const
                                        int32_t kv_dtype, int32_t num_groups, void* workspace, size_t workspace_bytes,
                                        treespec_stream_t stream) {
     return attend_trees(q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, shape, kv_dtype,
-                        groups_of(num_groups), GroupParams{group_offsets, shared_lens, nullptr, nullptr}, workspace,
+                        groups_of(num_groups), GroupParams{group_offsets, shared_lens}, workspace,
                         workspace_bytes, stream);
 }
 

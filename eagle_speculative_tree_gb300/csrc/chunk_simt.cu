@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     int from = 0, to = p.num_splits;
     if constexpr (M == kChunkShared) {
         to = 2 * p.num_splits;
-        if (p.skip[b] == 0) from = p.num_splits;
+        if (p.skip[b].x == 0) from = p.num_splits;
         if (to - from == 1) return;
     }
     float acc[DS];
@@ -61,6 +61,98 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     for (int e = 0; e < DS; ++e) store_out<T>(p.out, size_t(gw) * D + lane * DS + e, acc[e] * inv);
 }
 
+// The same behind the tensor-core kernels: a row's own part is in rows_*[1], the group's in rows_*[0] or, where its
+// unit was cut, in the slots of its pieces: piece k in slot 2 c0 + 1 (k = 0) or 2 (c0 + k), rows as in
+// chunk_tc.cuh (token it of a query tile and head g of the group: row r = it G + g in place 32 (r % 4) + r / 4).
+template <int D>
+__global__ void __launch_bounds__(256) group_merge_kernel(const ChunkParams p) {
+    constexpr int DS = D / 32, kAhead = 8;
+    const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (gw >= (long long)p.T * p.Hq) return;
+    const int t = int(gw / p.Hq), hq = int(gw % p.Hq);
+    int b;
+    if (p.offsets) {
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.offsets[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+    } else {
+        b = t / p.N;
+    }
+    const int2 skip = p.skip[b];
+    if (skip.x == 0) return;                               // a row of no group: in `out` already
+    const SeqRows sq = seq_rows(p, b);
+    const int i = t - sq.row0;
+    if (i < 0 || i >= sq.n) return;
+    float acc[DS], lsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < DS; ++e) acc[e] = 0.f;
+    if (sq.S >= 0 && i < sq.live) {
+        const size_t rows = size_t(p.T) * p.Hq;
+        const float2* rows_ml = reinterpret_cast<const float2*>(p.rows_ml);
+        const float2* part_ml = reinterpret_cast<const float2*>(p.part_ml);
+        int2 unit = make_int2(0, 1);
+        int place = 0;
+        if (p.units) {
+            const int4 g = p.gtab[skip.y];
+            const int tok = t - g.x, pr = tok / p.tpu, it = tok - pr * p.tpu, np = (g.y + p.tpu - 1) / p.tpu;
+            unit = p.units[p.Hkv * p.group_units[skip.y] + (hq / p.G) * np + pr];
+            const int tile = it / p.tpq, r = (it - tile * p.tpq) * p.G + hq % p.G;
+            place = tile * 128 + (r & 3) * 32 + (r >> 2);
+        }
+        // state k of the row: 0 its own, then the group's
+        const int n = 1 + unit.y;
+        auto ml_of = [&](int k) -> float2 {
+            if (k == 0) return rows_ml[rows + gw];
+            if (unit.y == 1) return rows_ml[gw];
+            return part_ml[size_t(k == 1 ? 2 * unit.x + 1 : 2 * (unit.x + k - 1)) * 256 + place];
+        };
+        auto acc_of = [&](int k) -> const float* {
+            if (k == 0) return p.rows_acc + (rows + gw) * D;
+            if (unit.y == 1) return p.rows_acc + gw * D;
+            return p.part_acc + (size_t(k == 1 ? 2 * unit.x + 1 : 2 * (unit.x + k - 1)) * 256 + place) * D;
+        };
+        float top = -INFINITY;
+        for (int k0 = 0; k0 < n; k0 += 32) top = fmaxf(top, warp_max(k0 + lane < n ? ml_of(k0 + lane).x : -INFINITY));
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            const float2 x = k0 + lane < n ? ml_of(k0 + lane) : make_float2(-INFINITY, 0.f);
+            // left out: a state without a weight above 0, not one whose weight rounds to 0 (a NaN stays one)
+            const float w = x.x == -INFINITY ? (x.y == 0.f ? -1.f : 1.f) : exp2f(x.x - top);
+            lsum += warp_sum(w < 0.f ? 0.f : x.y * w);
+            const int kn = min(32, n - k0);
+            for (int k = 0; k < kn; k += kAhead) {
+                float y[kAhead][DS];
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const float* src = acc_of(k0 + min(k + a, kn - 1)) + lane * DS;
+                    if constexpr (DS == 4) {
+                        const float4 z = *reinterpret_cast<const float4*>(src);
+                        y[a][0] = z.x; y[a][1] = z.y; y[a][2] = z.z; y[a][3] = z.w;
+                    } else {
+                        const float2 z = *reinterpret_cast<const float2*>(src);
+                        y[a][0] = z.x; y[a][1] = z.y;
+                    }
+                }
+#pragma unroll
+                for (int a = 0; a < kAhead; ++a) {
+                    const float wa = __shfl_sync(0xffffffffu, w, (k + a) & 31);
+                    if (k + a < kn && wa >= 0.f) {
+#pragma unroll
+                        for (int e = 0; e < DS; ++e) acc[e] = fmaf(y[a][e], wa, acc[e]);
+                    }
+                }
+            }
+        }
+        lsum = 1.f / lsum;
+    }
+#pragma unroll
+    for (int e = 0; e < DS; ++e) store_out<uint16_t>(p.out, size_t(gw) * D + lane * DS + e, acc[e] * lsum);
+}
+
 template <typename T, int D>
 cudaError_t launch_merge(const ChunkParams& p, ChunkMode mode, cudaStream_t s) {
     const unsigned blocks = unsigned(((long long)p.T * p.Hq + 7) / 8);
@@ -77,6 +169,13 @@ int chunk_simt_min_rows(int D, int elem) {
 }
 
 template cudaError_t launch_chunk_simt<kChunkPlain>(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
+
+cudaError_t launch_group_merge(const ChunkParams& p, cudaStream_t s) {
+    const unsigned blocks = unsigned(((long long)p.T * p.Hq + 7) / 8);
+    if (p.D == 64) group_merge_kernel<64><<<blocks, 256, 0, s>>>(p);
+    else group_merge_kernel<128><<<blocks, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s) {
     if (dtype == TREESPEC_DTYPE_F32) return p.D == 64 ? launch_merge<float, 64>(p, mode, s) : launch_merge<float, 128>(p, mode, s);

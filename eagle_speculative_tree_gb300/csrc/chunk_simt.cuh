@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
     const bool group = is_group<M>(p, v);
     const int b = group ? p.gtab[v].w : sequence_of<M>(p, v);   // whose row of the page table is read
     const SeqRows sq = entry_rows<M>(p, v);
-    const int skip = M == kChunkShared && !group ? p.skip[b] : 0;   // tokens that the group's blocks run over
+    const int skip = M == kChunkShared && !group ? p.skip[b].x : 0;   // tokens that the group's blocks run over
     const bool partial = p.num_splits > 1 || group || skip > 0;
     const long long rb = unit - block_base<M>(p, v);
     if (rb < 0 || rb * p.rows_block >= (long long)sq.n * p.G) return;

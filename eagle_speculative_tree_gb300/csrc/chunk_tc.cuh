@@ -9,7 +9,7 @@
 // One CTA per SM.  The units, ordered (sequence, kv head, rows), and within them their KV
 // tiles are cut into equal contiguous ranges, one per CTA, so single decoded tokens over a
 // long cache, prompts and any mixture load every SM alike, whatever the lengths; they are
-// on the device and the host does not know them.  A unit costs Tune::kKappa tiles beyond its own
+// on the device and the host does not know them.  A unit costs TuneUnits::kKappa tiles beyond its own
 // (its epilogue and the restart of the pipeline).  A unit cut between CTAs leaves a partial
 // (m, l, O) of each piece in the CTAs' slots; of the warps that hold the same 32 rows the
 // one that finishes last joins them, in the order of the pieces, so the result does not
@@ -59,14 +59,6 @@ using namespace sm100;
 constexpr int kM = 128;              // rows of a query tile = TMEM lanes
 constexpr int kNQ = 2;               // query tiles
 constexpr int kRaw = 5;              // e4m3: stages of the rings of codes
-struct Tune {                        // of the cut
-    static constexpr int kKappa = 7;                   // a unit's fixed cost, in tiles
-    // No piece of a unit with CTAs of its own is shorter than this.  Joining costs by the row, so
-    // units of many rows are cut into longer pieces (8 nodes x 4 heads over 2048 e4m3 tokens: 28.7
-    // us in pieces of 4 tiles, 30.9 of 9; 3 prompts of up to 816 tokens, 4 heads: 33 and 25).
-    static constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
-    static constexpr int kWholeTiles = 4;              // units up to this long are not cut
-};
 constexpr int kScaleRing = 4;        // e4m3: tiles of scales
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;        // S buffer b of tile t: [128 t + 64 b, 128 t + 64 b + 64)
@@ -424,14 +416,22 @@ __device__ __forceinline__ void look(const ChunkParams& p, const Seg<M>& s, cons
     }
 }
 
+// Where a CTA's range lies among the others': the cut of the batch, or what the plan says of it.
+template <ChunkMode M>
+using Whereabouts = std::conditional_t<M == kChunkPlain, Cut, const CtaPlan*>;
+
 // The last of the warps that hold these rows of a cut unit joins its pieces.
 template <int D, ChunkMode M>
-__device__ __forceinline__ void join_unit(const ChunkParams& p, const Cut& cut, const Seg<M>& s, int me, int t, int quarter,
-                                          const Row& ro) {
+__device__ __forceinline__ void join_unit(const ChunkParams& p, const Whereabouts<M>& cut, const Seg<M>& s, int me, int t,
+                                          int quarter, const Row& ro) {
     int c0, pieces;
-    if (cut.m) {
+    if constexpr (M != kChunkPlain) {
+        const bool head = s.j0 == 0;
+        c0 = head ? me : cut->first_cta;
+        pieces = head ? cut->last_pieces : cut->first_pieces;
+    } else if (cut.m) {
         c0 = me / cut.m * cut.m;
-        pieces = unit_pieces<Tune>(s.n, s.tokens * p.G, cut.m);
+        pieces = unit_pieces<TuneUnits>(s.n, s.tokens * p.G, cut.m);
     } else {
         const SeqUnits<M> u = seq_units<M>(p, s.b);
         const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
@@ -467,9 +467,13 @@ __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char
     using C = Cfg<D, E4M3>;
     constexpr int DS = D / 32;
     const int lane = threadIdx.x & 31, t = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3, me = blockIdx.x;
-    const Cut cut = cut_of<M, Tune>(p, reinterpret_cast<const long long*>(sm + C::kOffTiles),
-                           reinterpret_cast<const int*>(sm + C::kOffUnits),
-                           *reinterpret_cast<const int*>(sm + C::kOffMisc + 8));
+    Whereabouts<M> cut;
+    if constexpr (M == kChunkPlain)
+        cut = cut_of<M, TuneUnits>(p, reinterpret_cast<const long long*>(sm + C::kOffTiles),
+                                   reinterpret_cast<const int*>(sm + C::kOffUnits),
+                                   *reinterpret_cast<const int*>(sm + C::kOffMisc + 8), gridDim.x);
+    else
+        cut = reinterpret_cast<const CtaPlan*>(sm + C::kOffTiles);
     const End* ends = reinterpret_cast<const End*>(sm + C::kOffEnds);
     __syncwarp();                                          // the lanes' stores come before what is read and stored here
     Walk<M> walk;
@@ -644,40 +648,59 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     }
     grid_dep_wait();                                       // trees: the prologue's results
 
-    // ---- the entries' tiles and units, and this CTA's range
-    scan_units<M, C::kThreads>(p, tiles_s, units_s, reinterpret_cast<long long*>(sm + C::kOffWarp), longest);
-    const Cut cut = cut_of<M, Tune>(p, tiles_s, units_s, *longest);
-    zero_rows<M, D, C::kThreads>(p);
     const int me = blockIdx.x;
-    if (cut.total == 0 || me >= cut.parts) {               // nothing to compute
+    Whereabouts<M> cut;
+    bool idle;
+    if constexpr (M == kChunkPlain) {
+        // ---- the entries' tiles and units, and this CTA's range
+        scan_units<M, C::kThreads>(p, tiles_s, units_s, reinterpret_cast<long long*>(sm + C::kOffWarp), longest);
+        cut = cut_of<M, TuneUnits>(p, tiles_s, units_s, *longest, gridDim.x);
+        idle = cut.total == 0 || me >= cut.parts;
+    } else {
+        // ---- this CTA's range, as planned
+        CtaPlan* plan = reinterpret_cast<CtaPlan*>(sm + C::kOffTiles);
+        if (tid < int(sizeof(CtaPlan) / 4))
+            reinterpret_cast<uint32_t*>(plan)[tid] = reinterpret_cast<const uint32_t*>(p.plan + me)[tid];
+        __syncthreads();
+        cut = plan;
+        idle = plan->begin.x < 0;
+    }
+    zero_rows<M, D>(p, tid, C::kThreads);
+    if (idle) {                                            // nothing to compute
         __syncthreads();
         if (warp == kWarpMma) tmem_dealloc(*tmem_slot, kTmemCols);
         return;
     }
-    if (warp < 2) {                                        // warp 0 the begin, warp 1 the end of the range
-        const int c = me + warp;
-        End e;
-        if (cut.m) {
-            e = unit_at(p, cut, me / cut.m);
-            const SeqRows r = entry_rows<M>(p, e.b);
-            const SeqUnits<M> u = seq_units<M>(p, e.b, r);
-            const int n = u.tiles(e.pr), left = (is_group<M>(p, e.b) ? r.n : u.live) - e.pr * u.tpu;
-            const int pieces = unit_pieces<Tune>(n, min(u.tpu, left) * p.G, cut.m), k = me % cut.m + warp;
-            e.j = k > pieces ? n : int((long long)n * k / pieces);   // beyond the last piece: nothing
-        } else if (c >= cut.parts) {
-            e = End{cut.B, 0, 0, 0};
-        } else {
-            e = locate<M>(p, cut, cut.bound(c));
-            const int n = seq_units<M>(p, e.b).tiles(e.pr);
-            // Short units stay whole: the cut moves to the nearer end of one, and both neighbours
-            // see it there (160 units of 1 or 2 tiles: 43 us cut, 27 whole; with units of up to 10
-            // tiles kept whole the ranges of ragged prompts get uneven, 388 us against 380)
-            if (n <= Tune::kWholeTiles) e.j = 2 * e.j < n ? 0 : n;
+    if constexpr (M == kChunkPlain) {
+        if (warp < 2) {                                        // warp 0 the begin, warp 1 the end of the range
+            const int c = me + warp;
+            End e;
+            if (cut.m) {
+                e = unit_at(p, cut, me / cut.m);
+                const SeqRows r = entry_rows<M>(p, e.b);
+                const SeqUnits<M> u = seq_units<M>(p, e.b, r);
+                const int n = u.tiles(e.pr), left = (is_group<M>(p, e.b) ? r.n : u.live) - e.pr * u.tpu;
+                const int pieces = unit_pieces<TuneUnits>(n, min(u.tpu, left) * p.G, cut.m), k = me % cut.m + warp;
+                e.j = k > pieces ? n : int((long long)n * k / pieces);   // beyond the last piece: nothing
+            } else if (c >= cut.parts) {
+                e = End{cut.B, 0, 0, 0};
+            } else {
+                e = locate<M>(p, cut, cut.bound(c));
+                const int n = seq_units<M>(p, e.b).tiles(e.pr);
+                // Short units stay whole: the cut moves to the nearer end of one, and both neighbours
+                // see it there (160 units of 1 or 2 tiles: 43 us cut, 27 whole; with units of up to 10
+                // tiles kept whole the ranges of ragged prompts get uneven, 388 us against 380)
+                if (n <= TuneUnits::kWholeTiles) e.j = 2 * e.j < n ? 0 : n;
+            }
+            if (lane == 0) {
+                ends[warp] = e;
+                if (warp == 0) *first_rows = entry_rows<M>(p, e.b);
+            }
         }
-        if (lane == 0) {
-            ends[warp] = e;
-            if (warp == 0) *first_rows = entry_rows<M>(p, e.b);
-        }
+    } else if (tid == 0) {
+        ends[0] = End{cut->begin.x, cut->begin.y, cut->begin.z, cut->begin.w};
+        ends[1] = End{cut->end.x, cut->end.y, cut->end.z, cut->end.w};
+        *first_rows = SeqRows{cut->rows.x, cut->rows.y, cut->rows.z, cut->rows.w};
     }
 
     tc_fence_before();
@@ -1159,7 +1182,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 mbar_arrive(&bars->o_free[t]);
             }
             if (warp_rows) {
-                if (__any_sync(0xffffffffu, ro.ok && !(odd == 0.f)) && s.part() != 0) {
+                // a group's rows see all of its tokens, and the merge joins its pieces
+                if (s.part() == 0) {
+                } else if (__any_sync(0xffffffffu, ro.ok && !(odd == 0.f))) {
                     if (lane == 0) atomicOr(redo, (whole ? 4u : head ? 2u : 1u) << (4 * warp));
                 } else if (!whole) {
                     join_unit<D, M>(p, cut, s, me, t, quarter, ro);
@@ -1209,7 +1234,7 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.offsets && M != kChunkShared ? 0 : 1;   // trees and groups: start while the prologue runs
+    cfg.numAttrs = p.offsets && M == kChunkPlain ? 0 : 1;  // start while the prologue or the plan is made
     e = cudaLaunchKernelEx(&cfg, kern, p, mk, mv);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -13,6 +13,22 @@ using namespace sm100;
 
 constexpr int kBN = 64;              // tokens per KV tile
 
+// Of the cut: kKappa, a unit's fixed cost in tiles.  No piece of a unit with CTAs of its own is shorter than
+// kMinTiles (kMinTilesManyRows of more than 64 rows), and units up to kWholeTiles long are not cut.
+struct TuneUnits {                   // units of 256 rows (chunk_tc.cuh)
+    static constexpr int kKappa = 7;
+    // Joining costs by the row, so units of many rows are cut into longer pieces (8 nodes x 4 heads over
+    // 2048 e4m3 tokens: 28.7 us in pieces of 4 tiles, 30.9 of 9; 3 prompts of up to 816 tokens, 4
+    // heads: 33 and 25).
+    static constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
+    static constexpr int kWholeTiles = 4;
+};
+struct TuneFew {                     // units of up to 32 rows (chunk_few.cuh)
+    static constexpr int kKappa = 3;
+    static constexpr int kMinTiles = 2, kMinTilesManyRows = 2;
+    static constexpr int kWholeTiles = 2;
+};
+
 // ------------------------------------------------------------------ units and the cut
 
 // a / b of non-negative numbers; a 64-bit division costs several times a 32-bit one, and
@@ -52,10 +68,12 @@ template <ChunkMode M>
 struct UnitsOf {};
 template <>
 struct UnitsOf<kChunkWindow> {
+    int full;                         // units whose tokens are all there
     int low, sink_tiles;              // first token of the window of row 0; tiles of the sinks
 };
 template <>
 struct UnitsOf<kChunkShared> {
+    int full;
     int base;                         // the first tile
 };
 template <ChunkMode M>
@@ -89,13 +107,15 @@ struct SeqUnits : UnitsOf<M> {
     __device__ __forceinline__ long long tiles_before(int pr) const {
         if (pr <= 0) return 0;
         if (tree) return (long long)pr * tiles(0);
-        const int full = min(pr, live / tpu);              // units whose tokens are all there
+        int full;                                          // units whose tokens are all there
+        if constexpr (M == kChunkPlain) full = min(pr, live / tpu);
+        else full = min(pr, this->full);
         long long s = sum_tiles(full, S + kBN - 1 + tpu);
         if (pr > full) s += end(pr - 1);
         if constexpr (M == kChunkShared) s -= (long long)pr * this->base;
         if constexpr (M == kChunkWindow) {                 // the gaps, from the first unit that has one on
             const long long to_gap = (long long)kBN * (this->sink_tiles + 1) - this->low;
-            const int k = to_gap <= 0 ? 0 : int(min((long long)pr, (to_gap + tpu - 1) / tpu));
+            const int k = to_gap <= 0 ? 0 : int(min(uint32_t(pr), (uint32_t(to_gap) + tpu - 1) / uint32_t(tpu)));   // < 2^32
             if (k < pr) s -= sum_tiles(pr - k, this->low + k * tpu) - (long long)(pr - k) * this->sink_tiles;
         }
         return s;
@@ -108,14 +128,19 @@ __device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v, co
     u.tpu = p.tpu;
     u.S = r.S;
     u.live = r.S < 0 ? 0 : r.live;
-    u.np = (u.live + u.tpu - 1) / u.tpu;
+    if constexpr (M == kChunkPlain) {
+        u.np = (u.live + u.tpu - 1) / u.tpu;
+    } else {
+        u.full = u.live / u.tpu;
+        u.np = u.full + (u.live > u.full * u.tpu);
+    }
     if constexpr (M == kChunkWindow) {
         u.low = r.S - p.window + 1;
         u.sink_tiles = (p.sinks + kBN - 1) / kBN;
     }
     if constexpr (M == kChunkShared) {
         const bool group = is_group<M>(p, v);
-        u.base = group ? 0 : p.skip[sequence_of<M>(p, v)] / kBN;
+        u.base = group ? 0 : p.skip[sequence_of<M>(p, v)].x / kBN;
         if (group) {                                       // every unit over the shared tokens alone
             u.tree = true;
             u.live = 0;
@@ -153,7 +178,7 @@ __device__ __forceinline__ int unit_pieces(int n, int rows, int m) {
 
 // The cut of a batch: the prefix sums and the KV tiles of its longest unit.
 template <ChunkMode M, class Tune>
-__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest) {
+__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest, int ctas) {
     // A range that holds pieces of two units pays the fixed cost twice, so where there is less
     // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
     // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
@@ -169,11 +194,11 @@ __device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* til
     cut.k = Tune::kKappa;
     cut.total = p.Hkv * tiles[entries] + Tune::kKappa * n;
     cut.m = 0;
-    if (cut.total < (long long)(Tune::kKappa + 2) * gridDim.x && n <= gridDim.x && n > 0) {
-        const int m = int(gridDim.x) / int(n);
-        if (longest / unit_pieces<Tune>(longest, 1, m) <= int(cut.total) / int(gridDim.x) + 2 * Tune::kKappa) cut.m = m;
+    if (cut.total < (long long)(Tune::kKappa + 2) * ctas && n <= ctas && n > 0) {
+        const int m = ctas / int(n);
+        if (longest / unit_pieces<Tune>(longest, 1, m) <= int(cut.total) / ctas + 2 * Tune::kKappa) cut.m = m;
     }
-    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)gridDim.x, max(1ll, cut.total / (Tune::kKappa + 1))));
+    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)ctas, max(1ll, cut.total / (Tune::kKappa + 1))));
     return cut;
 }
 
@@ -289,16 +314,17 @@ __device__ __forceinline__ void scan_units(const ChunkParams& p, long long* tile
     __syncthreads();
 }
 
-// Rows without a token (a padded tree's, and those of an invalid sequence) are zeros.
-template <ChunkMode M, int D, int kThreads>
-__device__ __forceinline__ void zero_rows(const ChunkParams& p) {
+// Rows without a token (a padded tree's, and those of an invalid sequence) are zeros; `threads` threads of the
+// CTA, this one number `tid` of them.
+template <ChunkMode M, int D>
+__device__ __forceinline__ void zero_rows(const ChunkParams& p, int tid, int threads) {
     if (M == kChunkShared && p.entry0 + p.entries <= p.groups) return;   // a launch over the groups alone
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const SeqRows r = seq_rows(p, b);
         const int from = r.S < 0 ? 0 : r.live;
         const size_t words = size_t(r.n - from) * p.Hq * (D / 8);
         uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + size_t(r.row0 + from) * p.Hq * D);
-        for (size_t e = threadIdx.x; e < words; e += kThreads) dst[e] = make_uint4(0, 0, 0, 0);
+        for (size_t e = tid; e < words; e += threads) dst[e] = make_uint4(0, 0, 0, 0);
     }
 }
 

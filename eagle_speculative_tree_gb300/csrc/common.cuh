@@ -226,8 +226,16 @@ enum ChunkMode {
 };
 struct ChunkLayout {
     // [status, cleared): zeroed before every call
-    size_t status, counters, few_counters, cleared, anc, lens, nn, depth, gtab, skip, ml, acc, few_ml, few_acc, rows_ml,
-        rows_acc, total;
+    size_t status, counters, few_counters, cleared, anc, lens, nn, depth, gtab, skip, group_units, units, plan, few_plan, ml,
+        acc, few_ml, few_acc, rows_ml, rows_acc, total;
+};
+// One CTA's range of KV tiles (chunk_plan.cu), as (entry, kv head, unit, tile) of its first tile and of the
+// first tile behind it; begin.x < 0: none.  Where the range's first unit began in another CTA: the
+// CTA that holds its first piece, and its pieces; where its last unit goes on in others: its pieces.
+struct alignas(16) CtaPlan {
+    int4 begin, end;
+    int4 rows;                                // SeqRows of the first entry
+    int32_t first_cta, first_pieces, last_pieces, unused;
 };
 struct ChunkParams {
     const void* q;
@@ -251,28 +259,39 @@ struct ChunkParams {
     int num_splits, split_tokens, rows_block; // SIMT
     int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
     int tpu;                                  //             tokens per unit
-    int row_tiles;                            // few rows: row tiles of 16 in a unit, 1, 2 or 4
+    int rows_tile, row_tiles;                 // few rows: rows of a tile, 8 or 16; tiles of a unit, 1 or 2
     float scale_log2;
     uint64_t wait_ns;
     int window, sinks;                        // kChunkWindow: >= 1, >= 0, both at most 2^30
     const int32_t* depth;                     //               trees: [B][N] of the prologue
+    const CtaPlan* plan;                      // kChunkWindow, kChunkShared, persistent: [CTAs]
     int groups;                               // kChunkShared: >= 1
     int entry0, entries;                      //               the entries of this launch
     const int4* gtab;                         //               [groups] of the group prologue: the first row, the rows,
                                               //               the shared tokens (whole KV tiles; 0 with 0 rows where
                                               //               nothing is shared), the sequence whose pages are read
-    const int32_t* skip;                      //               [B] shared tokens of each sequence
+    const int2* skip;                         //               [B] shared tokens of each sequence, its group
+    const int2* units;                        //               of the groups' units of 256 rows, in the order of the cut:
+                                              //               the CTA that holds a unit's first piece, and its pieces; the
+                                              //               merge's NULL: the groups' parts are whole
+    const int32_t* group_units;               //               [groups] units before each group, one kv head
     float* rows_ml;                           //               persistent: the rows' two parts for the merge,
     float* rows_acc;                          //               [2][T][Hq][2] and [2][T][Hq][D]
 };
-// Groups of sequences (kChunkShared): what the group prologue reads and writes.
+// Groups of sequences (kChunkShared) as the caller gives them.
 struct GroupParams {
     const int32_t* group_offsets;             // [groups + 1]
     const int32_t* shared_lens;               // [groups]
-    int4* gtab;
-    int32_t* skip;
 };
-cudaError_t launch_group_prologue(const ChunkParams& p, const GroupParams& g, cudaStream_t s);
+// Checks the groups and lays out the ranges of `launches` launches over entries of one batch (their plan, gtab,
+// skip, units and group_units are written); `clear` words at `cleared` are zeroed before anything else.
+struct PlanParams {
+    ChunkParams launch[2];
+    GroupParams groups;
+    uint32_t* cleared;
+    int launches, clear;
+};
+cudaError_t launch_chunk_plan(const PlanParams& p, ChunkMode mode, cudaStream_t s);
 template <ChunkMode M>
 cudaError_t launch_chunk_simt(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
 // the smallest row block whose CTA still has 8 warps, `elem` bytes per K/V element
@@ -284,6 +303,7 @@ cudaError_t launch_chunk_few(const ChunkParams& p, int kv_dtype, cudaStream_t s)
 // entries: sequences and groups of them
 bool chunk_tc_supported(int dtype, int entries, long long pool_tokens);
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s);
+cudaError_t launch_group_merge(const ChunkParams& p, cudaStream_t s);
 
 // Rows of a sequence's new tokens: the first row, the rows, those of them that hold a
 // token (a padded tree's other rows are zeros), and the prefix length (-1: the sequence is
