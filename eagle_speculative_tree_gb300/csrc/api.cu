@@ -496,7 +496,7 @@ int check_chunk_shape(const treespec_chunk_shape* s, bool attn) {
 struct ChunkPlan {
     int kernel, num_splits, split_tokens, rows_block;
     int ctas;                                            // tensor cores: CTAs over units of 256 rows, 0: none
-    int few_ctas, rows_tile, row_tiles;                  // CTAs over units of row_tiles tiles of so many rows, 0: none
+    int few_ctas, few_rows;                              // CTAs over units of 8 or 16 rows, 0: none
 };
 
 // What a call adds to plain causal or tree attention.
@@ -573,7 +573,7 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int Hkv, int D
     const bool shared = x.mode == kChunkShared, tc = c.kernel == TREESPEC_KERNEL_TC_STREAM;
     const size_t rows = size_t(T) * Hq * (shared ? 2 : 1);
     const size_t parts = tc ? size_t(2) * c.ctas * 256 : c.num_splits > 1 || shared ? size_t(c.num_splits) * rows : 0;
-    const size_t few = size_t(2) * c.few_ctas * 32;
+    const size_t few = size_t(2) * c.few_ctas * 16;
     L.ml = take(parts * 2 * 4);
     L.acc = take(parts * D * 4);
     L.few_ml = take(few * 2 * 4);
@@ -596,11 +596,10 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
 ChunkPlan few_plan(ChunkPlan c, int kernel, const ChunkExtra& x, long long batch, long long rows, int G, int sms) {
     if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain) return c;
     const long long mean = std::max<long long>((rows + batch - 1) / batch, G);
-    if (mean > 32) return c;
-    c.rows_tile = mean <= 8 ? 8 : 16;
-    c.row_tiles = mean <= 16 ? 1 : 2;
+    if (mean > 16) return c;
+    c.few_rows = mean <= 8 ? 8 : 16;
     c.few_ctas = std::min(2 * sms, kChunkMaxCtas);
-    if (x.mode == kChunkWindow || rows <= 32) c.ctas = 0;   // else the groups' units are of 256 rows
+    if (x.mode == kChunkWindow || rows <= 16) c.ctas = 0;   // else the groups' units are of 256 rows
     return c;
 }
 ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
@@ -708,14 +707,14 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
     if (c.few_ctas) {
         few.plan = reinterpret_cast<CtaPlan*>(ws + lay.few_plan);
         few.ctas = c.few_ctas;
-        few.rows_tile = c.rows_tile;
-        few.row_tiles = c.row_tiles;
-        few.tpu = c.rows_tile * c.row_tiles / p.G;
+        few.few_rows = c.few_rows;
+        few.tpu = c.few_rows / p.G;
         few.counters = reinterpret_cast<int32_t*>(ws + lay.few_counters);
         few.part_ml = reinterpret_cast<float*>(ws + lay.few_ml);
         few.part_acc = reinterpret_cast<float*>(ws + lay.few_acc);
         if (shared && c.ctas) {                          // groups of many rows in a launch of their own
             p.entries = p.groups;
+            few.behind_groups = 1;
             few.entry0 = p.groups;
             few.entries = p.B;
         }

@@ -2,7 +2,7 @@
 // with a sliding window or behind shared prefixes: bf16 queries, head dim 64 or 128, K/V bf16 or
 // e4m3.
 //
-// Such a unit, 8 to 32 rows (tokens x query heads) of one sequence and kv head, is bound by the
+// Such a unit, 8 or 16 rows (tokens x query heads) of one sequence and kv head, is bound by the
 // reading of K and V, not by arithmetic.  In chunk_tc.cuh the chain S -> softmax ->
 // P V over tensor memory takes 0.8 (bf16) to 1.3 us (e4m3) per KV tile and SM however few the rows
 // are.  Here warps of their own run over the tiles, and no step waits for another warp's: a warp holds
@@ -11,9 +11,8 @@
 // rows waste nothing.  A lane reads 16 bytes of K at a time, which permutes the head elements (Q's alike);
 // V^T is transposed on the way from shared memory (ldmatrix), P^T by movmatrix.
 //
-// A CTA is four such warps and two that fill the K and V rings by TMA, two CTAs to an SM.  With R row
-// tiles, warp w holds tile w % R and takes every (4 / R)-th half of a KV tile.  Units, the cut into one
-// range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
+// A CTA is four such warps and two that fill the K and V rings by TMA, two CTAs to an SM.  Warp w takes
+// half w, w + 4, .. of the unit's KV tiles.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
 // of a unit (or piece) the warps' states are joined through shared memory.
 //
 // e4m3: K's codes are widened to f16 (exact), and Q, scaled by a power of two per row, with them: f16
@@ -152,14 +151,13 @@ __device__ __forceinline__ float state_weight(float m, float l, float top) {
     return m == -INFINITY ? (l == 0.f ? -1.f : 1.f) : ex2(m - top);
 }
 
-// Rows r, r + by, .. of a cut unit's row tile, by one warp: piece k of a row is in slot 2 c0 + 1 (k = 0)
+// Rows r, r + 4, .. of a cut unit, by one warp: piece k of a row is in slot 2 c0 + 1 (k = 0)
 // or 2 (c0 + k).  Four rows are on their way at a time, their (m, l) with a piece per lane.
 template <int D, ChunkMode M>
-__device__ __noinline__ void join_rows(const ChunkParams& p, const Seg<M>& s, int c0, int pieces, int first, int r, int by,
-                                       int used) {
-    constexpr int DS = D / 32, kR = 4;
+__device__ __noinline__ void join_rows(const ChunkParams& p, const Seg<M>& s, int c0, int pieces, int r, int used) {
+    constexpr int DS = D / 32, kR = 4, by = kWarps;
     const int lane = threadIdx.x & 31;
-    auto slot = [&](int k) { return size_t(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * 32 + first; };
+    auto slot = [&](int k) { return size_t(k == 0 ? 2 * c0 + 1 : 2 * (c0 + k)) * 16; };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
     for (; r < used; r += kR * by) {
         int row[kR];                                       // behind the last: the last again, not stored
@@ -214,7 +212,7 @@ __device__ __noinline__ void join_rows(const ChunkParams& p, const Seg<M>& s, in
         }
 #pragma unroll
         for (int i = 0; i < kR; ++i)
-            if (r + i * by < used) store_row<D, M>(p, few_row<M>(p, s, first + row[i], D), s.part(), top[i], l[i], acc[i]);
+            if (r + i * by < used) store_row<D, M>(p, few_row<M>(p, s, row[i], D), s.part(), top[i], l[i], acc[i]);
     }
 }
 
@@ -307,9 +305,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (tid == 0) {
         for (int s = 0; s < kNS; ++s) {
             mbar_init(&bars->k_full[s], 1);
-            mbar_init(&bars->k_empty[s], p.row_tiles == 1 ? 2 : kWarps);   // the warps that take a part of the tile
+            mbar_init(&bars->k_empty[s], 2);               // the warps that take a half of the tile
             mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->v_empty[s], p.row_tiles == 1 ? 2 : kWarps);
+            mbar_init(&bars->v_empty[s], 2);
         }
         mbar_init(&bars->part_full, 32 * kWarps);
         mbar_init(&bars->part_empty, 32 * kWarps);
@@ -320,24 +318,25 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    grid_dep_wait();                                       // the plan
+    // Behind the groups' launch, which begins to let this one start once the plan is there, the wait comes last: for
+    // what follows, the end of this launch stands for the end of that one
+    if (!p.behind_groups) grid_dep_wait();                 // the plan
+    grid_dep_release();
     const int me = blockIdx.x;
     if (tid < int(sizeof(CtaPlan) / 4))
         reinterpret_cast<uint32_t*>(sm + C::kOffEnds)[tid] = reinterpret_cast<const uint32_t*>(p.plan + me)[tid];
     __syncthreads();
     const bool idle = plan.begin.x < 0;                    // nothing to compute
-    const End begin{plan.begin.x, plan.begin.y, plan.begin.z, plan.begin.w}, end{plan.end.x, plan.end.y, plan.end.z, plan.end.w};
-    const SeqRows first_rows{plan.rows.x, plan.rows.y, plan.rows.z, plan.rows.w};
-
     if (warp >= kWarps) {
         regs_lower<kRegsProduce>();
         if (warp > kWarpFewV) {
             zero_rows<M, D>(p, tid - 32 * (kWarpFewV + 1), kFewThreads - 32 * (kWarpFewV + 1));
+            if (p.behind_groups) grid_dep_wait();
             return;
         }
         if (idle) return;
         Walk<M> walk;
-        walk.start(p, begin, end, first_rows);
+        walk.start(p, plan);
         Seg<M> s;
         // ---------------------------------------------------------------- TMA producers
         const bool is_v = warp == kWarpFewV;
@@ -361,7 +360,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     regs_raise<kRegsCompute>();
     if (idle) return;
     const int g = lane >> 2, q = lane & 3;
-    const int R = p.row_tiles, WT = kWarps / R, rt = warp % R, wt = warp / R;
     float* part = reinterpret_cast<float*>(sm + C::kOffPart) + warp * 16 * C::kPitch;
     float2* part_ml = reinterpret_cast<float2*>(sm + C::kOffMl) + warp * 16;
     // a wait of the whole warp: false for all of its lanes after a timeout of one, or when the CTA has been told to stop
@@ -375,7 +373,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     };
     static_assert(sizeof(Place) <= 256, "a warp's place in shared memory");
     Place& place = *reinterpret_cast<Place*>(sm + C::kOffSeg + warp * 256);
-    if (lane == 0) place.walk.start(p, begin, end, first_rows);
+    if (lane == 0) place.walk.start(p, plan);
     const Seg<M>& s = place.seg;
     auto next = [&]() -> bool {
         __syncwarp();                                      // the lanes are done with the last segment
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         float sc[NR][2];                                   // of a score of rows 2 q, 2 q + 1, to base 2
 #pragma unroll
         for (int h = 0; h < NR; ++h) {
-            const Row r = few_row<M>(p, s, rt * kRows + 8 * h + g, D);
+            const Row r = few_row<M>(p, s, 8 * h + g, D);
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + r.at;
 #pragma unroll
             for (int kk = 0; kk < NM; ++kk) {
@@ -432,7 +430,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
             for (int b = 0; b < 2; ++b) sc[h][b] = __shfl_sync(0xffffffffu, f, (2 * q + b) * 4);
         }
-        const int used = min(kRows, s.tokens * p.G - rt * kRows);   // rows of the warp
+        const int used = s.tokens * p.G;                   // rows of the unit
         // what every row of the unit sees: of prefix and new tokens those below `all_end`, of the window those from all_low on
         const int t1 = s.t1, ntiles = s.ntiles, all_end = min(t1, p.offsets ? s.S + s.i0 + 1 : s.S);
         int low = 0, all_low = 0;
@@ -451,14 +449,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 for (int i = 0; i < 4; ++i) o[t][h][i] = 0.f;
         }
 
-        // the warp's steps of the segment: halves of a KV tile, number WT n + wt of them
-        for (int step = wt; step < 2 * ntiles; step += WT) {
+        // the warp's steps of the segment: halves of a KV tile
+        for (int step = warp; step < 2 * ntiles; step += kWarps) {
             const int j = step >> 1, st = (ring + j) % kNS;
             const uint32_t ph = ((ring + j) / kNS) & 1;
             const int half = (step & 1) * kStep, pos0 = s.place(j) + half;
             const unsigned char* kt = sm + C::kOffK + st * C::kTile + half * kRowBytes;
             const unsigned char* vt = sm + C::kOffV + st * C::kTile + half * kRowBytes;
-            bool any = used > 0 && pos0 < t1;              // some row sees a token
+            bool any = pos0 < t1;                          // some row sees a token
             if constexpr (M == kChunkWindow) any = any && (pos0 + kStep > low || pos0 < p.sinks);
             if (!ready(&bars->k_full[st], ph)) { alive = false; break; }
             if (!any) {
@@ -538,7 +536,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 for (int h = 0; h < NR; ++h)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const Row r = few_row<M>(p, s, rt * kRows + 8 * h + 2 * q + b, D);
+                        const Row r = few_row<M>(p, s, 8 * h + 2 * q + b, D);
                         const Sight<M> si = sight_of<M>(p, s, r);
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
@@ -748,45 +746,43 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         ++segs;
         const bool whole = s.whole(), head = s.j0 == 0;
 #pragma unroll 4
-        for (int r = wt; r < used; r += WT) {
+        for (int r = warp; r < used; r += kWarps) {
             float2 x[kWarps];
             float top = -INFINITY, sum = 0.f, acc[DS];
 #pragma unroll
             for (int e = 0; e < DS; ++e) acc[e] = 0.f;
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                if (k < WT) {
-                    x[k] = reinterpret_cast<const float2*>(sm + C::kOffMl)[(k * R + rt) * 16 + r];
-                    top = fmaxf(top, x[k].x);
+            for (int k = 0; k < kWarps; ++k) {
+                x[k] = reinterpret_cast<const float2*>(sm + C::kOffMl)[k * 16 + r];
+                top = fmaxf(top, x[k].x);
+            }
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float w = state_weight(x[k].x, x[k].y, top);
+                if (w < 0.f) continue;
+                sum = fmaf(x[k].y, w, sum);
+                const float* src = reinterpret_cast<const float*>(sm + C::kOffPart) + (k * 16 + r) * C::kPitch + lane * DS;
+                float y[DS];
+                if constexpr (DS == 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(src);
+                    y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
+                } else {
+                    const float2 z = *reinterpret_cast<const float2*>(src);
+                    y[0] = z.x; y[1] = z.y;
                 }
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                if (k < WT) {
-                    const float w = state_weight(x[k].x, x[k].y, top);
-                    if (w < 0.f) continue;
-                    sum = fmaf(x[k].y, w, sum);
-                    const float* src = reinterpret_cast<const float*>(sm + C::kOffPart) + ((k * R + rt) * 16 + r) * C::kPitch + lane * DS;
-                    float y[DS];
-                    if constexpr (DS == 4) {
-                        const float4 z = *reinterpret_cast<const float4*>(src);
-                        y[0] = z.x; y[1] = z.y; y[2] = z.z; y[3] = z.w;
-                    } else {
-                        const float2 z = *reinterpret_cast<const float2*>(src);
-                        y[0] = z.x; y[1] = z.y;
-                    }
-#pragma unroll
-                    for (int e = 0; e < DS; ++e) acc[e] = fmaf(y[e], w, acc[e]);
-                }
+                for (int e = 0; e < DS; ++e) acc[e] = fmaf(y[e], w, acc[e]);
+            }
             if (whole) {
-                store_row<D, M>(p, few_row<M>(p, s, rt * kRows + r, D), s.part(), top, sum, acc);
+                store_row<D, M>(p, few_row<M>(p, s, r, D), s.part(), top, sum, acc);
             } else {
-                const size_t slot = size_t(2 * me + (head ? 1 : 0)) * 32 + rt * kRows + r;
+                const size_t slot = size_t(2 * me + (head ? 1 : 0)) * 16 + r;
                 store_slice<DS>(p.part_acc + slot * D + lane * DS, acc);
                 if (lane == 0) __stcg(reinterpret_cast<float2*>(p.part_ml) + slot, make_float2(top, sum));
             }
         }
         mbar_arrive(&bars->part_empty);
-        if (!whole && used > 0) {
+        if (!whole) {
             // the last of the warps that hold these rows of a cut unit joins its pieces
             const int c0 = head ? me : plan.first_cta, pieces = head ? plan.last_pieces : plan.first_pieces;
             __threadfence();
@@ -796,7 +792,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             n = __shfl_sync(0xffffffffu, n, 0);
             if (n == pieces - 1) {
                 __threadfence();
-                join_rows<D, M>(p, s, c0, pieces, rt * kRows, wt, WT, used);
+                join_rows<D, M>(p, s, c0, pieces, warp, used);
             }
         }
     }
@@ -809,9 +805,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 template <int D, bool E4M3, int NR, ChunkMode M>
 cudaError_t launch_few(const ChunkParams& p, cudaStream_t s) {
     using C = CfgFew<D, E4M3>;
-    if (p.ctas < 1 || p.ctas > kChunkMaxCtas || p.tpu < 1 || p.tpu * p.G > 8 * NR * p.row_tiles)
+    if (p.ctas < 1 || p.ctas > kChunkMaxCtas || p.tpu < 1 || p.tpu * p.G > 8 * NR)
         return cudaErrorInvalidValue;
-    if (p.row_tiles != 1 && p.row_tiles != 2) return cudaErrorInvalidValue;
     CUtensorMap mk = {}, mv = {};
     const long long pool_tokens = (long long)p.num_pool_pages * kPage;
     auto make = E4M3 ? make_code_map : make_pool_map;
@@ -841,7 +836,7 @@ cudaError_t launch_chunk_few(const ChunkParams& p, int kv_dtype, cudaStream_t s)
     auto launch = [&](auto dim, auto codes) {
         constexpr int D = decltype(dim)::value;
         constexpr bool kCodes = decltype(codes)::value;
-        return p.rows_tile == 8 ? launch_few<D, kCodes, 1, M>(p, s) : launch_few<D, kCodes, 2, M>(p, s);
+        return p.few_rows == 8 ? launch_few<D, kCodes, 1, M>(p, s) : launch_few<D, kCodes, 2, M>(p, s);
     };
     using D64 = std::integral_constant<int, 64>;
     using D128 = std::integral_constant<int, 128>;

@@ -8,9 +8,10 @@
 // new tokens, where one of them has a shorter prefix (BAD_LENGTH) and, as the rows of a
 // group have to be packed, anywhere in a batch whose offsets are out of order.
 //
-// The lengths are on the device.  One CTA per launch scans them and finds both ends of all ranges, a thread
-// per range; the launches' own CTAs then start with one load.  Scan and search in every one of these CTAs instead took
-// about 5 us of each, as the plain persistent kernel's do.
+// The lengths are on the device.  One CTA per launch scans them and finds where all ranges begin, a thread
+// per range; the launches' own CTAs then start with one load.  What bounds this kernel is the fetching of
+// its own instructions, which other kernels have displaced since its last run (the same code took 5 us run
+// twice in a row and 11 the first time): so it is short, with loops and calls where they save code.
 #include "chunk_units.cuh"
 
 namespace treespec {
@@ -23,29 +24,35 @@ static_assert(kChunkMaxBatch <= kThreads && kChunkMaxCtas <= kThreads, "a thread
 struct GroupSmem {
     int first[kMaxGroups], count[kMaxGroups], least[kMaxGroups];   // of the group's sequences with rows
     int off[kMaxGroups + 1], share[kMaxGroups];
+    int4 table[kMaxGroups];
     int bad_groups, bad_chunks;
 };
 struct CutSmem {
-    long long tiles[kChunkMaxBatch + 1];
-    long long warp_tiles[32], warp_rows[32];
-    int units[kChunkMaxBatch + 1];
-    int warp_units[32];
-    int longest;
+    long long start[kChunkMaxBatch + 1];                   // position of each entry in the cut
+    int units[kChunkMaxBatch + 1];                         // units before it, one kv head
+    long long head[kChunkMaxBatch];                        // positions of one kv head of it
+    int base[kChunkMaxBatch];                              // its first tile
     SeqRows rows[kChunkMaxBatch];
     int4 ends[kChunkMaxCtas];
     int pieces[kChunkMaxCtas];
+    long long warp_size[32], warp_units[32];
+    unsigned long long rows_sum;
+    float load[2];                                         // tiles of the sequences' units and of the groups'
+    int longest;
 };
-
-union PlanSmem {
+struct PlanSmem {
     GroupSmem groups;
     CutSmem cut;
 };
 
-__device__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, GroupSmem& sm, bool flags) {
+// `rows`, in shared memory: rows of sequence tid where there is one.
+__device__ __forceinline__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, GroupSmem& sm, const SeqRows& mine,
+                                               bool flags) {
     const int tid = threadIdx.x, NG = p.groups;
     int4* gtab = const_cast<int4*>(p.gtab);
     int2* skip = const_cast<int2*>(p.skip);
     if (tid == 0) sm.bad_groups = sm.bad_chunks = 0;
+    const int want0 = tid < NG ? g.shared_lens[tid] : 0;
     for (int k = tid; k <= NG; k += kThreads) sm.off[k] = g.group_offsets[k];
     for (int k = tid; k < NG; k += kThreads) {
         sm.first[k] = sm.least[k] = INT32_MAX;
@@ -69,18 +76,20 @@ __device__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, Group
         }
         return lo;
     };
+    const int mine_of = tid < p.B ? group_of(tid) : -1;
     for (int b = tid; b < p.B; b += kThreads) {
-        const int k = group_of(b);
+        const int k = b == tid ? mine_of : group_of(b);
         if (k < 0) continue;
-        const SeqRows r = seq_rows(p, b);
+        const SeqRows r = b == tid ? mine : seq_rows(p, b);
         if (r.n == 0) continue;
         atomicMin(&sm.first[k], b);
         atomicMin(&sm.least[k], r.S);
         atomicAdd(&sm.count[k], 1);
     }
     __syncthreads();
-    for (int k = tid; k < NG; k += kThreads) {
-        const int want = g.shared_lens[k];
+    static_assert(kMaxGroups <= kThreads, "a thread per group");
+    if (tid < NG) {
+        const int k = tid, want = want0;
         const bool ok = fine && want >= 0 && (sm.count[k] == 0 || want <= sm.least[k]);
         if (!ok && !sm.bad_chunks && flags) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
         int4 e = make_int4(0, 0, 0, 0);
@@ -91,176 +100,222 @@ __device__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, Group
             e.z = sm.share[k] = want / kSharedTile * kSharedTile;
             e.w = sm.first[k];
         }
-        gtab[k] = e;
+        sm.table[k] = gtab[k] = e;
     }
     __syncthreads();
     for (int b = tid; b < p.B; b += kThreads) {
-        const int k = group_of(b);
+        const int k = b == tid ? mine_of : group_of(b);
         skip[b] = k < 0 ? make_int2(0, 0) : make_int2(sm.share[k], k);
     }
-    __syncthreads();
 }
 
-// The tile at or after position x of the cut, by one thread.  x < total.
+struct Tuning {
+    int kappa, min_tiles, min_tiles_many_rows, whole_tiles;
+    int ctas;                                              // that get ranges
+};
+
+// Position of unit pr in its kv head: tiles and fixed costs of the units before it.  One copy of the code.
 template <ChunkMode M>
-__device__ End find(const ChunkParams& p, const Cut& q, const SeqRows* rows, long long x) {
-    int lo = 0, hi = q.B;                                  // the last b with before(b) <= x
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (q.before(mid) <= x) lo = mid;
-        else hi = mid;
-    }
-    End e;
-    e.b = lo;
-    const SeqUnits<M> u = seq_units<M>(p, lo, rows[lo]);
-    const long long head = div_pos(q.before(lo + 1) - q.before(lo), q.Hkv);
-    long long y = x - q.before(lo);
-    e.h = int(div_pos(y, head));
-    y -= e.h * head;
-    int at = 0, n = u.np;                                  // the last unit that begins at or before y
-    while (n - at > 1) {
-        const int mid = (at + n) >> 1;
-        if (u.tiles_before(mid) + (long long)q.k * mid <= y) at = mid;
-        else n = mid;
-    }
-    e.pr = at;
-    e.j = int(max(0ll, y - u.tiles_before(at) - (long long)q.k * at - q.k));
-    return e;
+__device__ __noinline__ long long unit_start(const SeqUnits<M>* u, int kappa, int pr) {
+    return u->tiles_before(pr) + (long long)kappa * pr;
 }
 
-template <ChunkMode M, class Tune>
-__device__ void lay_out_ranges(const ChunkParams& p, CutSmem& sm, bool flags) {
+// Scans a launch's entries and lays out its ranges.  Positions as in Cut, ranges even to one position: CTA c
+// of `parts` begins at c size + min(c, rest).
+template <ChunkMode M>
+__device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, const SeqRows& mine, const Tuning tune, bool flags) {
+    CutSmem& sm = all.cut;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int entries = chunk_entries<M>(p);
-    if (tid == 0) sm.longest = 0;
-    // ---- prefix sums of the entries' tiles and units
-    SeqRows r{0, 0, 0, -1};
-    long long nt = 0, nr = 0;
-    int nu = 0, top = 0;
+    const int entries = chunk_entries<M>(p), Hkv = p.Hkv;
+    if (tid == 0) {
+        sm.longest = 0;
+        sm.rows_sum = 0;
+    }
+    // ---- prefix sums of the entries' positions and units
+    long long size = 0;
+    int nu = 0, top = 0, nr = 0;
+    SeqUnits<M> u;
     if (tid < entries) {
-        r = entry_rows<M>(p, tid);
-        sm.rows[tid] = r;
-        const SeqUnits<M> u = seq_units<M>(p, tid, r);
+        SeqRows r = mine;
+        int base = 0;
+        if (M == kChunkShared) {
+            if (is_group<M>(p, tid)) {
+                const int4 g = all.groups.table[tid + p.entry0];
+                r = SeqRows{g.x, g.y, g.y, g.z};
+            } else {
+                const int b = sequence_of<M>(p, tid);
+                if (b != tid) r = seq_rows(p, b);
+                base = p.skip[b].x / kBN;                  // written by this block
+            }
+        }
+        u = seq_units<M>(p, tid, r, base);
         nu = u.np;
         if (nu) {
-            nt = nu == 1 ? u.tiles(0) : u.tiles_before(nu);
+            size = nu == 1 ? u.tiles(0) + tune.kappa : unit_start<M>(&u, tune.kappa, nu);
             top = u.tiles(nu - 1);
         }
+        sm.rows[tid] = r;
+        sm.base[tid] = base;
+        sm.head[tid] = size;
         if (!is_group<M>(p, tid)) {
             nr = r.n;
             if (flags && !seq_ok(p, sequence_of<M>(p, tid))) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
         }
     }
-    long long it = nt, ir = nr;
+    long long it = size;
     int iu = nu;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const long long a = __shfl_up_sync(0xffffffffu, it, o), b = __shfl_up_sync(0xffffffffu, ir, o);
+        const long long a = __shfl_up_sync(0xffffffffu, it, o);
         const int c = __shfl_up_sync(0xffffffffu, iu, o);
         if (lane >= o) {
             it += a;
-            ir += b;
             iu += c;
         }
     }
     if (lane == 31) {
-        sm.warp_tiles[warp] = it;
-        sm.warp_rows[warp] = ir;
+        sm.warp_size[warp] = it;
         sm.warp_units[warp] = iu;
     }
     top = __reduce_max_sync(0xffffffffu, top);
     __syncthreads();
     if (lane == 0 && top) atomicMax(&sm.longest, top);
-    long long bt = 0, all_t = 0, all_r = 0, bu = 0, all_u = 0;
+    if (nr) atomicAdd(&sm.rows_sum, (unsigned long long)nr);
+    long long bt = 0, all_t = 0, bu = 0, all_u = 0;
     const int used = (entries + 31) / 32;
+#pragma unroll 1
     for (int w = 0; w < used; ++w) {
         if (w == warp) bt = all_t, bu = all_u;
-        all_t += sm.warp_tiles[w];
-        all_r += sm.warp_rows[w];
+        all_t += sm.warp_size[w];
         all_u += sm.warp_units[w];
     }
-    // Sequences that share rows (offsets out of order) may have more units than 32 bits count: no row is
-    // computed then
-    const bool none = all_r > p.T;
     if (tid < entries) {
-        sm.tiles[tid] = bt + it - nt;
+        sm.start[tid] = Hkv * (bt + it - size);
         sm.units[tid] = int(bu) + iu - nu;
         if (is_group<M>(p, tid)) const_cast<int32_t*>(p.group_units)[tid + p.entry0] = sm.units[tid];
     }
     if (tid == 0) {
-        sm.tiles[entries] = none ? 0 : all_t;
-        sm.units[entries] = none ? 0 : int(all_u);
+        sm.start[entries] = Hkv * all_t;
+        sm.units[entries] = int(all_u);
     }
     __syncthreads();
 
-    // ---- the ranges
-    const Cut cut = cut_of<M, Tune>(p, sm.tiles, sm.units, sm.longest, p.ctas);
-    // rows of unit pr of entry b
-    auto rows_of = [&](int b, int pr, const SeqUnits<M>& u) {
-        return min(u.tpu, (is_group<M>(p, b) ? sm.rows[b].n : u.live) - pr * u.tpu) * p.G;
+    // ---- the cut, as cut_of() makes it.  Sequences that share rows (offsets out of order) may have more units than
+    // 32 bits count: no row is computed then
+    const long long total = sm.rows_sum > (unsigned long long)p.T ? 0 : Hkv * all_t, n = Hkv * all_u;
+    const int ctas = tune.ctas;
+    auto pieces_of = [&](int tiles, int rows, int m) {
+        return min(m, max(1, tiles / (rows > 64 ? tune.min_tiles_many_rows : tune.min_tiles)));
     };
-    // of unit e of n tiles: the CTA that holds its first piece, and its pieces
-    auto share_of = [&](const End& e, const SeqUnits<M>& u, int n, int index) -> int2 {
-        if (cut.m) return make_int2(index * cut.m, unit_pieces<Tune>(n, rows_of(e.b, e.pr, u), cut.m));
-        const long long ub = cut.before(e.b) + e.h * div_pos(cut.before(e.b + 1) - cut.before(e.b), cut.Hkv) +
-                             u.tiles_before(e.pr) + (long long)cut.k * e.pr + cut.k;
-        const int c0 = cut.owner(ub);
-        return make_int2(c0, n <= Tune::kWholeTiles ? 1 : cut.owner(ub + n - 1) - c0 + 1);
+    int m = 0;                                             // CTAs of each unit, 0: even ranges
+    if (total < (long long)(tune.kappa + 2) * ctas && n <= ctas && total > 0) {
+        m = ctas / int(n);
+        if (sm.longest / pieces_of(sm.longest, 1, m) > int(total) / ctas + 2 * tune.kappa) m = 0;
+    }
+    const int parts = total == 0 ? 0 : m ? m * int(n) : int(min((long long)ctas, max(1ll, total / (tune.kappa + 1))));
+    long long size_of = 1, rest = 0;                       // of a range
+    if (parts && !m) {
+        size_of = div_pos(total, parts);
+        rest = total - size_of * parts;
+    }
+    const long long wide = rest * (size_of + 1);
+    // The CTA that holds the first piece of a unit of `tiles` tiles at position `at` (number `index` of the batch), and its pieces
+    auto share_of = [&](long long at, int tiles, int rows, int index) -> int2 {
+        if (m) return make_int2(index * m, pieces_of(tiles, rows, m));
+        int c[2];
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            const long long x = at + (i ? tiles - 1 : 0);
+            c[i] = int(x < wide ? div_pos(x, size_of + 1) : rest + div_pos(x - wide, size_of));
+        }
+        return make_int2(c[0], tiles <= tune.whole_tiles ? 1 : c[1] - c[0] + 1);
     };
-    const int c = tid;
-    CtaPlan out{};
-    out.begin.x = -1;
-    if (cut.total > 0 && cut.m) {                          // m CTAs for each unit
-        if (c < cut.parts) {
-            End a = unit_at(p, cut, c / cut.m);
-            const SeqUnits<M> u = seq_units<M>(p, a.b, sm.rows[a.b]);
-            const int n = u.tiles(a.pr), k = c % cut.m;
-            const int2 share = share_of(a, u, n, c / cut.m);
-            auto at = [&](int k) { return k > share.y ? n : int((long long)n * k / share.y); };   // beyond the last: nothing
-            out.begin = make_int4(a.b, a.h, a.pr, at(k));
-            out.end = make_int4(a.b, a.h, a.pr, at(k + 1));
-            out.first_cta = share.x;
-            out.first_pieces = out.last_pieces = share.y;
+
+    // ---- the ranges, and behind them the groups' units of 256 rows for the merge: a thread per range or unit
+    const bool table = M == kChunkShared && !p.few_rows && is_group<M>(p, 0);
+    const int nunits = table && total > 0 ? Hkv * sm.units[min(entries, p.groups)] : 0;
+#pragma unroll 1
+    for (int pass = 0; pass < (table ? 2 : 1); ++pass)
+#pragma unroll 1
+        for (int job = tid; job < (pass ? nunits : kThreads); job += kThreads) {
+            const bool by_unit = pass || m, on = pass || job < parts;
+            End e{0, 0, 0, 0};
+            int2 share = make_int2(0, 0);
+            int tiles = 0;
+            if (on) {
+                const int index = pass ? job : m ? job / m : 0;
+                const long long x = by_unit ? index : job * size_of + min((long long)job, rest);
+                int lo = 0, hi = entries;                  // the last entry that begins at or before x
+#pragma unroll 1
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if ((by_unit ? (long long)Hkv * sm.units[mid] : sm.start[mid]) <= x) lo = mid;
+                    else hi = mid;
+                }
+                u = seq_units<M>(p, lo, sm.rows[lo], sm.base[lo]);
+                long long y = x - (by_unit ? (long long)Hkv * sm.units[lo] : sm.start[lo]);
+                const long long head = by_unit ? u.np : sm.head[lo];
+                e.b = lo;
+                e.h = int(div_pos(y, head));
+                y -= e.h * head;
+                long long at = 0;                          // of the unit, in its kv head
+                if (by_unit) {
+                    e.pr = int(y);
+                    if (!m && u.np > 1) at = unit_start<M>(&u, tune.kappa, e.pr);
+                } else if (u.np > 1) {
+                    int end = u.np;                        // the last unit that begins at or before y
+#pragma unroll 1
+                    while (end - e.pr > 1) {
+                        const int mid = (e.pr + end) >> 1;
+                        const long long z = unit_start<M>(&u, tune.kappa, mid);
+                        if (z <= y) {
+                            e.pr = mid;
+                            at = z;
+                        } else {
+                            end = mid;
+                        }
+                    }
+                }
+                tiles = u.tiles(e.pr);
+                const int rows = min(u.tpu, (is_group<M>(p, lo) ? sm.rows[lo].n : u.live) - e.pr * u.tpu) * p.G;
+                share = share_of(sm.start[lo] + e.h * sm.head[lo] + at + tune.kappa, tiles, rows, index);
+                if (!by_unit) {
+                    e.j = int(max(0ll, y - at - tune.kappa));
+                    // Short units stay whole: the cut moves to the nearer end of one, and both neighbours see it there
+                    if (tiles <= tune.whole_tiles) e.j = 2 * e.j < tiles ? 0 : tiles;
+                }
+            }
+            if (pass) {
+                const_cast<int2*>(p.units)[job] = share;
+                continue;
+            }
+            // one range ends where the next begins; of m CTAs for each unit, those beyond its pieces have nothing
+            auto cut_at = [&](int k) { return k > share.y ? tiles : int(uint32_t(tiles) * uint32_t(k) / uint32_t(share.y)); };
+            int4 begin = make_int4(entries, 0, 0, 0);
+            if (on) begin = make_int4(e.b, e.h, e.pr, m ? cut_at(job % m) : e.j);
+            if (job < p.ctas) {
+                sm.ends[job] = begin;
+                sm.pieces[job] = share.y;
+            }
+            __syncthreads();
+            if (job < p.ctas) {
+                CtaPlan out{};
+                out.begin = begin;
+                if (!on) {
+                    out.begin.x = -1;
+                } else {
+                    const bool last = job + 1 >= parts;
+                    out.end = m ? make_int4(e.b, e.h, e.pr, cut_at(job % m + 1)) : last ? make_int4(entries, 0, 0, 0) : sm.ends[job + 1];
+                    out.last_pieces = m ? share.y : last ? 0 : sm.pieces[job + 1];
+                    out.first_cta = share.x;
+                    out.first_pieces = share.y;
+                    const SeqRows& r = sm.rows[e.b];
+                    out.rows = make_int4(r.row0, r.n, r.live, r.S);
+                    out.base = sm.base[e.b];
+                }
+                const_cast<CtaPlan*>(p.plan)[job] = out;
+            }
         }
-    } else if (cut.total > 0) {                            // even ranges: one ends where the next begins
-        int2 share = make_int2(0, 0);
-        if (c < cut.parts) {
-            End e = find<M>(p, cut, sm.rows, cut.bound(c));
-            const SeqUnits<M> u = seq_units<M>(p, e.b, sm.rows[e.b]);
-            const int n = u.tiles(e.pr);
-            // Short units stay whole: the cut moves to the nearer end of one, and both neighbours see it there
-            if (n <= Tune::kWholeTiles) e.j = 2 * e.j < n ? 0 : n;
-            share = share_of(e, u, n, 0);
-            out.begin = make_int4(e.b, e.h, e.pr, e.j);
-        }
-        sm.ends[c] = c < cut.parts ? out.begin : make_int4(cut.B, 0, 0, 0);
-        sm.pieces[c] = share.y;
-        __syncthreads();
-        if (c < cut.parts) {
-            const bool last = c + 1 >= cut.parts;
-            out.end = last ? make_int4(cut.B, 0, 0, 0) : sm.ends[c + 1];
-            out.first_cta = share.x;
-            out.first_pieces = share.y;
-            out.last_pieces = last ? 0 : sm.pieces[c + 1];
-        }
-    }
-    if (c < p.ctas) {
-        if (out.begin.x >= 0) {
-            const SeqRows& r = sm.rows[out.begin.x];
-            out.rows = make_int4(r.row0, r.n, r.live, r.S);
-        }
-        const_cast<CtaPlan*>(p.plan)[c] = out;
-    }
-    // ---- the groups' units of 256 rows, for the merge
-    if (M == kChunkShared && !p.row_tiles && is_group<M>(p, 0)) {
-        const long long n = cut.total > 0 ? (long long)cut.Hkv * cut.units[cut.B] : 0;
-        for (int i = tid; i < n; i += kThreads) {
-            const End e = unit_at(p, cut, i);
-            if (!is_group<M>(p, e.b)) break;               // the sequences' come behind them
-            const SeqUnits<M> u = seq_units<M>(p, e.b, sm.rows[e.b]);
-            const_cast<int2*>(p.units)[i] = share_of(e, u, u.tiles(e.pr), i);
-        }
-    }
 }
 
 template <ChunkMode M>
@@ -275,10 +330,40 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         __syncthreads();
     }
     const ChunkParams& p = a.launch[blockIdx.x];
-    if (M == kChunkShared) lay_out_groups(p, a.groups, sm.groups, first);
+    SeqRows mine{0, 0, 0, -1};
+    if (int(threadIdx.x) < p.B) mine = seq_rows(p, threadIdx.x);
+    if (M == kChunkShared) lay_out_groups(p, a.groups, sm.groups, mine, first);
     if (a.launches == 0) return;
-    if (p.row_tiles) lay_out_ranges<M, TuneFew>(p, sm.cut, first);
-    else lay_out_ranges<M, TuneUnits>(p, sm.cut, first);
+    Tuning tune{TuneUnits::kKappa, TuneUnits::kMinTiles, TuneUnits::kMinTilesManyRows, TuneUnits::kWholeTiles, p.ctas};
+    if (p.few_rows) tune = Tuning{TuneFew::kKappa, TuneFew::kMinTiles, TuneFew::kMinTilesManyRows, TuneFew::kWholeTiles, p.ctas};
+    if (M == kChunkShared && a.launches == 2) {
+        // Two launches, the groups' on units of 256 rows with an SM for each CTA and the sequences' with two CTAs to an
+        // SM, run at the same time: each gets SMs by its tiles, which take about as long in both.
+        // (64 sequences of one token, 20 .. 600 tokens of their own behind 8192 shared ones: 89 us one launch after the
+        // other.)
+        if (threadIdx.x < 2) sm.cut.load[threadIdx.x] = 0;
+        __syncthreads();
+        const int g0 = a.launch[1].groups, tpu = a.launch[1].tpu, few_tpu = a.launch[0].tpu;
+        int tiles[2] = {0, 0};
+        if (int(threadIdx.x) < p.B && mine.S >= 0) {
+            const int base = p.skip[threadIdx.x].x / kBN;
+            tiles[0] = (mine.live + few_tpu - 1) / few_tpu * ((mine.S + mine.live + kBN - 1) / kBN - base + TuneFew::kKappa);
+        }
+        if (int(threadIdx.x) < g0) {
+            const int4 e = sm.groups.table[threadIdx.x];
+            if (e.y) tiles[1] = (e.y + tpu - 1) / tpu * (e.z / kBN + TuneUnits::kKappa);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i)
+            if (tiles[i]) atomicAdd(&sm.cut.load[i], float(tiles[i]));
+        __syncthreads();
+        const float own = sm.cut.load[0], shared = sm.cut.load[1];
+        const int sms = a.launch[1].ctas;
+        int for_groups = shared == 0.f ? 0 : min(sms, max(1, int(float(sms) * shared / (shared + own) + 0.5f)));
+        if (own > 0.f) for_groups = min(for_groups, max(1, sms - 1));
+        tune.ctas = p.few_rows ? max(1, p.ctas - int((long long)p.ctas * for_groups / sms)) : max(1, for_groups);
+    }
+    lay_out<M>(p, sm, mine, tune, first);
 }
 
 }  // namespace

@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(256) group_merge_kernel(const ChunkParams p) {
     constexpr int DS = D / 32, kAhead = 8;
     const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
+    grid_dep_wait();                                       // the attention kernels
     if (gw >= (long long)p.T * p.Hq) return;
     const int t = int(gw / p.Hq), hq = int(gw % p.Hq);
     int b;
@@ -171,10 +172,17 @@ int chunk_simt_min_rows(int D, int elem) {
 template cudaError_t launch_chunk_simt<kChunkPlain>(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
 
 cudaError_t launch_group_merge(const ChunkParams& p, cudaStream_t s) {
-    const unsigned blocks = unsigned(((long long)p.T * p.Hq + 7) / 8);
-    if (p.D == 64) group_merge_kernel<64><<<blocks, 256, 0, s>>>(p);
-    else group_merge_kernel<128><<<blocks, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(((long long)p.T * p.Hq + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, p.D == 64 ? group_merge_kernel<64> : group_merge_kernel<128>, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s) {

@@ -474,10 +474,14 @@ __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char
                                    *reinterpret_cast<const int*>(sm + C::kOffMisc + 8), gridDim.x);
     else
         cut = reinterpret_cast<const CtaPlan*>(sm + C::kOffTiles);
-    const End* ends = reinterpret_cast<const End*>(sm + C::kOffEnds);
     __syncwarp();                                          // the lanes' stores come before what is read and stored here
     Walk<M> walk;
-    walk.start(p, ends[0], ends[1], *reinterpret_cast<const SeqRows*>(ends + 2));
+    if constexpr (M == kChunkPlain) {
+        const End* ends = reinterpret_cast<const End*>(sm + C::kOffEnds);
+        walk.start(p, ends[0], ends[1], *reinterpret_cast<const SeqRows*>(ends + 2));
+    } else {
+        walk.start(p, *cut);
+    }
     Seg<M> s;
     Spoil before{};                                        // tokens `from` .. `upto` - 1 of kv head h of sequence b, which
     int b = -1, h = -1, from = 0, upto = 0;                // every row of the units at hand sees
@@ -646,7 +650,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         *redo = 0;
         fence_mbar_init();
     }
-    grid_dep_wait();                                       // trees: the prologue's results
+    grid_dep_wait();                                       // the prologue's or the plan's results
+    if (M != kChunkPlain) grid_dep_release();              // what follows may start where SMs are free
 
     const int me = blockIdx.x;
     Whereabouts<M> cut;
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         cut = plan;
         idle = plan->begin.x < 0;
     }
-    zero_rows<M, D>(p, tid, C::kThreads);
+    if (M == kChunkPlain || idle) zero_rows<M, D>(p, tid, C::kThreads);
     if (idle) {                                            // nothing to compute
         __syncthreads();
         if (warp == kWarpMma) tmem_dealloc(*tmem_slot, kTmemCols);
@@ -697,10 +702,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 if (warp == 0) *first_rows = entry_rows<M>(p, e.b);
             }
         }
-    } else if (tid == 0) {
-        ends[0] = End{cut->begin.x, cut->begin.y, cut->begin.z, cut->begin.w};
-        ends[1] = End{cut->end.x, cut->end.y, cut->end.z, cut->end.w};
-        *first_rows = SeqRows{cut->rows.x, cut->rows.y, cut->rows.z, cut->rows.w};
     }
 
     tc_fence_before();
@@ -709,7 +710,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     const uint32_t tbase = *tmem_slot;
     const uint32_t sbase = smem_u32(sm);
     Walk<M> walk;
-    walk.start(p, ends[0], ends[1], *first_rows);
+    if constexpr (M == kChunkPlain) walk.start(p, ends[0], ends[1], *first_rows);
+    else walk.start(p, *cut);
     Seg<M> sg;
 
     if (E4M3 && warp >= kWarpConv) {
@@ -1207,6 +1209,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
         }
     }
 
+    if (M != kChunkPlain && warp >= kWarpK && warp < kWarpMma)   // the producers are done long before the others
+        zero_rows<M, D>(p, tid - 32 * kWarpK, 32 * (kWarpMma - kWarpK));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -23,7 +23,7 @@ struct TuneUnits {                   // units of 256 rows (chunk_tc.cuh)
     static constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
     static constexpr int kWholeTiles = 4;
 };
-struct TuneFew {                     // units of up to 32 rows (chunk_few.cuh)
+struct TuneFew {                     // units of 8 or 16 rows (chunk_few.cuh)
     static constexpr int kKappa = 3;
     static constexpr int kMinTiles = 2, kMinTilesManyRows = 2;
     static constexpr int kWholeTiles = 2;
@@ -121,8 +121,9 @@ struct SeqUnits : UnitsOf<M> {
         return s;
     }
 };
+// `base`: with shared prefixes, the first tile of a sequence's own units.
 template <ChunkMode M>
-__device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v, const SeqRows& r) {
+__device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v, const SeqRows& r, int base) {
     SeqUnits<M> u;
     u.tree = !p.offsets;
     u.tpu = p.tpu;
@@ -139,14 +140,19 @@ __device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v, co
         u.sink_tiles = (p.sinks + kBN - 1) / kBN;
     }
     if constexpr (M == kChunkShared) {
-        const bool group = is_group<M>(p, v);
-        u.base = group ? 0 : p.skip[sequence_of<M>(p, v)].x / kBN;
-        if (group) {                                       // every unit over the shared tokens alone
+        u.base = base;
+        if (is_group<M>(p, v)) {                           // every unit over the shared tokens alone
             u.tree = true;
             u.live = 0;
         }
     }
     return u;
+}
+template <ChunkMode M>
+__device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v, const SeqRows& r) {
+    int base = 0;
+    if (M == kChunkShared && !is_group<M>(p, v)) base = p.skip[sequence_of<M>(p, v)].x / kBN;
+    return seq_units<M>(p, v, r, base);
 }
 template <ChunkMode M>
 __device__ __forceinline__ SeqUnits<M> seq_units(const ChunkParams& p, int v) {
@@ -176,14 +182,25 @@ __device__ __forceinline__ int unit_pieces(int n, int rows, int m) {
     return min(m, max(1, n / (rows > 64 ? Tune::kMinTilesManyRows : Tune::kMinTiles)));
 }
 
-// The cut of a batch: the prefix sums and the KV tiles of its longest unit.
-template <ChunkMode M, class Tune>
-__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest, int ctas) {
+// The shares of the cut of a batch of n units: the total is there, `longest` the tiles of its longest unit.
+template <class Tune>
+__device__ __forceinline__ void share_cut(Cut& cut, long long n, int longest, int ctas) {
     // A range that holds pieces of two units pays the fixed cost twice, so where there is less
     // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
     // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
     // 42 and 29), unless one long unit among short ones would then run far longer than its
     // share of all tiles
+    cut.m = 0;
+    if (cut.total < (long long)(Tune::kKappa + 2) * ctas && n <= ctas && n > 0) {
+        const int m = ctas / int(n);
+        if (longest / unit_pieces<Tune>(longest, 1, m) <= int(cut.total) / ctas + 2 * Tune::kKappa) cut.m = m;
+    }
+    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)ctas, max(1ll, cut.total / (Tune::kKappa + 1))));
+}
+
+// The cut of a batch: the prefix sums and the KV tiles of its longest unit.
+template <ChunkMode M, class Tune>
+__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest, int ctas) {
     Cut cut;
     const int entries = chunk_entries<M>(p);
     const long long n = (long long)p.Hkv * units[entries];
@@ -193,12 +210,7 @@ __device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* til
     cut.Hkv = p.Hkv;
     cut.k = Tune::kKappa;
     cut.total = p.Hkv * tiles[entries] + Tune::kKappa * n;
-    cut.m = 0;
-    if (cut.total < (long long)(Tune::kKappa + 2) * ctas && n <= ctas && n > 0) {
-        const int m = ctas / int(n);
-        if (longest / unit_pieces<Tune>(longest, 1, m) <= int(cut.total) / ctas + 2 * Tune::kKappa) cut.m = m;
-    }
-    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)ctas, max(1ll, cut.total / (Tune::kKappa + 1))));
+    share_cut<Tune>(cut, n, longest, ctas);
     return cut;
 }
 
@@ -392,13 +404,22 @@ struct Walk {
         u = seq_units<M>(*p, e.b, rows);
     }
     __device__ __forceinline__ void start(const ChunkParams& pp, const End& a, const End& z, const SeqRows& r) {
+        start(pp, a, z, r, seq_units<M>(pp, a.b < chunk_entries<M>(pp) ? a.b : 0, r));
+    }
+    __device__ __forceinline__ void start(const ChunkParams& pp, const CtaPlan& plan) {
+        const SeqRows r{plan.rows.x, plan.rows.y, plan.rows.z, plan.rows.w};
+        start(pp, End{plan.begin.x, plan.begin.y, plan.begin.z, plan.begin.w},
+              End{plan.end.x, plan.end.y, plan.end.z, plan.end.w}, r, seq_units<M>(pp, plan.begin.x, r, plan.base));
+    }
+    // rows and units: of entry a.b
+    __device__ __forceinline__ void start(const ChunkParams& pp, const End& a, const End& z, const SeqRows& r,
+                                          const SeqUnits<M>& su) {
         p = &pp;
         e = a;
         end = z;
-        rows = r;                                          // of entry a.b
-        const bool any = e.b < chunk_entries<M>(pp);
-        u = seq_units<M>(pp, any ? e.b : 0, r);
-        if (any && e.j >= u.tiles(e.pr)) advance();
+        rows = r;
+        u = su;
+        if (e.b < chunk_entries<M>(pp) && e.j >= u.tiles(e.pr)) advance();
     }
     __device__ __forceinline__ bool next(Seg<M>& s) {
         // behind the range: also where both its ends were moved to the same unit's end

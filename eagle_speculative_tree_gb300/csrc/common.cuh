@@ -235,7 +235,8 @@ struct ChunkLayout {
 struct alignas(16) CtaPlan {
     int4 begin, end;
     int4 rows;                                // SeqRows of the first entry
-    int32_t first_cta, first_pieces, last_pieces, unused;
+    int32_t first_cta, first_pieces, last_pieces;
+    int32_t base;                             // shared: the first tile of the first entry's units
 };
 struct ChunkParams {
     const void* q;
@@ -259,7 +260,8 @@ struct ChunkParams {
     int num_splits, split_tokens, rows_block; // SIMT
     int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
     int tpu;                                  //             tokens per unit
-    int rows_tile, row_tiles;                 // few rows: rows of a tile, 8 or 16; tiles of a unit, 1 or 2
+    int behind_groups;                        // few rows: the launch before is the groups', not the plan
+    int few_rows;                             // few rows: rows of a unit, 8 or 16; 0: units of 256
     float scale_log2;
     uint64_t wait_ns;
     int window, sinks;                        // kChunkWindow: >= 1, >= 0, both at most 2^30
