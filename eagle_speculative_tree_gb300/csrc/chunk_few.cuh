@@ -11,8 +11,8 @@
 // rows waste nothing.  A lane reads 16 bytes of K at a time, which permutes the head elements (Q's alike);
 // V^T is transposed on the way from shared memory (ldmatrix), P^T by movmatrix.
 //
-// A CTA is four such warps and two that fill the K and V rings by TMA, two CTAs to an SM.  Warp w takes
-// half w, w + 4, .. of the unit's KV tiles.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
+// A CTA is four such warps and two that fill the K and V rings by TMA, two CTAs to an SM; the warps take the
+// steps of the CTA's range in turn.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
 // of a unit (or piece) the warps' states are joined through shared memory.
 //
 // e4m3: K's codes are widened to f16 (exact), and Q, scaled by a power of two per row, with them: f16
@@ -42,27 +42,34 @@ constexpr int kStep = 32;                // tokens a warp takes at a time
 constexpr uint32_t kRegsCompute = 168, kRegsProduce = 88;
 constexpr int kWarpFewK = kWarps, kWarpFewV = kWarps + 1;
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NR>
 struct CfgFew {
-    static constexpr int kNP = D / 64;
-    static constexpr int kPanel = kBN * 128;
-    static constexpr int kTile = E4M3 ? kBN * D : kNP * kPanel;
-    static constexpr int kNS = 32 * 1024 / kTile > 6 ? 6 : 32 * 1024 / kTile;   // stages of the K ring, and of the V ring
+    static constexpr int kNP = E4M3 ? 1 : D / 64;         // panels of a stage
+    static constexpr int kRowBytes = E4M3 ? D : 128;      // of a token in a panel
+    static constexpr int kPanel = kStep * kRowBytes;
+    static constexpr int kStage = kNP * kPanel;           // a step of K or V: one warp's
+    static constexpr int kPitch = D + 4;                  // floats of a row of a warp's part
+    static constexpr int kPartBytes = kWarps * 8 * NR * (kPitch * 4 + 8);
+    // Stages of the K ring, and of the V ring: one or two for each warp, as two CTAs to an SM leave room.  Stage s is
+    // always warp s % 4's: a parity tells a warp that waits for a use of a stage from the use before
+    // it only, so no use may be another warp's (its data may land later than that of a step behind it)
+    static constexpr int kRoom = (113 * 1024 - 2560 - kPartBytes) / (2 * (kStage + (E4M3 ? kStep * 4 : 0)));
+    static constexpr int kNS = kRoom >= 2 * kWarps ? 2 * kWarps : kWarps;
     struct Bars {
         uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS], part_full, part_empty;
     };
-    static constexpr int kPitch = D + 4;                  // floats of a row of a warp's part
     static constexpr int kOffK = 0;
-    static constexpr int kOffV = kOffK + kNS * kTile;
-    static constexpr int kOffScale = kOffV + kNS * kTile;                      // [K, V][kNS][64]
-    static constexpr int kOffPart = kOffScale + (E4M3 ? 2 * kNS * kBN * 4 : 0);
-    static constexpr int kOffMl = kOffPart + kWarps * 16 * kPitch * 4;         // [kWarps][16] (m, l)
-    static constexpr int kOffBar = kOffMl + kWarps * 16 * 8;
+    static constexpr int kOffV = kOffK + kNS * kStage;
+    static constexpr int kOffScale = kOffV + kNS * kStage;                     // [K, V][kNS][kStep]
+    static constexpr int kOffPart = kOffScale + (E4M3 ? 2 * kNS * kStep * 4 : 0);   // [kWarps][8 NR] rows
+    static constexpr int kOffMl = kOffPart + kWarps * 8 * NR * kPitch * 4;     // [kWarps][8 NR] (m, l)
+    static constexpr int kOffBar = kOffMl + kWarps * 8 * NR * 8;
     static constexpr int kOffMisc = kOffBar + int(sizeof(Bars));
-    static constexpr int kOffEnds = (kOffMisc + 16 + 15) / 16 * 16;   // the CTA's plan
-    static constexpr int kOffSeg = kOffEnds + int(sizeof(CtaPlan));   // [kWarps] a warp's walk and segment
+    static constexpr int kOffEnds = (kOffMisc + 16 + 15) / 16 * 16;            // the CTA's plan
+    static constexpr int kOffSeg = kOffEnds + int(sizeof(CtaPlan));            // [kWarps] a warp's walk and segment
     static constexpr int kSmemBytes = kOffSeg + kWarps * 256;
-    static_assert(kOffBar % 8 == 0 && kOffEnds % 16 == 0 && kOffSeg % 8 == 0 && kOffMl % 8 == 0, "alignment");
+    static_assert(kOffV % 1024 == 0 && kOffScale % 64 == 0 && kOffPart % 16 == 0 && kOffBar % 8 == 0 && kOffSeg % 8 == 0 &&
+                      kRoom >= kWarps, "alignment");
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs to an SM");
 };
 
@@ -216,51 +223,52 @@ __device__ __noinline__ void join_rows(const ChunkParams& p, const Seg<M>& s, in
     }
 }
 
-// One warp streams the tiles of K (or V) of a segment, and their scales, into a ring.  Lanes 0 .. 3 own a
-// page each.  A page that some row of the unit sees a token of arrives by TMA, whole, whatever its other tokens hold;
+// One warp streams the steps of K (or V) of a segment, and their scales, into a ring.  Lanes 0 and 1 own a page
+// each.  A page that some row of the unit sees a token of arrives by TMA, whole, whatever its other tokens hold;
 // one whose id is bad (flagged) is written by the warp as zeros; others are left as they are.  `g`
-// counts tiles over the CTA's life.  False after a timeout or an abort.
-template <int D, bool E4M3, ChunkMode M>
-__device__ __forceinline__ bool produce_tiles(const ChunkParams& p, const CUtensorMap* map, const float* scales,
+// counts steps over the CTA's life.  False after a timeout or an abort.
+template <int D, bool E4M3, int NR, ChunkMode M>
+__device__ __forceinline__ bool produce_steps(const ChunkParams& p, const CUtensorMap* map, const float* scales,
                                               unsigned char* ring, float* sring, uint64_t* full, uint64_t* empty,
                                               const Seg<M>& s, int& g, volatile uint32_t* abort_flag) {
-    using C = CfgFew<D, E4M3>;
+    using C = CfgFew<D, E4M3, NR>;
     constexpr int kNS = C::kNS, kPageBytes = 16 * D * (E4M3 ? 1 : 2);
-    const int lane = threadIdx.x & 31, sub = lane & 3;
+    const int lane = threadIdx.x & 31, sub = lane & 1;
     const int* ptab = p.page_table + size_t(s.sequence()) * p.max_pages;
-    const int t1 = s.t1, ntiles = s.ntiles, h = s.h;
+    const int t1 = s.t1, nsteps = 2 * s.ntiles, h = s.h;
+    auto place = [&](int i) { return s.place(i >> 1) + (i & 1) * kStep + sub * 16; };   // of the lane's page of step i
     auto needed = [&](int pos) -> bool {
         if constexpr (M == kChunkWindow) return pos < t1 && (pos + 16 > s.low || pos < p.sinks);
         return pos < t1;
     };
-    auto fetch = [&](int bi) -> int {                      // page ids of 8 tiles, one warp-wide load
-        const int jt = 8 * bi + (lane >> 2), pos = s.place(jt) + sub * 16;
-        return jt < ntiles && needed(pos) ? __ldg(ptab + (pos >> 4)) : -1;
+    auto fetch = [&](int bi) -> int {                      // page ids of 16 steps, one warp-wide load
+        const int i = 16 * bi + (lane >> 1), pos = place(i);
+        return i < nsteps && needed(pos) ? __ldg(ptab + (pos >> 4)) : -1;
     };
     int cur = fetch(0), nxt = fetch(1);
-    for (int j = 0; j < ntiles; ++j, ++g) {
+    for (int i = 0; i < nsteps; ++i, ++g) {
         const int st = g % kNS;
-        if (j > 0 && (j & 7) == 0) {
+        if (i > 0 && (i & 15) == 0) {
             cur = nxt;
-            nxt = fetch(j / 8 + 1);
+            nxt = fetch(i / 16 + 1);
         }
-        const int page = __shfl_sync(0xffffffffu, cur, (j & 7) * 4 + sub);
-        const bool mine = lane < 4 && needed(s.place(j) + sub * 16), ok = page >= 0 && page < p.num_pool_pages;
+        const int page = __shfl_sync(0xffffffffu, cur, (i & 15) * 2 + sub);
+        const bool mine = lane < 2 && needed(place(i)), ok = page >= 0 && page < p.num_pool_pages;
         if (g >= kNS && !mbar_wait_bounded(&empty[st], ((g / kNS) - 1) & 1, p.wait_ns)) {
             *abort_flag = 1;
             atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
         }
         if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-        unsigned char* dst = ring + st * C::kTile;
+        unsigned char* dst = ring + st * C::kStage;
         const unsigned bad = __ballot_sync(0xffffffffu, mine && !ok), by_tma = __ballot_sync(0xffffffffu, mine && ok);
         if (bad) {
             if (lane == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
             for (unsigned w = bad; w; w &= w - 1) {
                 const int pg = __ffs(w) - 1;
-                constexpr int kRun = kPageBytes / (E4M3 ? 1 : C::kNP) / 16;   // words of 16 bytes in a panel
-                for (int e = lane; e < kPageBytes / 16; e += 32)
+                constexpr int kRun = C::kRowBytes;         // words of 16 bytes of a page in a panel
+                for (int e = lane; e < C::kNP * kRun; e += 32)
                     *reinterpret_cast<uint4*>(dst + e / kRun * C::kPanel + (pg * kRun + e % kRun) * 16) = make_uint4(0, 0, 0, 0);
-                if (E4M3 && lane < 16) sring[st * kBN + pg * 16 + lane] = 0.f;
+                if (E4M3 && lane < 16) sring[st * kStep + pg * 16 + lane] = 0.f;
             }
             fence_proxy_async_smem();                      // the next use of the stage may be by TMA
             __syncwarp();
@@ -270,7 +278,7 @@ __device__ __forceinline__ bool produce_tiles(const ChunkParams& p, const CUtens
         if (mine && ok) {
             if constexpr (E4M3) {
                 tma_load_3d(dst + lane * kPageBytes, map, 0, h, page * 16, &full[st]);
-                bulk_load_64(sring + st * kBN + lane * 16, scales + (size_t(page) * p.Hkv + h) * kPage, &full[st]);
+                bulk_load_64(sring + st * kStep + lane * 16, scales + (size_t(page) * p.Hkv + h) * kPage, &full[st]);
             } else {
 #pragma unroll
                 for (int pn = 0; pn < C::kNP; ++pn)
@@ -285,7 +293,7 @@ __device__ __forceinline__ bool produce_tiles(const ChunkParams& p, const CUtens
 template <int D, bool E4M3, int NR, ChunkMode M>
 __global__ void __launch_bounds__(kFewThreads, 2)
     chunk_few_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
-    using C = CfgFew<D, E4M3>;
+    using C = CfgFew<D, E4M3, NR>;
     using Bars = typename C::Bars;
     constexpr int kNS = C::kNS;
     constexpr int NM = D / 16;                             // tiles of 16 head elements
@@ -305,9 +313,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (tid == 0) {
         for (int s = 0; s < kNS; ++s) {
             mbar_init(&bars->k_full[s], 1);
-            mbar_init(&bars->k_empty[s], 2);               // the warps that take a half of the tile
+            mbar_init(&bars->k_empty[s], 1);               // a step is one warp's
             mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->v_empty[s], 2);
+            mbar_init(&bars->v_empty[s], 1);
         }
         mbar_init(&bars->part_full, 32 * kWarps);
         mbar_init(&bars->part_empty, 32 * kWarps);
@@ -344,10 +352,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
         int armed = 0;
         while (walk.next(s))
-            if (!produce_tiles<D, E4M3, M>(p, is_v ? &tmv : &tmk, is_v ? p.v_scales : p.k_scales,
-                                           sm + (is_v ? C::kOffV : C::kOffK),
-                                           reinterpret_cast<float*>(sm + C::kOffScale) + (is_v ? kNS * kBN : 0), full, empty, s,
-                                           armed, abort_flag))
+            if (!produce_steps<D, E4M3, NR, M>(p, is_v ? &tmv : &tmk, is_v ? p.v_scales : p.k_scales,
+                                               sm + (is_v ? C::kOffV : C::kOffK),
+                                               reinterpret_cast<float*>(sm + C::kOffScale) + (is_v ? kNS * kStep : 0), full,
+                                               empty, s, armed, abort_flag))
                 break;
         tcparts::ProducerArgs a{};                         // only what the drain looks at
         a.full = full;
@@ -360,8 +368,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     regs_raise<kRegsCompute>();
     if (idle) return;
     const int g = lane >> 2, q = lane & 3;
-    float* part = reinterpret_cast<float*>(sm + C::kOffPart) + warp * 16 * C::kPitch;
-    float2* part_ml = reinterpret_cast<float2*>(sm + C::kOffMl) + warp * 16;
+    float* part = reinterpret_cast<float*>(sm + C::kOffPart) + warp * kRows * C::kPitch;
+    float2* part_ml = reinterpret_cast<float2*>(sm + C::kOffMl) + warp * kRows;
     // a wait of the whole warp: false for all of its lanes after a timeout of one, or when the CTA has been told to stop
     auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns) && *abort_flag == 0);
@@ -387,9 +395,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     int koff[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) koff[c] = E4M3 ? g * D + q * (D / 4) + c * 16 : int(sw128_offset(g, 2 * q + c));
-    constexpr int kRowBytes = E4M3 ? D : 128;              // of a row of a tile's panel
+    constexpr int kRowBytes = C::kRowBytes;
     bool alive = true;
-    int ring = 0;                                          // tiles over the CTA's life
+    int ring = 0;                                          // steps over the CTA's life
     int segs = 0;
     while (alive && next()) {
         // ---- Q: row g + 8 h of the warp's; matrix instruction kk has the elements of `inner`
@@ -449,13 +457,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 for (int i = 0; i < 4; ++i) o[t][h][i] = 0.f;
         }
 
-        // the warp's steps of the segment: halves of a KV tile
-        for (int step = warp; step < 2 * ntiles; step += kWarps) {
-            const int j = step >> 1, st = (ring + j) % kNS;
-            const uint32_t ph = ((ring + j) / kNS) & 1;
-            const int half = (step & 1) * kStep, pos0 = s.place(j) + half;
-            const unsigned char* kt = sm + C::kOffK + st * C::kTile + half * kRowBytes;
-            const unsigned char* vt = sm + C::kOffV + st * C::kTile + half * kRowBytes;
+        // the warp's steps of the segment, each a half of a KV tile: of all steps of the CTA, numbers warp, warp + 4, ..
+        for (int step = (warp - ring) & (kWarps - 1); step < 2 * ntiles; step += kWarps) {
+            const int st = (ring + step) % kNS;
+            const uint32_t ph = ((ring + step) / kNS) & 1;
+            const int pos0 = s.place(step >> 1) + (step & 1) * kStep;
+            const unsigned char* kt = sm + C::kOffK + st * C::kStage;
+            const unsigned char* vt = sm + C::kOffV + st * C::kStage;
             bool any = pos0 < t1;                          // some row sees a token
             if constexpr (M == kChunkWindow) any = any && (pos0 + kStep > low || pos0 < p.sinks);
             if (!ready(&bars->k_full[st], ph)) { alive = false; break; }
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
             }
             if constexpr (E4M3) {
-                const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) + st * kBN + half + g;
+                const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) + st * kStep + g;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -599,7 +607,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 }
             if (!ready(&bars->v_full[st], ph)) { alive = false; break; }
             if constexpr (E4M3) {                          // P times V's scale: one rounding, to bf16
-                const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) + kNS * kBN + st * kBN + half + g;
+                const float* scl = reinterpret_cast<const float*>(sm + C::kOffScale) + (kNS + st) * kStep + g;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -628,16 +636,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 if constexpr (M == kChunkWindow) dead = dead || (pos < low && pos >= p.sinks);
                 if (dead) {
 #pragma unroll
-                    for (int e = 0; e < (E4M3 ? D / 16 : 8 * C::kNP); ++e)
+                    for (int e = 0; e < C::kNP * kRowBytes / 16; ++e)
                         *reinterpret_cast<uint4*>(const_cast<unsigned char*>(vt) + (e >> 3) * C::kPanel + lane * kRowBytes +
                                                   (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();              // the stage's next use is by TMA
                 }
                 __syncwarp();
-                constexpr int kWords = kStep * kRowBytes / 4;   // of a panel's rows of the step
 #pragma unroll 1
-                for (int e = lane; e < (E4M3 ? 1 : C::kNP) * kWords; e += 32) {
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + e / kWords * C::kPanel + e % kWords * 4);
+                for (int e = lane; e < C::kStage / 4; e += 32) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + e * 4);
                     if constexpr (E4M3) odd |= (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
                     else odd |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
                 }
@@ -722,7 +729,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             if (lane == 0) mbar_arrive(&bars->v_empty[st]);
         }
         if (!alive) break;
-        ring += ntiles;
+        ring += 2 * ntiles;
 
         // ---- the warps' states of the unit's rows, joined through shared memory
         if (segs > 0 && !ready(&bars->part_empty, (segs - 1) & 1)) { alive = false; break; }
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             for (int e = 0; e < DS; ++e) acc[e] = 0.f;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) {
-                x[k] = reinterpret_cast<const float2*>(sm + C::kOffMl)[k * 16 + r];
+                x[k] = reinterpret_cast<const float2*>(sm + C::kOffMl)[k * kRows + r];
                 top = fmaxf(top, x[k].x);
             }
 #pragma unroll
@@ -761,7 +768,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 const float w = state_weight(x[k].x, x[k].y, top);
                 if (w < 0.f) continue;
                 sum = fmaf(x[k].y, w, sum);
-                const float* src = reinterpret_cast<const float*>(sm + C::kOffPart) + (k * 16 + r) * C::kPitch + lane * DS;
+                const float* src = reinterpret_cast<const float*>(sm + C::kOffPart) + (k * kRows + r) * C::kPitch + lane * DS;
                 float y[DS];
                 if constexpr (DS == 4) {
                     const float4 z = *reinterpret_cast<const float4*>(src);
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 template <int D, bool E4M3, int NR, ChunkMode M>
 cudaError_t launch_few(const ChunkParams& p, cudaStream_t s) {
-    using C = CfgFew<D, E4M3>;
+    using C = CfgFew<D, E4M3, NR>;
     if (p.ctas < 1 || p.ctas > kChunkMaxCtas || p.tpu < 1 || p.tpu * p.G > 8 * NR)
         return cudaErrorInvalidValue;
     CUtensorMap mk = {}, mv = {};

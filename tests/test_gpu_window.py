@@ -257,3 +257,35 @@ def test_tree_shared(ts, cuda_device, case, dtype, e4m3, kernel):
     ref, spread, reach = tree64(p, q, parents.cpu().numpy())
     check_attention(out, ref, spread, reach, max(S + n for S, n in zip(p.prefix, p.new)), dim, dtype,
                     on_tensor_cores(ts, p, kernel))
+
+
+# ------------------------------------------------------------------------------ few rows, long ragged ranges
+
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (64, 4, 128), (16, 8, 64), (12, 1, 64)])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_decoded_tokens_of_many_ragged_sequences(ts, cuda_device, hq, hkv, dim, e4m3):
+    """Ranges of many units of odd numbers of tiles, so that their steps and ring stages fall to other warps each time;
+    several calls, which have to agree to the bit."""
+    rng = np.random.default_rng([hq, dim])
+    prefix = [int(x) for x in rng.integers(0, 4000, 45)] + [0, 1, 63, 64, 2999]
+    p = make(cuda_device, prefix, [1] * len(prefix), hq, hkv, dim, "bf16", e4m3, seed=dim)
+    window, sinks = 1501, 70
+    assert drop_pages(p, window, sinks) > 100
+    assert check_chunk_window(ts, p, window, sinks) == 0
+    first, _ = run_chunk_window(ts, p, window, sinks)
+    for _ in range(5):
+        assert torch.equal(run_chunk_window(ts, p, window, sinks)[0], first)
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(32, 8, 128), (64, 4, 64)])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_decoded_tokens_behind_shared_prefixes(ts, cuda_device, hq, hkv, dim, e4m3):
+    rng = np.random.default_rng([hq, dim, 1])
+    groups = [(1000, [int(x) for x in rng.integers(0, 900, 20)]), (3007, [int(x) for x in rng.integers(0, 300, 17)]),
+              (130, [int(x) for x in rng.integers(0, 2500, 9)])]
+    B = sum(len(own) for _, own in groups)
+    p, go, sl = make_shared(cuda_device, groups, [1] * B, hq, hkv, dim, "bf16", e4m3, seed=dim)
+    assert check_chunk_shared(ts, p, go, sl) == 0
+    first, _ = run_chunk_shared(ts, p, go, sl)
+    for _ in range(5):
+        assert torch.equal(run_chunk_shared(ts, p, go, sl)[0], first)
