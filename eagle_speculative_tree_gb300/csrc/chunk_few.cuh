@@ -11,8 +11,8 @@
 // rows waste nothing.  A lane reads 16 bytes of K at a time, which permutes the head elements (Q's alike);
 // V^T is transposed on the way from shared memory (ldmatrix), P^T by movmatrix.
 //
-// A CTA is four such warps and two that fill the K and V rings by TMA, two CTAs to an SM; the warps take the
-// steps of the CTA's range in turn.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
+// A CTA is four such warps, two that fill the K and V rings by TMA and one that walks along the CTA's range and
+// hands its segments on, ahead of the others; two CTAs to an SM.  The warps take the steps of the range in turn.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
 // of a unit (or piece) the warps' states are joined through shared memory.
 //
 // e4m3: K's codes are widened to f16 (exact), and Q, scaled by a power of two per row, with them: f16
@@ -40,7 +40,8 @@ constexpr int kFewThreads = 256;         // and a warpgroup of which two warps p
 constexpr int kStep = 32;                // tokens a warp takes at a time
 // registers of the computing warps and of the others: 128 (168 + 88) = 256 x the 128 of the launch
 constexpr uint32_t kRegsCompute = 168, kRegsProduce = 88;
-constexpr int kWarpFewK = kWarps, kWarpFewV = kWarps + 1;
+constexpr int kWarpFewK = kWarps, kWarpFewV = kWarps + 1, kWarpWalk = kWarps + 2;
+constexpr int kSegRing = 4;              // segments that the walking warp is ahead, at most
 
 template <int D, bool E4M3, int NR>
 struct CfgFew {
@@ -56,7 +57,8 @@ struct CfgFew {
     static constexpr int kRoom = (113 * 1024 - 2560 - kPartBytes) / (2 * (kStage + (E4M3 ? kStep * 4 : 0)));
     static constexpr int kNS = kRoom >= 2 * kWarps ? 2 * kWarps : kWarps;
     struct Bars {
-        uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS], part_full, part_empty;
+        uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS], part_full, part_empty, seg_full[kSegRing],
+            seg_empty[kSegRing];
     };
     static constexpr int kOffK = 0;
     static constexpr int kOffV = kOffK + kNS * kStage;
@@ -66,8 +68,8 @@ struct CfgFew {
     static constexpr int kOffBar = kOffMl + kWarps * 8 * NR * 8;
     static constexpr int kOffMisc = kOffBar + int(sizeof(Bars));
     static constexpr int kOffEnds = (kOffMisc + 16 + 15) / 16 * 16;            // the CTA's plan
-    static constexpr int kOffSeg = kOffEnds + int(sizeof(CtaPlan));            // [kWarps] a warp's walk and segment
-    static constexpr int kSmemBytes = kOffSeg + kWarps * 256;
+    static constexpr int kOffSeg = kOffEnds + int(sizeof(CtaPlan));            // [kSegRing] segments
+    static constexpr int kSmemBytes = kOffSeg + kSegRing * 128;
     static_assert(kOffV % 1024 == 0 && kOffScale % 64 == 0 && kOffPart % 16 == 0 && kOffBar % 8 == 0 && kOffSeg % 8 == 0 &&
                       kRoom >= kWarps, "alignment");
     static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs to an SM");
@@ -223,37 +225,43 @@ __device__ __noinline__ void join_rows(const ChunkParams& p, const Seg<M>& s, in
     }
 }
 
+// Whether a row of the unit sees a token of the page at `pos` (of its sequence, in the segment).
+template <ChunkMode M>
+__device__ __forceinline__ bool needed_page(const ChunkParams& p, const Seg<M>& s, int pos) {
+    if constexpr (M == kChunkWindow) return pos < s.t1 && (pos + 16 > s.low || pos < p.sinks);
+    return pos < s.t1;
+}
+// Page ids of the segment's steps 16 i .. 16 i + 15, two lanes each, by one warp-wide load.
+template <ChunkMode M>
+__device__ __forceinline__ int step_pages(const ChunkParams& p, const Seg<M>& s, int i) {
+    const int lane = threadIdx.x & 31, step = 16 * i + (lane >> 1);
+    const int pos = s.place(step >> 1) + (step & 1) * kStep + (lane & 1) * 16;
+    if (step >= 2 * s.ntiles || !needed_page<M>(p, s, pos)) return -1;
+    return __ldg(p.page_table + size_t(s.sequence()) * p.max_pages + (pos >> 4));
+}
+
 // One warp streams the steps of K (or V) of a segment, and their scales, into a ring.  Lanes 0 and 1 own a page
 // each.  A page that some row of the unit sees a token of arrives by TMA, whole, whatever its other tokens hold;
-// one whose id is bad (flagged) is written by the warp as zeros; others are left as they are.  `g`
-// counts steps over the CTA's life.  False after a timeout or an abort.
+// one whose id is bad (flagged) is written by the warp as zeros; others are left as they are.  `cur`: the
+// first page ids.  `g` counts steps over the CTA's life.  False after a timeout or an abort.
 template <int D, bool E4M3, int NR, ChunkMode M>
 __device__ __forceinline__ bool produce_steps(const ChunkParams& p, const CUtensorMap* map, const float* scales,
                                               unsigned char* ring, float* sring, uint64_t* full, uint64_t* empty,
-                                              const Seg<M>& s, int& g, volatile uint32_t* abort_flag) {
+                                              const Seg<M>& s, int cur, int& g, volatile uint32_t* abort_flag) {
     using C = CfgFew<D, E4M3, NR>;
     constexpr int kNS = C::kNS, kPageBytes = 16 * D * (E4M3 ? 1 : 2);
     const int lane = threadIdx.x & 31, sub = lane & 1;
-    const int* ptab = p.page_table + size_t(s.sequence()) * p.max_pages;
-    const int t1 = s.t1, nsteps = 2 * s.ntiles, h = s.h;
+    const int nsteps = 2 * s.ntiles, h = s.h;
     auto place = [&](int i) { return s.place(i >> 1) + (i & 1) * kStep + sub * 16; };   // of the lane's page of step i
-    auto needed = [&](int pos) -> bool {
-        if constexpr (M == kChunkWindow) return pos < t1 && (pos + 16 > s.low || pos < p.sinks);
-        return pos < t1;
-    };
-    auto fetch = [&](int bi) -> int {                      // page ids of 16 steps, one warp-wide load
-        const int i = 16 * bi + (lane >> 1), pos = place(i);
-        return i < nsteps && needed(pos) ? __ldg(ptab + (pos >> 4)) : -1;
-    };
-    int cur = fetch(0), nxt = fetch(1);
+    int nxt = step_pages<M>(p, s, 1);
     for (int i = 0; i < nsteps; ++i, ++g) {
         const int st = g % kNS;
         if (i > 0 && (i & 15) == 0) {
             cur = nxt;
-            nxt = fetch(i / 16 + 1);
+            nxt = step_pages<M>(p, s, i / 16 + 1);
         }
         const int page = __shfl_sync(0xffffffffu, cur, (i & 15) * 2 + sub);
-        const bool mine = lane < 2 && needed(place(i)), ok = page >= 0 && page < p.num_pool_pages;
+        const bool mine = lane < 2 && needed_page<M>(p, s, place(i)), ok = page >= 0 && page < p.num_pool_pages;
         if (g >= kNS && !mbar_wait_bounded(&empty[st], ((g / kNS) - 1) & 1, p.wait_ns)) {
             *abort_flag = 1;
             atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
@@ -317,6 +325,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             mbar_init(&bars->v_full[s], 1);
             mbar_init(&bars->v_empty[s], 1);
         }
+        for (int s = 0; s < kSegRing; ++s) {
+            mbar_init(&bars->seg_full[s], 1);
+            mbar_init(&bars->seg_empty[s], kWarps + 2);    // its readers
+        }
         mbar_init(&bars->part_full, 32 * kWarps);
         mbar_init(&bars->part_empty, 32 * kWarps);
         *abort_flag = 0;
@@ -335,28 +347,85 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         reinterpret_cast<uint32_t*>(sm + C::kOffEnds)[tid] = reinterpret_cast<const uint32_t*>(p.plan + me)[tid];
     __syncthreads();
     const bool idle = plan.begin.x < 0;                    // nothing to compute
+    // a wait of the whole warp: false for all of its lanes after a timeout of one, or when the CTA has been told to stop
+    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns) && *abort_flag == 0);
+    };
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        if (lane == 0) atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+    };
+    struct Slot {                                          // segment i of the CTA's range, or the end of it
+        Seg<M> seg;
+        int more;
+    };
+    static_assert(sizeof(Slot) <= 128, "a slot of the ring of segments");
+    auto slot = [&](int i) -> Slot& { return *reinterpret_cast<Slot*>(sm + C::kOffSeg + (i & (kSegRing - 1)) * 128); };
+    auto seg_ready = [&](int i) { return ready(&bars->seg_full[i & (kSegRing - 1)], (i / kSegRing) & 1); };
+    auto seg_done = [&](int i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->seg_empty[i & (kSegRing - 1)]);
+    };
     if (warp >= kWarps) {
         regs_lower<kRegsProduce>();
-        if (warp > kWarpFewV) {
-            zero_rows<M, D>(p, tid - 32 * (kWarpFewV + 1), kFewThreads - 32 * (kWarpFewV + 1));
+        if (warp > kWarpWalk) {
+            zero_rows<M, D>(p, lane, 32);
             if (p.behind_groups) grid_dep_wait();
             return;
         }
         if (idle) return;
-        Walk<M> walk;
-        walk.start(p, plan);
-        Seg<M> s;
+        if (warp == kWarpWalk) {
+            // ------------------------------------------------------------ segments
+            Walk<M> walk;
+            walk.start(p, plan);
+            bool more = true;
+            for (int i = 0; more; ++i) {
+                Seg<M> s;
+                more = walk.next(s);
+                if (i >= kSegRing && !ready(&bars->seg_empty[i & (kSegRing - 1)], (i / kSegRing - 1) & 1)) {
+                    give_up();
+                    break;
+                }
+                if (lane == 0) {
+                    if (more) slot(i).seg = s;
+                    slot(i).more = more;
+                    mbar_arrive(&bars->seg_full[i & (kSegRing - 1)]);
+                }
+            }
+            return;
+        }
         // ---------------------------------------------------------------- TMA producers
         const bool is_v = warp == kWarpFewV;
         uint64_t* full = is_v ? bars->v_full : bars->k_full;
         uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
-        int armed = 0;
-        while (walk.next(s))
+        int armed = 0, ids = 0;
+        Seg<M> s{}, nxt{};
+        auto take = [&](int i, Seg<M>& to, int& pages) -> bool {   // segment i and its first page ids
+            if (!seg_ready(i)) {
+                give_up();
+                return false;
+            }
+            const bool more = slot(i).more != 0;
+            if (more) {
+                to = slot(i).seg;
+                pages = step_pages<M>(p, to, 0);
+            }
+            seg_done(i);
+            return more;
+        };
+        bool more = take(0, s, ids);
+        for (int i = 1; more; ++i) {
+            int next_ids = 0;
+            const bool next_more = take(i, nxt, next_ids);   // its page ids are on their way while this one is copied
             if (!produce_steps<D, E4M3, NR, M>(p, is_v ? &tmv : &tmk, is_v ? p.v_scales : p.k_scales,
                                                sm + (is_v ? C::kOffV : C::kOffK),
                                                reinterpret_cast<float*>(sm + C::kOffScale) + (is_v ? kNS * kStep : 0), full,
-                                               empty, s, armed, abort_flag))
+                                               empty, s, ids, armed, abort_flag))
                 break;
+            s = nxt;
+            ids = next_ids;
+            more = next_more;
+        }
         tcparts::ProducerArgs a{};                         // only what the drain looks at
         a.full = full;
         a.nst = kNS;
@@ -370,39 +439,16 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const int g = lane >> 2, q = lane & 3;
     float* part = reinterpret_cast<float*>(sm + C::kOffPart) + warp * kRows * C::kPitch;
     float2* part_ml = reinterpret_cast<float2*>(sm + C::kOffMl) + warp * kRows;
-    // a wait of the whole warp: false for all of its lanes after a timeout of one, or when the CTA has been told to stop
-    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_ns) && *abort_flag == 0);
-    };
-    // The walk and the segment at hand stand in shared memory, to leave the registers to O: lane 0 walks
-    struct Place {
-        Walk<M> walk;
-        Seg<M> seg;
-    };
-    static_assert(sizeof(Place) <= 256, "a warp's place in shared memory");
-    Place& place = *reinterpret_cast<Place*>(sm + C::kOffSeg + warp * 256);
-    if (lane == 0) place.walk.start(p, plan);
-    const Seg<M>& s = place.seg;
-    auto next = [&]() -> bool {
-        __syncwarp();                                      // the lanes are done with the last segment
-        int more = 0;
-        if (lane == 0) more = place.walk.next(place.seg);
-        more = __shfl_sync(0xffffffffu, more, 0);
-        __syncwarp();
-        return more != 0;
-    };
     // bytes of the lane's chunk c of row g of K in a tile's panel
     int koff[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) koff[c] = E4M3 ? g * D + q * (D / 4) + c * 16 : int(sw128_offset(g, 2 * q + c));
     constexpr int kRowBytes = C::kRowBytes;
-    bool alive = true;
     int ring = 0;                                          // steps over the CTA's life
     int segs = 0;
-    while (alive && next()) {
-        // ---- Q: row g + 8 h of the warp's; matrix instruction kk has the elements of `inner`
-        uint32_t qb[NR][NM][2];
-        float sc[NR][2];                                   // of a score of rows 2 q, 2 q + 1, to base 2
+    // Q of a segment, row g + 8 h; matrix instruction kk has the elements of `inner`
+    uint32_t qb[NR][NM][2];
+    auto load_q = [&](const Seg<M>& s) {
 #pragma unroll
         for (int h = 0; h < NR; ++h) {
             const Row r = few_row<M>(p, s, 8 * h + g, D);
@@ -414,6 +460,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 qb[h][kk][0] = x.x;
                 qb[h][kk][1] = x.y;
             }
+        }
+    };
+    bool alive = seg_ready(0), more = alive && slot(0).more;
+    if (more) load_q(slot(0).seg);
+    while (alive && more) {
+        const Seg<M>& s = slot(segs).seg;
+        float sc[NR][2];                                   // of a score of rows 2 q, 2 q + 1, to base 2
+#pragma unroll
+        for (int h = 0; h < NR; ++h) {
             float f = p.scale_log2;
             if constexpr (E4M3) {                          // to f16, the largest element to 2^14 .. 2^15
                 uint32_t top = 0;                          // its bits; a row with a NaN or an infinity is spoiled anyway
@@ -749,8 +804,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int i = 0; i < 2; ++i) dst[E4M3 ? g * (D / 8) + 2 * t + i : 16 * t + 8 * i + g] = o[t][h][2 * i + b];
             }
         mbar_arrive(&bars->part_full);
+        // the next segment's Q is on its way while this one's rows are joined
+        if (!seg_ready(segs + 1)) { alive = false; break; }
+        more = slot(segs + 1).more;
+        if (more) load_q(slot(segs + 1).seg);
         if (!ready(&bars->part_full, segs & 1)) { alive = false; break; }
-        ++segs;
         const bool whole = s.whole(), head = s.j0 == 0;
 #pragma unroll 4
         for (int r = warp; r < used; r += kWarps) {
@@ -802,11 +860,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 join_rows<D, M>(p, s, c0, pieces, warp, used);
             }
         }
+        seg_done(segs);
+        ++segs;
     }
-    if (!alive) {
-        *abort_flag = 1;
-        if (lane == 0) atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
-    }
+    if (!alive) give_up();
 }
 
 template <int D, bool E4M3, int NR, ChunkMode M>
