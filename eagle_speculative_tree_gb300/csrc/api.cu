@@ -561,6 +561,7 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int Hkv, int D
     L.anc = take(size_t(tree_rows) * kAncWords * 8);
     L.lens = take(tree_rows ? size_t(batch) * 4 : 0);
     L.nn = take(tree_rows ? size_t(batch) * 4 : 0);
+    L.flags = take(tree_rows && x.mode != kChunkPlain ? size_t(batch) * 4 : 0);
     L.depth = take(x.mode == kChunkWindow ? size_t(tree_rows) * 4 : 0);
     L.gtab = take(size_t(x.groups) * 16);
     L.skip = take(x.groups ? size_t(batch) * 8 : 0);
@@ -672,6 +673,11 @@ ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const Ch
     return chunk_layout(c, rows, s.num_q_heads, s.num_kv_heads, s.head_dim, rows, s.batch, x);
 }
 
+// Whether a plan kernel runs, which also clears what the call needs zeroed.
+bool planned(const ChunkExtra& x, const ChunkPlan& c) {
+    return x.mode == kChunkShared || (x.mode == kChunkWindow && c.kernel == TREESPEC_KERNEL_TC_STREAM);
+}
+
 // What the attention calls share once their arguments are checked.
 int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const ChunkExtra& x, const GroupParams& g,
               unsigned char* ws, int dtype, int kv_dtype, cudaStream_t st) {
@@ -724,14 +730,15 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
         if (err == cudaSuccess) g_launches++;
         return err;
     };
-    if (shared || (tc && x.mode == kChunkWindow)) {
-        PlanParams plan{};                               // chunks: also clears the status word and the counters
+    if (planned(x, c)) {
+        PlanParams plan{};                               // also clears the status word and the counters
         plan.groups = g;
         plan.launches = !tc ? 0 : c.few_ctas && c.ctas ? 2 : 1;
         plan.launch[0] = c.few_ctas ? few : p;
         plan.launch[1] = p;
         plan.cleared = p.status;
-        plan.clear = p.offsets ? int((lay.cleared - lay.status) / 4) : 0;
+        plan.clear = int((lay.cleared - lay.status) / 4);
+        plan.flags = p.offsets ? nullptr : reinterpret_cast<uint32_t*>(ws + lay.flags);
         e = launch(launch_chunk_plan(plan, x.mode, st));
         if (e != cudaSuccess) return launch_failed(e);
     }
@@ -797,8 +804,7 @@ int attend_chunks(const void* q, const void* k_pages, const void* v_pages, const
     p.num_pool_pages = s.num_pool_pages;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool planned = x.mode == kChunkShared || (x.mode == kChunkWindow && plan.kernel == TREESPEC_KERNEL_TC_STREAM);
-    if (!planned)
+    if (!planned(x, plan))
         if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
     return run_chunk(p, plan, lay, x, g, ws, s.dtype, s.kv_dtype, st);
 }
@@ -860,7 +866,10 @@ int attend_trees(const void* q, const void* k_pages, const void* v_pages, const 
     a.max_pages = s.max_pages_per_seq;
     a.ps = kPage;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess) return launch_failed(e);
+    if (planned(x, plan))
+        a.flags = reinterpret_cast<uint32_t*>(ws + lay.flags);
+    else if (const cudaError_t e = cudaMemsetAsync(ws + lay.status, 0, lay.cleared, st); e != cudaSuccess)
+        return launch_failed(e);
     const cudaError_t e = launch_tree_prologue(a, st);
     if (e != cudaSuccess) return launch_failed(e);
     g_launches++;

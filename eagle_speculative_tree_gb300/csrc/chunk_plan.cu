@@ -330,11 +330,14 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         __syncthreads();
     }
     const ChunkParams& p = a.launch[blockIdx.x];
+    if (first && a.flags)
+        for (int b = threadIdx.x; b < p.B; b += kThreads)
+            if (const uint32_t st = a.flags[b]) atomicOr(p.status, st);
     SeqRows mine{0, 0, 0, -1};
     if (int(threadIdx.x) < p.B) mine = seq_rows(p, threadIdx.x);
     if (M == kChunkShared) lay_out_groups(p, a.groups, sm.groups, mine, first);
     if (a.launches == 0) return;
-    Tuning tune{TuneUnits::kKappa, TuneUnits::kMinTiles, TuneUnits::kMinTilesManyRows, TuneUnits::kWholeTiles, p.ctas};
+    Tuning tune{TuneUnits::kKappa, 2, TuneUnits::kMinTilesManyRows, TuneUnits::kWholeTiles, p.ctas};
     if (p.few_rows) tune = Tuning{TuneFew::kKappa, TuneFew::kMinTiles, TuneFew::kMinTilesManyRows, TuneFew::kWholeTiles, p.ctas};
     if (M == kChunkShared && a.launches == 2) {
         // Two launches, the groups' on units of 256 rows with an SM for each CTA and the sequences' with two CTAs to an

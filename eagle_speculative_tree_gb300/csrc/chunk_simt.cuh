@@ -239,23 +239,6 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
     }
 
     const int live_rows = min(rows, sq.live * p.G - r0);  // rows of a padded tree's other slots lie behind them
-#pragma unroll 4
-    for (int e = tid; e < RW * 8 * D; e += nthr) {
-        const int lr = e / D;
-        Qs[e] = lr < live_rows ? load_q<T>(p.q, at_s[lr] + e % D) * p.scale_log2 : 0.f;
-    }
-    if constexpr (M == kChunkWindow) {
-        for (int lr = tid; lr < rows; lr += nthr) {
-            const int i = (r0 + lr) / p.G;
-            low_s[lr] = S - p.window + 1 + (p.offsets ? i : p.depth[size_t(b) * p.N + i]);
-        }
-    }
-    if (!p.offsets && !group) {
-        for (int e = tid; e < rows * kAncWords; e += nthr)
-            anc_s[e / kAncWords][e % kAncWords] =
-                p.anc[(size_t(b) * p.N + (r0 + e / kAncWords) / p.G) * kAncWords + e % kAncWords];
-    }
-
     const int* ptab = p.page_table + size_t(b) * p.max_pages;
     auto issue = [&](int tile, int stage) {
         const int base = t0 + tile * TT;
@@ -307,6 +290,24 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
         asm volatile("cp.async.commit_group;\n" ::);
     };
 
+    issue(0, 0);                                           // the first tile is on its way while Q is read
+#pragma unroll 4
+    for (int e = tid; e < RW * 8 * D; e += nthr) {
+        const int lr = e / D;
+        Qs[e] = lr < live_rows ? load_q<T>(p.q, at_s[lr] + e % D) * p.scale_log2 : 0.f;
+    }
+    if constexpr (M == kChunkWindow) {
+        for (int lr = tid; lr < rows; lr += nthr) {
+            const int i = (r0 + lr) / p.G;
+            low_s[lr] = S - p.window + 1 + (p.offsets ? i : p.depth[size_t(b) * p.N + i]);
+        }
+    }
+    if (!p.offsets && !group) {
+        for (int e = tid; e < rows * kAncWords; e += nthr)
+            anc_s[e / kAncWords][e % kAncWords] =
+                p.anc[(size_t(b) * p.N + (r0 + e / kAncWords) / p.G) * kAncWords + e % kAncWords];
+    }
+
     float m[8], l[8], acc[8][DS];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
     const int ntiles = (t1 - t0 + TT - 1) / TT;
     float* pt_w = Pt + warp * 256;
 
-    issue(0, 0);
     for (int tile = 0; tile < ntiles; ++tile) {
         if (tile + 1 < ntiles) issue(tile + 1, (tile + 1) & 1);
         else asm volatile("cp.async.commit_group;\n" ::);
@@ -402,9 +402,12 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
                     const unsigned who = __shfl_sync(0xffffffffu, seen_by, t);
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        if (!((who >> r) & 1u)) continue;
+                        const bool on = (who >> r) & 1u;       // chosen, not branched on: the rows' chains overlap
 #pragma unroll
-                        for (int e = 0; e < DS; ++e) acc[r][e] = fmaf(pr[r], vf[e], acc[r][e]);
+                        for (int e = 0; e < DS; ++e) {
+                            const float y = fmaf(pr[r], vf[e], acc[r][e]);
+                            acc[r][e] = on ? y : acc[r][e];
+                        }
                     }
                 }
             }

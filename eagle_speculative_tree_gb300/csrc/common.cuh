@@ -111,6 +111,7 @@ struct AttnParams {
     int32_t* stream_flags;        // persistent two-tile kernel: [2 * CTAs][2] a piece's partial is written
                                   // (slot, query tile); zeroed by the prologue
     uint64_t wait_ns;             // bound of the tensor-core kernels' pipeline waits (kDefaultWaitNs unless a test shortens it)
+    uint32_t* flags;              // [B] a sequence's status bits, in place of setting them in the status word; NULL: no
     int32_t* depth;               // [B][N] depth of each node, and ancestor sets within the window alone; NULL: no window
     int window, sinks;
 };
@@ -226,7 +227,7 @@ enum ChunkMode {
 };
 struct ChunkLayout {
     // [status, cleared): zeroed before every call
-    size_t status, counters, few_counters, cleared, anc, lens, nn, depth, gtab, skip, group_units, units, plan, few_plan, ml,
+    size_t status, counters, few_counters, cleared, anc, lens, nn, flags, depth, gtab, skip, group_units, units, plan, few_plan, ml,
         acc, few_ml, few_acc, rows_ml, rows_acc, total;
 };
 // One CTA's range of KV tiles (chunk_plan.cu), as (entry, kv head, unit, tile) of its first tile and of the
@@ -290,6 +291,7 @@ struct GroupParams {
 struct PlanParams {
     ChunkParams launch[2];
     GroupParams groups;
+    const uint32_t* flags;                    // [B] status bits of the tree prologue, or NULL
     uint32_t* cleared;
     int launches, clear;
 };

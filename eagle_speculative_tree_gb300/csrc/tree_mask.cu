@@ -75,7 +75,8 @@ __global__ void __launch_bounds__(kMaxNodes) tree_prologue_kernel(AttnParams p) 
         bool ok = S >= 0 && need <= (long long)p.max_pages * p.ps;
         p.lens[b] = ok ? S : -1;
         uint32_t st = (bad ? TREESPEC_STATUS_BAD_PARENT : 0u) | (ok ? 0u : TREESPEC_STATUS_BAD_LENGTH);
-        if (st) atomicOr(p.status, st);
+        if (p.flags) p.flags[b] = st;                     // the plan collects them
+        else if (st) atomicOr(p.status, st);
     }
 }
 
