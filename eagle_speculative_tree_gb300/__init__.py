@@ -636,9 +636,9 @@ def chunk_attn_workspace_bytes(prob: ChunkProblem) -> int:
 
 
 def _attend_chunks(fn, need, q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales,
-                   kernel, workspace, stream, groups=(), more=()) -> torch.Tensor:
-    """An attention call over packed chunks: `need` gives the workspace bytes of a problem, `groups`
-    are (group_offsets, shared_lens), `more` the call's whole numbers behind the shape."""
+                   kernel, workspace, stream, need_args=(), more=(), groups=()) -> torch.Tensor:
+    """An attention call over packed chunks: need(problem, *need_args) gives its workspace bytes, `more`
+    are the call's whole numbers behind the shape, `groups` (group_offsets, shared_lens)."""
     dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
         raise _float_type_error(q)
@@ -651,12 +651,12 @@ def _attend_chunks(fn, need, q, k_pages, v_pages, page_table, prefix_lens, chunk
     if groups:
         wants += _group_wants(*groups)
     if out is None:
-        out = _fresh(q.shape, dt, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _fresh(q.shape, dt, q.device, stream)   # q is contiguous
     else:
         wants.append((out, "out", dt, q.shape))
     _need_all(index, *wants)
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        workspace = _workspace_for(workspace, need(ChunkProblem(*sizes)), index, q.device, stream)
+        workspace = _workspace_for(workspace, need(ChunkProblem(*sizes), *need_args), index, q.device, stream)
     _launch(index, stream, fn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales),
             _ptr(v_scales), page_table.data_ptr(), prefix_lens.data_ptr(), chunk_offsets.data_ptr(),
             *[t.data_ptr() for t in groups], out.data_ptr(), _chunk_struct(*sizes), *more, workspace.data_ptr(),
@@ -687,7 +687,7 @@ def attn_e4m3_workspace_bytes(prob: AttnProblem) -> int:
 
 
 def _attend_trees(fn, need, q, k_pages, v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel,
-                  workspace, stream, groups=(), more=()) -> torch.Tensor:
+                  workspace, stream, need_args=(), more=(), groups=()) -> torch.Tensor:
     """A verification call over any pools; arguments as for _attend_chunks."""
     dt = getattr(q, "dtype", None)
     if dt is not _BF16 and dt is not _F32:
@@ -704,7 +704,7 @@ def _attend_trees(fn, need, q, k_pages, v_pages, k_scales, v_scales, page_table,
     if groups:
         wants += _group_wants(*groups)
     if out is None:
-        out = _fresh(q.shape, dt, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _fresh(q.shape, dt, q.device, stream)   # q is contiguous
     else:
         wants.append((out, "out", dt, q.shape))
     _need_all(index, *wants)
@@ -712,7 +712,7 @@ def _attend_trees(fn, need, q, k_pages, v_pages, k_scales, v_scales, page_table,
     if D2 != D:
         raise ValueError("head_dim of q and k_pages differ")
     if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
-        workspace = _workspace_for(workspace, need(attn_problem(q, k_pages, page_table, kernel=kernel)), index, q.device,
+        workspace = _workspace_for(workspace, need(attn_problem(q, k_pages, page_table, kernel=kernel), *need_args), index, q.device,
                                    stream)
     _launch(index, stream, fn, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scales), _ptr(v_scales),
             page_table.data_ptr(), prefix_lens.data_ptr(), tree_parents.data_ptr(), *[t.data_ptr() for t in groups],
@@ -774,12 +774,16 @@ def tree_kv_commit_e4m3(k_pages, v_pages, k_scales, v_scales, page_table, prefix
 
 # --------------------------------------------- sliding windows and shared prefixes
 
-def _group_wants(group_offsets, shared_lens) -> tuple:
+def _groups_of(group_offsets, shared_lens) -> int:
     _need_tensors(group_offsets=group_offsets, shared_lens=shared_lens)
-    if shared_lens.dim() != 1 or shared_lens.shape[0] < 1:
+    if shared_lens.dim() != 1 or shared_lens.numel() < 1:
         raise ValueError("shared_lens must have shape [groups], with one group at least")
-    return ((group_offsets, "group_offsets", _I32, (shared_lens.shape[0] + 1,)),
-            (shared_lens, "shared_lens", _I32, shared_lens.shape))
+    return shared_lens.numel()
+
+
+def _group_wants(group_offsets, shared_lens) -> tuple:
+    n = shared_lens.numel()
+    return (group_offsets, "group_offsets", _I32, (n + 1,)), (shared_lens, "shared_lens", _I32, (n,))
 
 
 def _window_of(window, sinks) -> tuple:
@@ -829,9 +833,8 @@ def tree_chunk_attn_window(q, k_pages, v_pages, page_table, prefix_lens, chunk_o
     first `sinks` tokens; see include/treespec.h.  Pages that no row sees are not read, and their
     entries in page_table may hold anything."""
     w = _window_of(window, sinks)
-    return _attend_chunks(_lib.tree_chunk_attn_window, lambda prob: chunk_window_workspace_bytes(prob, *w), q, k_pages,
-                          v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace,
-                          stream, (), w)
+    return _attend_chunks(_lib.tree_chunk_attn_window, chunk_window_workspace_bytes, q, k_pages, v_pages, page_table,
+                          prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace, stream, w, w)
 
 
 def tree_attn_verify_window(q, k_pages, v_pages, page_table, prefix_lens, tree_parents, window: int, sinks: int = 0,
@@ -844,10 +847,9 @@ def tree_attn_verify_window(q, k_pages, v_pages, page_table, prefix_lens, tree_p
     q [B][N][Hq][D], k_pages / v_pages in the same type or float8_e4m3fn with k_scales /
     v_scales, the rest as for tree_attn_verify."""
     w = _window_of(window, sinks)
-    kv = _kv_dtype(q, k_pages)
-    return _attend_trees(_lib.tree_attn_verify_window, lambda prob: attn_window_workspace_bytes(prob, kv, *w), q, k_pages,
-                         v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel, workspace, stream,
-                         (), (kv, *w))
+    more = (_kv_dtype(q, k_pages), *w)
+    return _attend_trees(_lib.tree_attn_verify_window, attn_window_workspace_bytes, q, k_pages, v_pages, k_scales, v_scales,
+                         page_table, prefix_lens, tree_parents, out, kernel, workspace, stream, more, more)
 
 
 def tree_chunk_attn_shared(q, k_pages, v_pages, page_table, prefix_lens, chunk_offsets, group_offsets, shared_lens,
@@ -857,12 +859,10 @@ def tree_chunk_attn_shared(q, k_pages, v_pages, page_table, prefix_lens, chunk_o
     sequences group_offsets[g] .. group_offsets[g + 1] - 1 have their first shared_lens[g] tokens
     in common.  group_offsets [groups + 1] and shared_lens [groups] int32 on the device; see
     include/treespec.h."""
-    groups = (group_offsets, shared_lens)
-    _group_wants(*groups)
-    n = shared_lens.shape[0]
-    return _attend_chunks(_lib.tree_chunk_attn_shared, lambda prob: chunk_shared_workspace_bytes(prob, n), q, k_pages,
-                          v_pages, page_table, prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace,
-                          stream, groups, (n,))
+    n = _groups_of(group_offsets, shared_lens)
+    return _attend_chunks(_lib.tree_chunk_attn_shared, chunk_shared_workspace_bytes, q, k_pages, v_pages, page_table,
+                          prefix_lens, chunk_offsets, out, k_scales, v_scales, kernel, workspace, stream, (n,), (n,),
+                          (group_offsets, shared_lens))
 
 
 def tree_attn_verify_shared(q, k_pages, v_pages, page_table, prefix_lens, tree_parents, group_offsets, shared_lens,
@@ -870,12 +870,10 @@ def tree_attn_verify_shared(q, k_pages, v_pages, page_table, prefix_lens, tree_p
                             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Tree verification of a batch whose sequences share prefixes; groups as for
     tree_chunk_attn_shared, pools as for tree_attn_verify_window.  See include/treespec.h."""
-    groups = (group_offsets, shared_lens)
-    _group_wants(*groups)
-    n, kv = shared_lens.shape[0], _kv_dtype(q, k_pages)
-    return _attend_trees(_lib.tree_attn_verify_shared, lambda prob: attn_shared_workspace_bytes(prob, kv, n), q, k_pages,
-                         v_pages, k_scales, v_scales, page_table, prefix_lens, tree_parents, out, kernel, workspace, stream,
-                         groups, (kv, n))
+    more = (_kv_dtype(q, k_pages), _groups_of(group_offsets, shared_lens))
+    return _attend_trees(_lib.tree_attn_verify_shared, attn_shared_workspace_bytes, q, k_pages, v_pages, k_scales, v_scales,
+                         page_table, prefix_lens, tree_parents, out, kernel, workspace, stream, more, more,
+                         (group_offsets, shared_lens))
 
 
 def read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -523,10 +523,14 @@ int tree_kv_commit_e4m3(void *k_pages, void *v_pages, float *k_scales, float *v_
  * lengths, offsets and pages are those of tree_chunk_attn and tree_attn_verify /
  * tree_attn_verify_e4m3.  Of the tree calls, shape->dtype is that of q and out and kv_dtype that
  * of the pools (the same, or TREESPEC_DTYPE_E4M3 with scales; else the scales are not used);
- * shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q), num_splits is not used.
+ * shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q), num_splits is not used.  AUTO takes, of bf16
+ * queries, by their rows per sequence (tokens x query heads per kv head, the mean of the batch): up
+ * to 16 a kernel bound by the reading of the cache, else TC_STREAM, units of 256 rows.
+ * Of trees, all calls give a node the rows of its logical index in the pages (prefix_lens[b] + i).
  */
 
-/* Workspace bytes of the two window calls (0 if the arguments are invalid). */
+/* Workspace bytes of the two window calls (0 if the arguments are invalid): on tensor cores about
+ * tree_chunk_attn's, or an eighth of it for batches of few rows. */
 size_t treespec_chunk_window_workspace_bytes(const treespec_chunk_shape *shape, int32_t window, int32_t sinks);
 size_t treespec_attn_window_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t window,
                                             int32_t sinks);
@@ -555,7 +559,8 @@ int tree_attn_verify_window(const void *q, const void *k_pages, const void *v_pa
                             int32_t kv_dtype, int32_t window, int32_t sinks, void *workspace,
                             size_t workspace_bytes, treespec_stream_t stream);
 
-/* Workspace bytes of the two calls over shared prefixes (0 if the arguments are invalid). */
+/* Workspace bytes of the two calls over shared prefixes (0 if the arguments are invalid): on tensor cores
+ * tree_chunk_attn's, some 5 MB and two float32 states of every row: 8 (D + 2) bytes a token and query head. */
 size_t treespec_chunk_shared_workspace_bytes(const treespec_chunk_shape *shape, int32_t num_groups);
 size_t treespec_attn_shared_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t num_groups);
 
