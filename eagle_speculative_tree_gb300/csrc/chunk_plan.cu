@@ -37,7 +37,7 @@ struct CutSmem {
     int pieces[kChunkMaxCtas];
     long long warp_size[32], warp_units[32];
     unsigned long long rows_sum;
-    float load[2];                                         // tiles of the sequences' units and of the groups'
+    unsigned long long load[2];                                         // tiles of the sequences' units and of the groups'
     int longest;
 };
 struct PlanSmem {
@@ -107,6 +107,7 @@ __device__ __forceinline__ void lay_out_groups(const ChunkParams& p, const Group
         const int k = b == tid ? mine_of : group_of(b);
         skip[b] = k < 0 ? make_int2(0, 0) : make_int2(sm.share[k], k);
     }
+    __syncthreads();                                       // the cut reads other threads' sequences
 }
 
 struct Tuning {
@@ -358,9 +359,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         }
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
-            if (tiles[i]) atomicAdd(&sm.cut.load[i], float(tiles[i]));
+            if (tiles[i]) atomicAdd(&sm.cut.load[i], (unsigned long long)tiles[i]);
         __syncthreads();
-        const float own = sm.cut.load[0], shared = 1.4f * sm.cut.load[1];
+        const float own = float(sm.cut.load[0]), shared = 1.4f * float(sm.cut.load[1]);
         const int sms = a.launch[1].ctas;
         int for_groups = shared == 0.f ? 0 : min(sms, max(1, int(float(sms) * shared / (shared + own) + 0.5f)));
         if (own > 0.f) for_groups = min(for_groups, max(1, sms - 1));
