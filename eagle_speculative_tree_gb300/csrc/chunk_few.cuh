@@ -40,7 +40,7 @@ constexpr int kFewThreads = 256;         // and a warpgroup of which two warps p
 constexpr int kStep = 32;                // tokens a warp takes at a time
 // registers of the computing warps and of the others: 128 (168 + 88) = 256 x the 128 of the launch
 constexpr uint32_t kRegsCompute = 168, kRegsProduce = 88;
-constexpr int kWarpFewK = kWarps, kWarpFewV = kWarps + 1, kWarpWalk = kWarps + 2;
+constexpr int kWarpProduce = kWarps, kWarpWalk = kWarps + 2;   // the first of two that produce; the one that walks
 constexpr int kSegRing = 4;              // segments that the walking warp is ahead, at most
 
 template <int D, bool E4M3, int NR>
@@ -56,6 +56,7 @@ struct CfgFew {
     // it only, so no use may be another warp's (its data may land later than that of a step behind it)
     static constexpr int kRoom = (113 * 1024 - 2560 - kPartBytes) / (2 * (kStage + (E4M3 ? kStep * 4 : 0)));
     static constexpr int kNS = kRoom >= 2 * kWarps ? 2 * kWarps : kWarps;
+    static constexpr bool kPairs = kNS == 2 * kWarps;     // the tile that a producing warp takes is a quarter of the ring
     struct Bars {
         uint64_t k_full[kNS], k_empty[kNS], v_full[kNS], v_empty[kNS], part_full, part_empty, seg_full[kSegRing],
             seg_empty[kSegRing];
@@ -113,6 +114,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+__device__ __forceinline__ void copy_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// An arrival once all the thread's copies so far are there.
+__device__ __forceinline__ void arrive_behind_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
@@ -231,67 +239,97 @@ __device__ __forceinline__ bool needed_page(const ChunkParams& p, const Seg<M>& 
     if constexpr (M == kChunkWindow) return pos < s.t1 && (pos + 16 > s.low || pos < p.sinks);
     return pos < s.t1;
 }
-// Page ids of the segment's steps 16 i .. 16 i + 15, two lanes each, by one warp-wide load.
+// Page ids of the segment's KV tiles 8 i .. 8 i + 7, four lanes each, by one warp-wide load.
 template <ChunkMode M>
-__device__ __forceinline__ int step_pages(const ChunkParams& p, const Seg<M>& s, int i) {
-    const int lane = threadIdx.x & 31, step = 16 * i + (lane >> 1);
-    const int pos = s.place(step >> 1) + (step & 1) * kStep + (lane & 1) * 16;
-    if (step >= 2 * s.ntiles || !needed_page<M>(p, s, pos)) return -1;
+__device__ __forceinline__ int tile_pages(const ChunkParams& p, const Seg<M>& s, int i) {
+    const int lane = threadIdx.x & 31, tile = 8 * i + (lane >> 2), pos = s.place(tile) + (lane & 3) * 16;
+    if (tile >= s.ntiles || !needed_page<M>(p, s, pos)) return -1;
     return __ldg(p.page_table + size_t(s.sequence()) * p.max_pages + (pos >> 4));
 }
 
-// One warp streams the steps of K (or V) of a segment, and their scales, into a ring.  Lanes 0 and 1 own a page
-// each.  A page that some row of the unit sees a token of arrives by TMA, whole, whatever its other tokens hold;
-// one whose id is bad (flagged) is written by the warp as zeros; others are left as they are.  `cur`: the
-// first page ids.  `g` counts steps over the CTA's life.  False after a timeout or an abort.
+// One of the two producing warps fills the rings with a segment's K, V and scales.  An iteration is a chain of a
+// wait, two votes, an arrival and the issue of the copies, about 1 us however little it copies.  With
+// two steps to a computing warp (kPairs) it therefore takes the whole KV tile, K and V of two steps, and the
+// warps take every second tile of the CTA; as one warp for K and one for V, a step at a time, the computing
+// warps waited for them (32 tokens over e4m3 windows of up to 2063: 59 us so, 49 this way).  With one step to a
+// warp V of a step would hold up K of the next, so there the warps are one for K and one for V (64 tokens over bf16
+// windows of up to 4100: 223 us in tiles, 174 this way).
+//
+// Lanes 4 i .. 4 i + 3 own page i of the iteration, the first of them its TMA copy and each a quarter of its
+// scales, which come by plain asynchronous copies (a 64-byte bulk copy each takes as long to issue as a page).
+// A page that some row of the unit sees a token of arrives whole, whatever its other tokens hold; one whose id is bad
+// (flagged) is written by the warp as zeros; others are left as they are.  `cur`: the ids of
+// tile_pages(0).  `ring` counts steps over the CTA's life.  False after a timeout or an abort.
 template <int D, bool E4M3, int NR, ChunkMode M>
-__device__ __forceinline__ bool produce_steps(const ChunkParams& p, const CUtensorMap* map, const float* scales,
-                                              unsigned char* ring, float* sring, uint64_t* full, uint64_t* empty,
-                                              const Seg<M>& s, int cur, int& g, volatile uint32_t* abort_flag) {
+__device__ __forceinline__ bool produce(const ChunkParams& p, const CUtensorMap* tmk, const CUtensorMap* tmv, unsigned char* sm,
+                                        typename CfgFew<D, E4M3, NR>::Bars* bars, const Seg<M>& s, int cur, int ring, int who,
+                                        int& armed, volatile uint32_t* abort_flag) {
     using C = CfgFew<D, E4M3, NR>;
-    constexpr int kNS = C::kNS, kPageBytes = 16 * D * (E4M3 ? 1 : 2);
-    const int lane = threadIdx.x & 31, sub = lane & 1;
-    const int nsteps = 2 * s.ntiles, h = s.h;
-    auto place = [&](int i) { return s.place(i >> 1) + (i & 1) * kStep + sub * 16; };   // of the lane's page of step i
-    int nxt = step_pages<M>(p, s, 1);
-    for (int i = 0; i < nsteps; ++i, ++g) {
-        const int st = g % kNS;
+    constexpr int kNS = C::kNS, kPageBytes = 16 * D * (E4M3 ? 1 : 2), kSteps = C::kPairs ? 2 : 1;
+    constexpr int kPages = C::kPairs ? 8 : 2, kBars = C::kPairs ? 4 : 1;   // of an iteration: (K, V), step, page; (K, V), step
+    const int lane = threadIdx.x & 31, h = s.h;
+    // the lane's page
+    const int pi = lane >> 2, half = C::kPairs ? (pi >> 1) & 1 : 0, sub = pi & 1;
+    const bool page_is_v = C::kPairs ? pi >= 4 : who == 1;
+    unsigned char* const pages = sm + (page_is_v ? C::kOffV : C::kOffK) + sub * 16 * C::kRowBytes;
+    float* const lines = reinterpret_cast<float*>(sm + C::kOffScale) + (page_is_v ? kNS * kStep : 0) + sub * 16 + (lane & 3) * 4;
+    const CUtensorMap* map = page_is_v ? tmv : tmk;
+    const float* scales = (page_is_v ? p.v_scales : p.k_scales) + (lane & 3) * 4;
+    uint64_t* const page_full = page_is_v ? bars->v_full : bars->k_full;
+    // the barrier of lanes 0 .. kBars - 1, and its pages among the lanes that issue copies
+    const int bar_half = C::kPairs ? lane & 1 : 0;
+    const bool bar_is_v = C::kPairs ? (lane & 2) != 0 : who == 1;
+    uint64_t* const bar_full = bar_is_v ? bars->v_full : bars->k_full;
+    uint64_t* const bar_empty = bar_is_v ? bars->v_empty : bars->k_empty;
+    const unsigned bar_pages = 0x11u << (C::kPairs ? 8 * (lane & 3) : 0);
+    static_assert(!C::kPairs || (kBars == 4 && kPages == 8), "lanes 2 v + half of the barriers, 4 v + 2 half + sub of the pages");
+    int nxt = tile_pages<M>(p, s, 1);
+    for (int i = 0; i < 2 * s.ntiles; i += kSteps) {
+        const int j = i >> 1, g = ring + i;
         if (i > 0 && (i & 15) == 0) {
             cur = nxt;
-            nxt = step_pages<M>(p, s, i / 16 + 1);
+            nxt = tile_pages<M>(p, s, j / 8 + 1);
         }
-        const int page = __shfl_sync(0xffffffffu, cur, (i & 15) * 2 + sub);
-        const bool mine = lane < 2 && needed_page<M>(p, s, place(i)), ok = page >= 0 && page < p.num_pool_pages;
-        if (g >= kNS && !mbar_wait_bounded(&empty[st], ((g / kNS) - 1) & 1, p.wait_ns)) {
-            *abort_flag = 1;
-            atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
-        }
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
-        unsigned char* dst = ring + st * C::kStage;
-        const unsigned bad = __ballot_sync(0xffffffffu, mine && !ok), by_tma = __ballot_sync(0xffffffffu, mine && ok);
-        if (bad) {
-            if (lane == 0) atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
-            for (unsigned w = bad; w; w &= w - 1) {
-                const int pg = __ffs(w) - 1;
-                constexpr int kRun = C::kRowBytes;         // words of 16 bytes of a page in a panel
-                for (int e = lane; e < C::kNP * kRun; e += 32)
-                    *reinterpret_cast<uint4*>(dst + e / kRun * C::kPanel + (pg * kRun + e % kRun) * 16) = make_uint4(0, 0, 0, 0);
-                if (E4M3 && lane < 16) sring[st * kStep + pg * 16 + lane] = 0.f;
+        if (C::kPairs && ((g >> 1) & 1) != who) continue;
+        const int in_tile = 2 * ((i & 1) + half) + sub;
+        const int page = __shfl_sync(0xffffffffu, cur, (j & 7) * 4 + in_tile);
+        const bool mine = pi < kPages && needed_page<M>(p, s, s.place(j) + in_tile * 16);
+        const bool ok = mine && page >= 0 && page < p.num_pool_pages;
+        const int bar_step = g + bar_half, bar_stage = bar_step % kNS;
+        const bool room = lane >= kBars || bar_step < kNS ||
+                          mbar_wait_bounded(&bar_empty[bar_stage], (bar_step / kNS - 1) & 1, p.wait_ns);
+        if (!__all_sync(0xffffffffu, room && *abort_flag == 0)) {
+            if (!room) {
+                *abort_flag = 1;
+                atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
             }
-            fence_proxy_async_smem();                      // the next use of the stage may be by TMA
+            return false;
+        }
+        const unsigned by_tma = __ballot_sync(0xffffffffu, ok);
+        const int st = (g + half) % kNS;
+        if (__any_sync(0xffffffffu, mine && !ok)) {
+            if (mine && !ok) {                             // a lane a quarter of the page's rows
+                atomicOr(p.status, TREESPEC_STATUS_BAD_PAGE);
+                unsigned char* dst = pages + st * C::kStage + (lane & 3) * 4 * C::kRowBytes;
+                for (int pn = 0; pn < C::kNP; ++pn)
+                    for (int e = 0; e < 4 * C::kRowBytes / 16; ++e)
+                        *reinterpret_cast<uint4*>(dst + pn * C::kPanel + e * 16) = make_uint4(0, 0, 0, 0);
+                if (E4M3) *reinterpret_cast<float4*>(lines + st * kStep) = make_float4(0.f, 0.f, 0.f, 0.f);
+                fence_proxy_async_smem();                  // the next use of the stage may be by TMA
+            }
             __syncwarp();
         }
-        if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(__popc(by_tma)) * (kPageBytes + (E4M3 ? 64u : 0u)));
+        if (lane < kBars) mbar_arrive_expect_tx(&bar_full[bar_stage], uint32_t(__popc(by_tma & bar_pages)) * kPageBytes);
+        armed = g + kSteps;
         __syncwarp();
-        if (mine && ok) {
-            if constexpr (E4M3) {
-                tma_load_3d(dst + lane * kPageBytes, map, 0, h, page * 16, &full[st]);
-                bulk_load_64(sring + st * kStep + lane * 16, scales + (size_t(page) * p.Hkv + h) * kPage, &full[st]);
-            } else {
+        if (ok && (lane & 3) == 0) {
+            unsigned char* dst = pages + st * C::kStage;
 #pragma unroll
-                for (int pn = 0; pn < C::kNP; ++pn)
-                    tma_load_3d(dst + pn * C::kPanel + lane * 2048, map, 64 * pn, h, page * 16, &full[st]);
-            }
+            for (int pn = 0; pn < C::kNP; ++pn) tma_load_3d(dst + pn * C::kPanel, map, 64 * pn, h, page * 16, &page_full[st]);
+        }
+        if (E4M3 && pi < kPages) {                         // each of the lanes arrives once its copy, if any, is there
+            if (ok) copy_16(lines + st * kStep, scales + (size_t(page) * p.Hkv + h) * kPage);
+            arrive_behind_copies(&page_full[st]);
         }
         __syncwarp();
     }
@@ -319,10 +357,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         return;
     }
     if (tid == 0) {
+        constexpr int kFullCount = E4M3 ? 9 : 1;           // and the lanes that copy the scales of two pages
         for (int s = 0; s < kNS; ++s) {
-            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->k_full[s], kFullCount);
             mbar_init(&bars->k_empty[s], 1);               // a step is one warp's
-            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->v_full[s], kFullCount);
             mbar_init(&bars->v_empty[s], 1);
         }
         for (int s = 0; s < kSegRing; ++s) {
@@ -334,7 +373,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kWarpFewK && lane == 0) {
+    if (warp == kWarpProduce && lane == 0) {
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
@@ -395,10 +434,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             return;
         }
         // ---------------------------------------------------------------- TMA producers
-        const bool is_v = warp == kWarpFewV;
-        uint64_t* full = is_v ? bars->v_full : bars->k_full;
-        uint64_t* empty = is_v ? bars->v_empty : bars->k_empty;
-        int armed = 0, ids = 0;
+        const int who = warp - kWarpProduce;
+        int ring = 0, armed = 0, ids = 0;                  // steps before the segment; behind the last tile armed here
         Seg<M> s{}, nxt{};
         auto take = [&](int i, Seg<M>& to, int& pages) -> bool {   // segment i and its first page ids
             if (!seg_ready(i)) {
@@ -408,7 +445,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const bool more = slot(i).more != 0;
             if (more) {
                 to = slot(i).seg;
-                pages = step_pages<M>(p, to, 0);
+                pages = tile_pages<M>(p, to, 0);
             }
             seg_done(i);
             return more;
@@ -417,19 +454,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         for (int i = 1; more; ++i) {
             int next_ids = 0;
             const bool next_more = take(i, nxt, next_ids);   // its page ids are on their way while this one is copied
-            if (!produce_steps<D, E4M3, NR, M>(p, is_v ? &tmv : &tmk, is_v ? p.v_scales : p.k_scales,
-                                               sm + (is_v ? C::kOffV : C::kOffK),
-                                               reinterpret_cast<float*>(sm + C::kOffScale) + (is_v ? kNS * kStep : 0), full,
-                                               empty, s, ids, armed, abort_flag))
-                break;
+            if (!produce<D, E4M3, NR, M>(p, &tmk, &tmv, sm, bars, s, ids, ring, who, armed, abort_flag)) break;
+            ring += 2 * s.ntiles;
             s = nxt;
             ids = next_ids;
             more = next_more;
         }
-        tcparts::ProducerArgs a{};                         // only what the drain looks at
-        a.full = full;
-        a.nst = kNS;
-        tcparts::drain_copies(a, armed);
+        // the copies on their way land before the CTA may end: the last use of each stage that this
+        // warp fills, a lane for each stage of each ring
+        const int stage = lane % kNS, last = armed - 1 - ((armed - 1 - stage) & (kNS - 1));
+        const bool own = C::kPairs ? ((stage >> 1) & 1) == who : lane / kNS == who;
+        if (lane < 2 * kNS && own && last >= 0)
+            mbar_wait_bounded(&(lane < kNS ? bars->k_full : bars->v_full)[stage], (last / kNS) & 1, kDefaultWaitNs);
         return;
     }
 

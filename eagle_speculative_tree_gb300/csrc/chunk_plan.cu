@@ -9,9 +9,11 @@
 // group have to be packed, anywhere in a batch whose offsets are out of order.
 //
 // The lengths are on the device.  One CTA per launch scans them and finds where all ranges begin, a thread
-// per range; the launches' own CTAs then start with one load.  What bounds this kernel is the fetching of
-// its own instructions, which other kernels have displaced since its last run (the same code took 5 us run
-// twice in a row and 11 the first time): so it is short, with loops and calls where they save code.
+// per range; the launches' own CTAs then start with one load (when each scanned the batch by itself, the
+// start of a small call took 3 to 4 us longer).  It reads and writes a few KB.  What bounds it is the
+// fetching of its own instructions, which other kernels have displaced since its last run (5 us of a
+// call; the same code took 11 us the first time and 5 right behind that): so it is short, with loops and
+// calls where they save code.
 #include "chunk_units.cuh"
 
 namespace treespec {
@@ -37,7 +39,7 @@ struct CutSmem {
     int pieces[kChunkMaxCtas];
     long long warp_size[32], warp_units[32];
     unsigned long long rows_sum;
-    unsigned long long load[2];                                         // tiles of the sequences' units and of the groups'
+    unsigned long long load[2];                            // tiles of the sequences' units and of the groups'
     int longest;
 };
 struct PlanSmem {
@@ -45,9 +47,10 @@ struct PlanSmem {
     CutSmem cut;
 };
 
-// `rows`, in shared memory: rows of sequence tid where there is one.
-__device__ __forceinline__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, GroupSmem& sm, const SeqRows& mine,
-                                               bool flags) {
+// Checks the groups and writes their table and every sequence's share, by all threads.  `mine`: rows of
+// sequence tid where there is one.
+__device__ __forceinline__ void lay_out_groups(const ChunkParams& p, const GroupParams& g, GroupSmem& sm,
+                                               const SeqRows& mine, bool flags) {
     const int tid = threadIdx.x, NG = p.groups;
     int4* gtab = const_cast<int4*>(p.gtab);
     int2* skip = const_cast<int2*>(p.skip);
@@ -121,10 +124,11 @@ __device__ __noinline__ long long unit_start(const SeqUnits<M>* u, int kappa, in
     return u->tiles_before(pr) + (long long)kappa * pr;
 }
 
-// Scans a launch's entries and lays out its ranges.  Positions as in Cut, ranges even to one position: CTA c
-// of `parts` begins at c size + min(c, rest).
+// Scans a launch's entries and lays out its ranges.  Positions, pieces and whole units are as in Cut
+// (chunk_units.cuh), but ranges are even to one position: CTA c of `parts` begins at c size + min(c, rest).
 template <ChunkMode M>
-__device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, const SeqRows& mine, const Tuning tune, bool flags) {
+__device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, const SeqRows& mine, const Tuning tune,
+                                        bool flags) {
     CutSmem& sm = all.cut;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int entries = chunk_entries<M>(p), Hkv = p.Hkv;
@@ -220,7 +224,8 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
         rest = total - size_of * parts;
     }
     const long long wide = rest * (size_of + 1);
-    // The CTA that holds the first piece of a unit of `tiles` tiles at position `at` (number `index` of the batch), and its pieces
+    // The CTA that holds the first piece of a unit of `tiles` tiles at position `at` (number `index` of the batch),
+    // and its pieces
     auto share_of = [&](long long at, int tiles, int rows, int index) -> int2 {
         if (m) return make_int2(index * m, pieces_of(tiles, rows, m));
         int c[2];
@@ -291,7 +296,9 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
                 continue;
             }
             // one range ends where the next begins; of m CTAs for each unit, those beyond its pieces have nothing
-            auto cut_at = [&](int k) { return k > share.y ? tiles : int(uint32_t(tiles) * uint32_t(k) / uint32_t(share.y)); };
+            auto cut_at = [&](int k) {
+                return k > share.y ? tiles : int(uint32_t(tiles) * uint32_t(k) / uint32_t(share.y));
+            };
             int4 begin = make_int4(entries, 0, 0, 0);
             if (on) begin = make_int4(e.b, e.h, e.pr, m ? cut_at(job % m) : e.j);
             if (job < p.ctas) {
@@ -306,7 +313,8 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
                     out.begin.x = -1;
                 } else {
                     const bool last = job + 1 >= parts;
-                    out.end = m ? make_int4(e.b, e.h, e.pr, cut_at(job % m + 1)) : last ? make_int4(entries, 0, 0, 0) : sm.ends[job + 1];
+                    out.end = m ? make_int4(e.b, e.h, e.pr, cut_at(job % m + 1))
+                                : last ? make_int4(entries, 0, 0, 0) : sm.ends[job + 1];
                     out.last_pieces = m ? share.y : last ? 0 : sm.pieces[job + 1];
                     out.first_cta = share.x;
                     out.first_pieces = share.y;
@@ -338,13 +346,15 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     if (int(threadIdx.x) < p.B) mine = seq_rows(p, threadIdx.x);
     if (M == kChunkShared) lay_out_groups(p, a.groups, sm.groups, mine, first);
     if (a.launches == 0) return;
-    Tuning tune{TuneUnits::kKappa, 2, TuneUnits::kMinTilesManyRows, TuneUnits::kWholeTiles, p.ctas};
-    if (p.few_rows) tune = Tuning{TuneFew::kKappa, TuneFew::kMinTiles, TuneFew::kMinTilesManyRows, TuneFew::kWholeTiles, p.ctas};
+    const int kappa = p.k_scales && a.launches == 1 ? TuneUnits::kPlanKappaCodes : TuneUnits::kPlanKappa;
+    Tuning tune{kappa, TuneUnits::kPlanMinTiles, TuneUnits::kMinTilesManyRows, TuneUnits::kWholeTiles, p.ctas};
+    if (p.few_rows) tune = Tuning{TuneFew::kKappa, TuneFew::kMinTiles, TuneFew::kMinTiles, TuneFew::kWholeTiles, p.ctas};
     if (M == kChunkShared && a.launches == 2) {
-        // Two launches, the groups' on units of 256 rows with an SM for each CTA and the sequences' with two CTAs to an
-        // SM, run at the same time: each gets SMs by its tiles, a tile of 256 rows counted 1.4 times.
-        // (64 sequences of one token, 20 .. 600 tokens of their own behind 8192 shared ones: 89 us one launch after the
-        // other.)
+        // Two launches, the groups' on units of 256 rows with an SM for each CTA and the sequences' with
+        // two CTAs to an SM, run at the same time: each gets SMs by its tiles, a tile of 256 rows
+        // counted 2.3 times (64 sequences of one token, 20 .. 600 tokens of their own behind 8192
+        // shared ones: 65 us, e4m3 66; 69 and 73 counted 1.4 times, 71 and 66 counted 3.4; 89 one
+        // launch after the other).
         if (threadIdx.x < 2) sm.cut.load[threadIdx.x] = 0;
         __syncthreads();
         const int g0 = a.launch[1].groups, tpu = a.launch[1].tpu, few_tpu = a.launch[0].tpu;
@@ -355,13 +365,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         }
         if (int(threadIdx.x) < g0) {
             const int4 e = sm.groups.table[threadIdx.x];
-            if (e.y) tiles[1] = (e.y + tpu - 1) / tpu * (e.z / kBN + TuneUnits::kKappa);
+            if (e.y) tiles[1] = (e.y + tpu - 1) / tpu * (e.z / kBN + kappa);
         }
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
             if (tiles[i]) atomicAdd(&sm.cut.load[i], (unsigned long long)tiles[i]);
         __syncthreads();
-        const float own = float(sm.cut.load[0]), shared = 1.4f * float(sm.cut.load[1]);
+        const float own = float(sm.cut.load[0]), shared = 2.3f * float(sm.cut.load[1]);
         const int sms = a.launch[1].ctas;
         int for_groups = shared == 0.f ? 0 : min(sms, max(1, int(float(sms) * shared / (shared + own) + 0.5f)));
         if (own > 0.f) for_groups = min(for_groups, max(1, sms - 1));

@@ -431,7 +431,7 @@ __device__ __forceinline__ void join_unit(const ChunkParams& p, const Whereabout
         pieces = head ? cut->last_pieces : cut->first_pieces;
     } else if (cut.m) {
         c0 = me / cut.m * cut.m;
-        pieces = unit_pieces<TuneUnits>(s.n, s.tokens * p.G, cut.m);
+        pieces = unit_pieces(s.n, s.tokens * p.G, cut.m);
     } else {
         const SeqUnits<M> u = seq_units<M>(p, s.b);
         const long long ub = cut.before(s.b) + s.h * div_pos(cut.before(s.b + 1) - cut.before(s.b), cut.Hkv) +
@@ -469,9 +469,9 @@ __device__ __noinline__ void redo_rows(const ChunkParams& p, const unsigned char
     const int lane = threadIdx.x & 31, t = threadIdx.x >> 7, quarter = (threadIdx.x >> 5) & 3, me = blockIdx.x;
     Whereabouts<M> cut;
     if constexpr (M == kChunkPlain)
-        cut = cut_of<M, TuneUnits>(p, reinterpret_cast<const long long*>(sm + C::kOffTiles),
-                                   reinterpret_cast<const int*>(sm + C::kOffUnits),
-                                   *reinterpret_cast<const int*>(sm + C::kOffMisc + 8), gridDim.x);
+        cut = cut_of(p, reinterpret_cast<const long long*>(sm + C::kOffTiles),
+                     reinterpret_cast<const int*>(sm + C::kOffUnits),
+                     *reinterpret_cast<const int*>(sm + C::kOffMisc + 8), gridDim.x);
     else
         cut = reinterpret_cast<const CtaPlan*>(sm + C::kOffTiles);
     __syncwarp();                                          // the lanes' stores come before what is read and stored here
@@ -657,9 +657,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
     Whereabouts<M> cut;
     bool idle;
     if constexpr (M == kChunkPlain) {
-        // ---- the entries' tiles and units, and this CTA's range
-        scan_units<M, C::kThreads>(p, tiles_s, units_s, reinterpret_cast<long long*>(sm + C::kOffWarp), longest);
-        cut = cut_of<M, TuneUnits>(p, tiles_s, units_s, *longest, gridDim.x);
+        // ---- the sequences' tiles and units, and this CTA's range
+        scan_units<C::kThreads>(p, tiles_s, units_s, reinterpret_cast<long long*>(sm + C::kOffWarp), longest);
+        cut = cut_of(p, tiles_s, units_s, *longest, gridDim.x);
         idle = cut.total == 0 || me >= cut.parts;
     } else {
         // ---- this CTA's range, as planned
@@ -682,15 +682,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             End e;
             if (cut.m) {
                 e = unit_at(p, cut, me / cut.m);
-                const SeqRows r = entry_rows<M>(p, e.b);
-                const SeqUnits<M> u = seq_units<M>(p, e.b, r);
-                const int n = u.tiles(e.pr), left = (is_group<M>(p, e.b) ? r.n : u.live) - e.pr * u.tpu;
-                const int pieces = unit_pieces<TuneUnits>(n, min(u.tpu, left) * p.G, cut.m), k = me % cut.m + warp;
+                const SeqUnits<M> u = seq_units<M>(p, e.b);
+                const int n = u.tiles(e.pr), left = u.live - e.pr * u.tpu;
+                const int pieces = unit_pieces(n, min(u.tpu, left) * p.G, cut.m), k = me % cut.m + warp;
                 e.j = k > pieces ? n : int((long long)n * k / pieces);   // beyond the last piece: nothing
             } else if (c >= cut.parts) {
                 e = End{cut.B, 0, 0, 0};
             } else {
-                e = locate<M>(p, cut, cut.bound(c));
+                e = locate(p, cut, cut.bound(c));
                 const int n = seq_units<M>(p, e.b).tiles(e.pr);
                 // Short units stay whole: the cut moves to the nearer end of one, and both neighbours
                 // see it there (160 units of 1 or 2 tiles: 43 us cut, 27 whole; with units of up to 10
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
             }
             if (lane == 0) {
                 ends[warp] = e;
-                if (warp == 0) *first_rows = entry_rows<M>(p, e.b);
+                if (warp == 0) *first_rows = seq_rows(p, e.b);
             }
         }
     }

@@ -13,19 +13,28 @@ using namespace sm100;
 
 constexpr int kBN = 64;              // tokens per KV tile
 
-// Of the cut: kKappa, a unit's fixed cost in tiles.  No piece of a unit with CTAs of its own is shorter than
-// kMinTiles (kMinTilesManyRows of more than 64 rows), and units up to kWholeTiles long are not cut.
+// Of the cut: kKappa, a unit's fixed cost in tiles.  No piece of a unit with CTAs of its own is shorter
+// than kMinTiles (kMinTilesManyRows of more than 64 rows), and units up to kWholeTiles long are not cut.
 struct TuneUnits {                   // units of 256 rows (chunk_tc.cuh)
     static constexpr int kKappa = 7;
     // Joining costs by the row, so units of many rows are cut into longer pieces (8 nodes x 4 heads over
     // 2048 e4m3 tokens: 28.7 us in pieces of 4 tiles, 30.9 of 9; 3 prompts of up to 816 tokens, 4
     // heads: 33 and 25).
     static constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
+    // where the ranges are planned ahead (chunk_plan.cu), a CTA starts sooner and shorter pieces pay (8 nodes
+    // x 4 heads over 2048 e4m3 tokens, 512 of them in the window: 31.0 us in pieces of 2 tiles, 32.8 of 4)
+    static constexpr int kPlanMinTiles = 2;
+    // There, too, the fixed cost counts in each type's tiles, 0.8 us of bf16 and 1.3 of e4m3 (4 prompts
+    // through a window and 32 trees behind a shared prefix, bf16: 217 and 171 us, and 219 and 176 with 7;
+    // 4 prompts and 47 short chunks behind 3 prefixes, e4m3: 379 and 108 us, and 395 and 110 with 7); but
+    // the groups of decoded tokens are cut into pieces whose stores count for more (64 sequences, e4m3:
+    // 66 us, and 69 with 7).
+    static constexpr int kPlanKappa = 10, kPlanKappaCodes = 5;
     static constexpr int kWholeTiles = 4;
 };
 struct TuneFew {                     // units of 8 or 16 rows (chunk_few.cuh)
     static constexpr int kKappa = 3;
-    static constexpr int kMinTiles = 2, kMinTilesManyRows = 2;
+    static constexpr int kMinTiles = 2;
     static constexpr int kWholeTiles = 2;
 };
 
@@ -177,40 +186,31 @@ struct End {                          // tile j of unit (b, h, pr)
     int b, h, pr, j;
 };
 // Pieces of a unit of n tiles and that many rows that m CTAs share.
-template <class Tune>
 __device__ __forceinline__ int unit_pieces(int n, int rows, int m) {
-    return min(m, max(1, n / (rows > 64 ? Tune::kMinTilesManyRows : Tune::kMinTiles)));
+    return min(m, max(1, n / (rows > 64 ? TuneUnits::kMinTilesManyRows : TuneUnits::kMinTiles)));
 }
 
-// The shares of the cut of a batch of n units: the total is there, `longest` the tiles of its longest unit.
-template <class Tune>
-__device__ __forceinline__ void share_cut(Cut& cut, long long n, int longest, int ctas) {
+// The cut of a batch: the prefix sums and the KV tiles of its longest unit.
+__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest, int ctas) {
+    Cut cut;
+    const long long n = (long long)p.Hkv * units[p.B];
+    cut.tiles = tiles;
+    cut.units = units;
+    cut.B = p.B;
+    cut.Hkv = p.Hkv;
+    cut.k = TuneUnits::kKappa;
+    cut.total = p.Hkv * tiles[p.B] + TuneUnits::kKappa * n;
     // A range that holds pieces of two units pays the fixed cost twice, so where there is less
     // than about that cost for each CTA, every unit gets CTAs of its own instead (119 new
     // tokens, 32 q / 8 kv heads: 35 us cut evenly, 21 this way; 8 nodes over 2048 e4m3 tokens:
     // 42 and 29), unless one long unit among short ones would then run far longer than its
     // share of all tiles
     cut.m = 0;
-    if (cut.total < (long long)(Tune::kKappa + 2) * ctas && n <= ctas && n > 0) {
+    if (cut.total < (long long)(TuneUnits::kKappa + 2) * ctas && n <= ctas && n > 0) {
         const int m = ctas / int(n);
-        if (longest / unit_pieces<Tune>(longest, 1, m) <= int(cut.total) / ctas + 2 * Tune::kKappa) cut.m = m;
+        if (longest / unit_pieces(longest, 1, m) <= int(cut.total) / ctas + 2 * TuneUnits::kKappa) cut.m = m;
     }
-    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)ctas, max(1ll, cut.total / (Tune::kKappa + 1))));
-}
-
-// The cut of a batch: the prefix sums and the KV tiles of its longest unit.
-template <ChunkMode M, class Tune>
-__device__ __forceinline__ Cut cut_of(const ChunkParams& p, const long long* tiles, const int* units, int longest, int ctas) {
-    Cut cut;
-    const int entries = chunk_entries<M>(p);
-    const long long n = (long long)p.Hkv * units[entries];
-    cut.tiles = tiles;
-    cut.units = units;
-    cut.B = entries;
-    cut.Hkv = p.Hkv;
-    cut.k = Tune::kKappa;
-    cut.total = p.Hkv * tiles[entries] + Tune::kKappa * n;
-    share_cut<Tune>(cut, n, longest, ctas);
+    cut.parts = cut.m ? cut.m * int(n) : int(min((long long)ctas, max(1ll, cut.total / (TuneUnits::kKappa + 1))));
     return cut;
 }
 
@@ -227,7 +227,6 @@ __device__ __forceinline__ End unit_at(const ChunkParams& p, const Cut& q, int u
 }
 
 // The tile at or after position x of the cut, by one warp.  x < total.
-template <ChunkMode M>
 __device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long long x) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = q.B;                                  // the last b with before(b) <= x
@@ -238,7 +237,7 @@ __device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long l
     }
     End e;
     e.b = lo;
-    const SeqUnits<M> u = seq_units<M>(p, lo);
+    const SeqUnits<kChunkPlain> u = seq_units<kChunkPlain>(p, lo);
     const long long head = div_pos(q.before(lo + 1) - q.before(lo), q.Hkv);
     long long y = x - q.before(lo);
     e.h = int(div_pos(y, head));
@@ -259,26 +258,23 @@ __device__ __forceinline__ End locate(const ChunkParams& p, const Cut& q, long l
     return e;
 }
 
-// The prefix sums of the entries' tiles and units, and *longest, the tiles of the longest unit, by all
+// The prefix sums of the sequences' tiles and units, and *longest, the tiles of the longest unit, by all
 // threads of the CTA; flags bad lengths.  wt: [warps] {tiles, units, rows}.
-template <ChunkMode M, int kThreads>
+template <int kThreads>
 __device__ __forceinline__ void scan_units(const ChunkParams& p, long long* tiles_s, int* units_s, long long* wt,
                                            int* longest) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int entries = chunk_entries<M>(p);
-    const int per = (entries + kThreads - 1) / kThreads;
-    const int b0 = min(entries, tid * per), b1 = min(entries, b0 + per);
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
     long long nt = 0;
     int nu = 0, top = 0, rows_lo = 0, rows_hi = 0;     // rows in 16-bit halves: sums of 96 sequences fit
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
-        const SeqRows r = entry_rows<M>(p, b);
-        const SeqUnits<M> u = seq_units<M>(p, b, r);
-        if (!is_group<M>(p, b)) {
-            bad |= !seq_ok(p, sequence_of<M>(p, b));
-            rows_lo += r.n & 0xffff;
-            rows_hi += r.n >> 16;
-        }
+        const SeqRows r = seq_rows(p, b);
+        const SeqUnits<kChunkPlain> u = seq_units<kChunkPlain>(p, b, r);
+        bad |= !seq_ok(p, b);
+        rows_lo += r.n & 0xffff;
+        rows_hi += r.n >> 16;
         tiles_s[b] = nt;                               // relative to the thread's first
         units_s[b] = nu;
         nt += u.np == 1 ? u.tiles(0) : u.tiles_before(u.np);
@@ -320,8 +316,8 @@ __device__ __forceinline__ void scan_units(const ChunkParams& p, long long* tile
     if (tid == kThreads - 1) {
         // Sequences that share rows (offsets out of order) may have more units than 32 bits count:
         // no row is computed then
-        tiles_s[entries] = rows > p.T ? 0 : bt + nt;
-        units_s[entries] = rows > p.T ? 0 : int(bu + nu);
+        tiles_s[p.B] = rows > p.T ? 0 : bt + nt;
+        units_s[p.B] = rows > p.T ? 0 : int(bu + nu);
     }
     __syncthreads();
 }

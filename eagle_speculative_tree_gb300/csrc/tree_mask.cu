@@ -15,7 +15,6 @@
 
 namespace treespec {
 
-//
 // With a window (kWindow) the sets hold only what the window leaves of them: a node sees its
 // ancestors fewer than `window` steps above it, and those whose position S + depth is a sink's.
 template <bool kWindow>
