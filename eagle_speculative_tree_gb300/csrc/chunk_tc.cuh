@@ -122,6 +122,51 @@ __device__ __forceinline__ Row row_of(const ChunkParams& p, const Seg<M>& s, int
     o.at = (size_t(s.row0 + i) * p.Hq + o.hq) * D;
     return o;
 }
+// Stores N 16-byte units of each lane's row, those with `ok`.  A store of 32 lanes to as many rows takes the
+// memory pipe 32 turns, some 4000 (bf16) or 8000 clocks for the 256 rows of a unit; so where more than 8 rows
+// are there, four lanes first exchange their units (kExchange), and a store writes 64 bytes of 8 rows: 4 prompts
+// through a window 208 us, 216 without; 32 trees 286 and 293; 6 prompts without a window 362 and 378.  Over
+// 8-bit pools (prompts through a window 383, 378 without; 47 short chunks behind 3 prefixes 115 and 108) and
+// for the parts of shared prefixes (the same chunks in bf16: 96 and 93) the exchange costs more than it gives.
+template <int N, bool kExchange>
+__device__ __forceinline__ void store_row(void* row, bool ok, uint32_t (&w)[4 * N]) {
+    const int lane = threadIdx.x & 31;
+    const unsigned rows = __ballot_sync(0xffffffffu, ok);
+    if (!kExchange || __popc(rows) <= 8) {
+        if (ok)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                __stcg(static_cast<uint4*>(row) + e, make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]));
+        return;
+    }
+    // of units a and b, with or without `bit` in their number: a stays with the lanes without it, b with the others
+    auto exchange = [&](uint32_t& a, uint32_t& b, int bit) {
+        const bool up = (lane & bit) != 0;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, bit);
+        if (up) a = got;
+        else b = got;
+    };
+    uint4* dst[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        dst[k] = reinterpret_cast<uint4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (lane & 28) + k)) +
+                 (lane & 3);
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            exchange(w[4 * e + i], w[4 * (e + 1) + i], 1);
+            exchange(w[4 * (e + 2) + i], w[4 * (e + 3) + i], 1);
+            exchange(w[4 * e + i], w[4 * (e + 2) + i], 2);
+            exchange(w[4 * (e + 1) + i], w[4 * (e + 3) + i], 2);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)                        // unit e + lane % 4 of row k of the four
+            if ((rows >> ((lane & 28) + k)) & 1u)
+                __stcg(dst[k] + e, make_uint4(w[4 * (e + k)], w[4 * (e + k) + 1], w[4 * (e + k) + 2], w[4 * (e + k) + 3]));
+    }
+}
+
 // A row's exact attention over the segment's visible tokens, by one warp on CUDA cores:
 // (m, l) and O in lane-wise slices of D / 32 elements.  Nothing of a token that the row does
 // not see is read.
@@ -1151,11 +1196,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                 }
                 tc_fence_before();
                 mbar_arrive(&bars->o_free[t]);
-                if (ro.ok) {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + ro.at);
-#pragma unroll
-                    for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(w2[4 * e], w2[4 * e + 1], w2[4 * e + 2], w2[4 * e + 3]);
-                }
+                store_row<D / 8, !E4M3>(static_cast<uint16_t*>(p.out) + ro.at, ro.ok, w2);
             } else {
                 if (warp_rows) {
                     float* acc = apart ? p.rows_acc + side_offset(p, s.part()) * D + ro.at : p.part_acc + prow * D;
@@ -1166,13 +1207,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1)
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
-                        if (ro.ok) {
-                            float4* dst = reinterpret_cast<float4*>(acc + c * 32);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                __stcg(dst + e, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                            __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
-                        }
+                        store_row<8, !E4M3 && M != kChunkShared>(acc + c * 32, ro.ok, o);
                     }
                     if (ro.ok)
                         __stcg(reinterpret_cast<float2*>(apart ? p.rows_ml : p.part_ml) +
