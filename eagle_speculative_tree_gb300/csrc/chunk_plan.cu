@@ -37,10 +37,11 @@ struct CutSmem {
     SeqRows rows[kChunkMaxBatch];
     int4 ends[kChunkMaxCtas];
     int pieces[kChunkMaxCtas];
-    long long warp_size[32], warp_units[32];
-    unsigned long long rows_sum;
-    unsigned long long load[2];                            // tiles of the sequences' units and of the groups'
-    int longest;
+    // of each warp's entries.  (Sums and maxima pass through here, not through 64-bit atomics on shared memory,
+    // which took 64 sequences 3 to 4 us.)
+    long long warp_size[32], warp_units[32], warp_rows[32];
+    int warp_top[32];
+    float warp_load[2][32];                                // tiles of the sequences' units and of the groups'
 };
 struct PlanSmem {
     GroupSmem groups;
@@ -132,10 +133,6 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
     CutSmem& sm = all.cut;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int entries = chunk_entries<M>(p), Hkv = p.Hkv;
-    if (tid == 0) {
-        sm.longest = 0;
-        sm.rows_sum = 0;
-    }
     // ---- prefix sums of the entries' positions and units
     long long size = 0;
     int nu = 0, top = 0, nr = 0;
@@ -178,21 +175,25 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
             iu += c;
         }
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const long long rows = (long long)__reduce_add_sync(0xffffffffu, nr >> 16) * 65536 + __reduce_add_sync(0xffffffffu, nr & 0xffff);
     if (lane == 31) {
         sm.warp_size[warp] = it;
         sm.warp_units[warp] = iu;
+        sm.warp_rows[warp] = rows;
+        sm.warp_top[warp] = top;
     }
-    top = __reduce_max_sync(0xffffffffu, top);
     __syncthreads();
-    if (lane == 0 && top) atomicMax(&sm.longest, top);
-    if (nr) atomicAdd(&sm.rows_sum, (unsigned long long)nr);
-    long long bt = 0, all_t = 0, bu = 0, all_u = 0;
+    long long bt = 0, all_t = 0, bu = 0, all_u = 0, all_rows = 0;
+    int longest = 0;
     const int used = (entries + 31) / 32;
 #pragma unroll 1
     for (int w = 0; w < used; ++w) {
         if (w == warp) bt = all_t, bu = all_u;
         all_t += sm.warp_size[w];
         all_u += sm.warp_units[w];
+        all_rows += sm.warp_rows[w];
+        longest = max(longest, sm.warp_top[w]);
     }
     if (tid < entries) {
         sm.start[tid] = Hkv * (bt + it - size);
@@ -207,7 +208,7 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
 
     // ---- the cut, as cut_of() makes it.  Sequences that share rows (offsets out of order) may have more units than
     // 32 bits count: no row is computed then
-    const long long total = sm.rows_sum > (unsigned long long)p.T ? 0 : Hkv * all_t, n = Hkv * all_u;
+    const long long total = all_rows > p.T ? 0 : Hkv * all_t, n = Hkv * all_u;
     const int ctas = tune.ctas;
     auto pieces_of = [&](int tiles, int rows, int m) {
         return min(m, max(1, tiles / (rows > 64 ? tune.min_tiles_many_rows : tune.min_tiles)));
@@ -215,7 +216,7 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
     int m = 0;                                             // CTAs of each unit, 0: even ranges
     if (total < (long long)(tune.kappa + 2) * ctas && n <= ctas && total > 0) {
         m = ctas / int(n);
-        if (sm.longest / pieces_of(sm.longest, 1, m) > int(total) / ctas + 2 * tune.kappa) m = 0;
+        if (longest / pieces_of(longest, 1, m) > int(total) / ctas + 2 * tune.kappa) m = 0;
     }
     const int parts = total == 0 ? 0 : m ? m * int(n) : int(min((long long)ctas, max(1ll, total / (tune.kappa + 1))));
     long long size_of = 1, rest = 0;                       // of a range
@@ -355,23 +356,33 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         // counted 2.3 times (64 sequences of one token, 20 .. 600 tokens of their own behind 8192
         // shared ones: 65 us, e4m3 66; 69 and 73 counted 1.4 times, 71 and 66 counted 3.4; 89 one
         // launch after the other).
-        if (threadIdx.x < 2) sm.cut.load[threadIdx.x] = 0;
-        __syncthreads();
         const int g0 = a.launch[1].groups, tpu = a.launch[1].tpu, few_tpu = a.launch[0].tpu;
-        int tiles[2] = {0, 0};
+        float load[2] = {0.f, 0.f};
         if (int(threadIdx.x) < p.B && mine.S >= 0) {
             const int base = p.skip[threadIdx.x].x / kBN;
-            tiles[0] = (mine.live + few_tpu - 1) / few_tpu * ((mine.S + mine.live + kBN - 1) / kBN - base + TuneFew::kKappa);
+            load[0] = float((mine.live + few_tpu - 1) / few_tpu) *
+                      float((mine.S + mine.live + kBN - 1) / kBN - base + TuneFew::kKappa);
         }
         if (int(threadIdx.x) < g0) {
             const int4 e = sm.groups.table[threadIdx.x];
-            if (e.y) tiles[1] = (e.y + tpu - 1) / tpu * (e.z / kBN + kappa);
+            if (e.y) load[1] = float((e.y + tpu - 1) / tpu) * float(e.z / kBN + kappa);
         }
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i)
-            if (tiles[i]) atomicAdd(&sm.cut.load[i], (unsigned long long)tiles[i]);
+        for (int o = 16; o; o >>= 1) {
+            load[0] += __shfl_xor_sync(0xffffffffu, load[0], o);
+            load[1] += __shfl_xor_sync(0xffffffffu, load[1], o);
+        }
+        if ((threadIdx.x & 31) == 0) {
+            sm.cut.warp_load[0][threadIdx.x >> 5] = load[0];
+            sm.cut.warp_load[1][threadIdx.x >> 5] = load[1];
+        }
         __syncthreads();
-        const float own = float(sm.cut.load[0]), shared = 2.3f * float(sm.cut.load[1]);
+        float own = 0.f, shared = 0.f;                     // added up in one order, whatever the run
+#pragma unroll 1
+        for (int w = 0; w < (max(p.B, g0) + 31) / 32; ++w) {
+            own += sm.cut.warp_load[0][w];
+            shared += 2.3f * sm.cut.warp_load[1][w];
+        }
         const int sms = a.launch[1].ctas;
         int for_groups = shared == 0.f ? 0 : min(sms, max(1, int(float(sms) * shared / (shared + own) + 0.5f)));
         if (own > 0.f) for_groups = min(for_groups, max(1, sms - 1));
