@@ -2,27 +2,38 @@
 // with a sliding window or behind shared prefixes: bf16 queries, head dim 64 or 128, K/V bf16 or
 // e4m3.
 //
-// Such a unit, 8 or 16 rows (tokens x query heads) of one sequence and kv head, is bound by the
-// reading of K and V, not by arithmetic.  In chunk_tc.cuh the chain S -> softmax ->
-// P V over tensor memory takes 0.8 (bf16) to 1.3 us (e4m3) per KV tile and SM however few the rows
-// are.  Here warps of their own run over the tiles, and no step waits for another warp's: a warp holds
-// 8 NR rows of Q and O in registers (NR = 1 or 2), and a step is 32 tokens in 16 x 8 x 16 matrix instructions with the
-// rows across: S^T = K Q^T (16 tokens x 8 rows) and O^T += V^T P^T (16 head elements x 8 rows), so eight
-// rows waste nothing.  A lane reads 16 bytes of K at a time, which permutes the head elements (Q's alike);
-// V^T is transposed on the way from shared memory (ldmatrix), P^T by movmatrix.
+// A unit is 8 or 16 rows (tokens x query heads) of one sequence and kv head.  It is bound by the
+// reading of K and V, not by arithmetic: 4 D operations per row and token against 4 D bytes (bf16) per
+// token.  In chunk_tc.cuh the chain S -> softmax -> P V over tensor memory takes 0.8 (bf16) to 1.3 us
+// (e4m3) per KV tile and SM however few the rows are.  Here warps of their own run over the tiles, and
+// no step waits for another warp's.  A warp holds 8 NR rows of Q and O in registers (NR = 1 or 2), and
+// a step is 32 tokens in 16 x 8 x 16 matrix instructions with the rows across: S^T = K Q^T (16 tokens x
+// 8 rows) and O^T += V^T P^T (16 head elements x 8 rows), so eight rows waste nothing; with the rows
+// along the other side of 16, window decode (below) took 190 us for 185.  A lane reads 16 bytes of K at
+// a time, which permutes the head elements (Q's alike); V^T is transposed on the way from shared memory
+// (ldmatrix), P^T by movmatrix.
 //
-// A CTA is four such warps, two that fill the K and V rings by TMA and one that walks along the CTA's range and
-// hands its segments on, ahead of the others; two CTAs to an SM.  The warps take the steps of the range in turn.  Units, the cut into one range per CTA, pieces and the join by the last to finish are those of chunk_units.cuh; at the end
-// of a unit (or piece) the warps' states are joined through shared memory.
+// A CTA is four such warps, two that fill the K and V rings by TMA and one that walks along the CTA's
+// range and hands its segments on, ahead of the others (185 us without it, 175 with); two CTAs to an SM,
+// so that one computes while the other joins.  The warps take the steps of the range in turn.  Units,
+// pieces and segments are those of chunk_units.cuh, one range per CTA laid out by chunk_plan.cu; at the
+// end of a unit (or piece) the warps' states are joined through shared memory, and the pieces of a cut
+// unit by the last CTA to finish.
+//
+// Measured (calls replayed from a graph, 32 / 8 heads of 128): 64 tokens over bf16 windows of up to 4100
+// (window decode) 171 us, 6.0 TB/s, 0.88 of the copy rate; 32 tokens of 64 / 8 heads over e4m3 windows of
+// up to 2063 45 us, 2.8 TB/s: 8 of it the plan, and then about 900 clocks of S and softmax and 1200 of P V
+// for a warp's step, mostly the widening of codes, and 9000 for a unit's end.
 //
 // e4m3: K's codes are widened to f16 (exact), and Q, scaled by a power of two per row, with them: f16
 // holds Q's 8 bits from the row's largest element down to 2^-28 of it, and what is smaller is off by
-// 2^-39 of that element.  V's codes are widened to bf16 (exact), as P times V's scale is bf16, whose range it needs.
+// 2^-39 of that element.  V's codes are widened to bf16 (exact), as P times V's scale is bf16, whose
+// range it needs.
 //
-// A value that a row may not see must not reach it, and P V multiplies it by zero.  V of tokens that no row
-// of the unit sees is overwritten with zeros before use; a step that only some rows see whole is then looked through for
-// values that are not finite, and where there is one its P V is done token by token without
-// the hidden ones.
+// A value that a row may not see must not reach it, and P V multiplies it by zero.  V of tokens that no
+// row of the unit sees is overwritten with zeros before use; a step that only some rows see whole is
+// then looked through for values that are not finite, and where there is one its P V is done token by
+// token without the hidden ones.
 //
 // Every wait is bounded, as in chunk_tc.cuh.
 #pragma once
@@ -51,9 +62,9 @@ struct CfgFew {
     static constexpr int kStage = kNP * kPanel;           // a step of K or V: one warp's
     static constexpr int kPitch = D + 4;                  // floats of a row of a warp's part
     static constexpr int kPartBytes = kWarps * 8 * NR * (kPitch * 4 + 8);
-    // Stages of the K ring, and of the V ring: one or two for each warp, as two CTAs to an SM leave room.  Stage s is
-    // always warp s % 4's: a parity tells a warp that waits for a use of a stage from the use before
-    // it only, so no use may be another warp's (its data may land later than that of a step behind it)
+    // Stages of the K ring, and of the V ring: one or two for each warp, as two CTAs to an SM leave room.
+    // Stage s is always warp s % 4's: a parity tells a warp that waits for a use of a stage from the use
+    // before it only, so no use may be another warp's (its data may land later than that of a step behind it)
     static constexpr int kRoom = (113 * 1024 - 2560 - kPartBytes) / (2 * (kStage + (E4M3 ? kStep * 4 : 0)));
     static constexpr int kNS = kRoom >= 2 * kWarps ? 2 * kWarps : kWarps;
     static constexpr bool kPairs = kNS == 2 * kWarps;     // the tile that a producing warp takes is a quarter of the ring
@@ -247,19 +258,20 @@ __device__ __forceinline__ int tile_pages(const ChunkParams& p, const Seg<M>& s,
     return __ldg(p.page_table + size_t(s.sequence()) * p.max_pages + (pos >> 4));
 }
 
-// One of the two producing warps fills the rings with a segment's K, V and scales.  An iteration is a chain of a
-// wait, two votes, an arrival and the issue of the copies, about 1 us however little it copies.  With
-// two steps to a computing warp (kPairs) it therefore takes the whole KV tile, K and V of two steps, and the
-// warps take every second tile of the CTA; as one warp for K and one for V, a step at a time, the computing
-// warps waited for them (32 tokens over e4m3 windows of up to 2063: 59 us so, 49 this way).  With one step to a
-// warp V of a step would hold up K of the next, so there the warps are one for K and one for V (64 tokens over bf16
-// windows of up to 4100: 223 us in tiles, 174 this way).
+// One of the two producing warps fills the rings with a segment's K, V and scales.  An iteration is a
+// chain of a wait, two votes, an arrival and the issue of the copies, 0.5 us or more however little it
+// copies.  With two stages to a computing warp (kPairs) it therefore takes the whole KV tile, K and V of
+// two steps, and the producers take every second tile of the CTA; as one warp for K and one for V, a step at a
+// time, the computing warps waited for them (window decode e4m3: 59 us so, 49 this way).  With one
+// stage to a warp, V of a step would hold up K of the next, so there they are one for K and one
+// for V (window decode: 223 us in tiles, 174 this way).
 //
-// Lanes 4 i .. 4 i + 3 own page i of the iteration, the first of them its TMA copy and each a quarter of its
-// scales, which come by plain asynchronous copies (a 64-byte bulk copy each takes as long to issue as a page).
-// A page that some row of the unit sees a token of arrives whole, whatever its other tokens hold; one whose id is bad
-// (flagged) is written by the warp as zeros; others are left as they are.  `cur`: the ids of
-// tile_pages(0).  `ring` counts steps over the CTA's life.  False after a timeout or an abort.
+// Lanes 4 i .. 4 i + 3 own page i of the iteration, the first of them its TMA copy and each a quarter of
+// its scales, which come by plain asynchronous copies: a bulk copy of 64 bytes takes as long to issue as
+// a page's.  A page that some row of the unit sees a token of arrives whole, whatever its other tokens
+// hold; one whose id is bad (flagged) is written by the warp as zeros; others are left as they are.
+// `cur`: the ids of tile_pages(0).  `ring` counts steps over the CTA's life.  False after a timeout or an
+// abort.
 template <int D, bool E4M3, int NR, ChunkMode M>
 __device__ __forceinline__ bool produce(const ChunkParams& p, const CUtensorMap* tmk, const CUtensorMap* tmv, unsigned char* sm,
                                         typename CfgFew<D, E4M3, NR>::Bars* bars, const Seg<M>& s, int cur, int ring, int who,
@@ -530,7 +542,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             for (int b = 0; b < 2; ++b) sc[h][b] = __shfl_sync(0xffffffffu, f, (2 * q + b) * 4);
         }
         const int used = s.tokens * p.G;                   // rows of the unit
-        // what every row of the unit sees: of prefix and new tokens those below `all_end`, of the window those from all_low on
+        // what every row of the unit sees: of prefix and new tokens those below all_end, of the window those from
+        // all_low on
         const int t1 = s.t1, ntiles = s.ntiles, all_end = min(t1, p.offsets ? s.S + s.i0 + 1 : s.S);
         int low = 0, all_low = 0;
         if constexpr (M == kChunkWindow) {
@@ -548,7 +561,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 for (int i = 0; i < 4; ++i) o[t][h][i] = 0.f;
         }
 
-        // the warp's steps of the segment, each a half of a KV tile: of all steps of the CTA, numbers warp, warp + 4, ..
+        // the warp's steps of the segment, each a half of a KV tile: of all steps of the CTA, warp, warp + 4, ..
         for (int step = (warp - ring) & (kWarps - 1); step < 2 * ntiles; step += kWarps) {
             const int st = (ring + step) % kNS;
             const uint32_t ph = ((ring + step) / kNS) & 1;
@@ -733,21 +746,22 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     fence_proxy_async_smem();              // the stage's next use is by TMA
                 }
                 __syncwarp();
-#pragma unroll 1
-                for (int e = lane; e < C::kStage / 4; e += 32) {
-                    const uint32_t v = *reinterpret_cast<const uint32_t*>(vt + e * 4);
-                    if constexpr (E4M3) odd |= (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
-                    else odd |= (v & 0x7f80u) == 0x7f80u || (v & 0x7f800000u) == 0x7f800000u;
+                uint32_t found = 0;                        // a carry out of a value's exponent (and mantissa, e4m3)
+#pragma unroll 4
+                for (int e = lane; e < C::kStage / 16; e += 32) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(vt + e * 16);
+                    constexpr uint32_t kMost = E4M3 ? 0x7f7f7f7fu : 0x7f807f80u, kOne = E4M3 ? 0x01010101u : 0x00800080u;
+                    found |= ((v.x & kMost) + kOne) | ((v.y & kMost) + kOne) | ((v.z & kMost) + kOne) | ((v.w & kMost) + kOne);
                 }
-                odd = __any_sync(0xffffffffu, odd);
+                odd = __any_sync(0xffffffffu, (found & (E4M3 ? 0x80808080u : 0x80008000u)) != 0);
             }
             if (!odd) {
                 // ---- O^T += V^T P^T, 16 tokens at a time
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if constexpr (E4M3) {
-                        // the lane has D / 8 head elements from g D / 8 on of tokens 2 q, 2 q + 1 and 8 more: elements 2 t
-                        // and 2 t + 1 are rows g and g + 8 of tile t
+                        // the lane has D / 8 head elements from g D / 8 on of tokens 2 q, 2 q + 1 and 8 more:
+                        // elements 2 t and 2 t + 1 are rows g and g + 8 of tile t
                         uint32_t w[4][D / 32];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {

@@ -61,9 +61,12 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     for (int e = 0; e < DS; ++e) store_out<T>(p.out, size_t(gw) * D + lane * DS + e, acc[e] * inv);
 }
 
-// The same behind the tensor-core kernels: a row's own part is in rows_*[1], the group's in rows_*[0] or, where its
-// unit was cut, in the slots of its pieces: piece k in slot 2 c0 + 1 (k = 0) or 2 (c0 + k), rows as in
-// chunk_tc.cuh (token it of a query tile and head g of the group: row r = it G + g in place 32 (r % 4) + r / 4).
+// The same behind the tensor-core kernels: a row's own part is in rows_*[1], the group's in rows_*[0] or,
+// where its unit was cut, in the slots of its pieces: piece k in slot 2 c0 + 1 (k = 0) or 2 (c0 + k), rows
+// as in chunk_tc.cuh (token it of a query tile and head g of the group: row r = it G + g in place
+// 32 (r % 4) + r / 4).  Bound by latency: a warp's row has one chain of loads to its states (a lane for
+// each), and then the states' rows, eight of them on their way at a time; some 4 us behind the
+// attention kernels for 2048 rows of 9 states.
 template <int D>
 __global__ void __launch_bounds__(256) group_merge_kernel(const ChunkParams p) {
     constexpr int DS = D / 32, kAhead = 8;

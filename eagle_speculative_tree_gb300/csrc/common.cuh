@@ -270,7 +270,7 @@ struct ChunkParams {
     const CtaPlan* plan;                      // kChunkWindow, kChunkShared, persistent: [CTAs]
     int groups;                               // kChunkShared: >= 1
     int entry0, entries;                      //               the entries of this launch
-    const int4* gtab;                         //               [groups] of the group prologue: the first row, the rows,
+    const int4* gtab;                         //               [groups] of the plan: the first row, the rows,
                                               //               the shared tokens (whole KV tiles; 0 with 0 rows where
                                               //               nothing is shared), the sequence whose pages are read
     const int2* skip;                         //               [B] shared tokens of each sequence, its group
