@@ -154,10 +154,13 @@ __device__ __forceinline__ long long block_base(const ChunkParams& p, int v) {
     return p.offsets ? (long long)max(0, p.offsets[b]) * p.G / RB + b : (long long)b * ((p.N * p.G + RB - 1) / RB);
 }
 
-// float32 K/V take 139 KB of shared memory, so one CTA fits an SM: told so, the compiler uses the
-// registers there are (5 short chunks of 64-element heads: 26.7 us, 29 with 128 registers and spills)
+// Registers.  Without a window or shared prefixes: float32 K/V take up to 139 KB of shared memory, so one CTA
+// fits an SM; told so, the compiler uses the registers there are (5 short chunks of 64-element heads:
+// 26.7 us, 29 with 128 registers and spills).  With them: 128, for two CTAs to an SM where they fit, as a row
+// block's run is short and mostly latency (50 chunks of up to 3 tokens x 32 kv heads over e4m3: 126 us, 201
+// with one; float32, 2 chunks of up to 300 tokens x 32 / 8 heads: 534 and 619; a few small batches 2 to 4% slower).
 template <typename T, KvKind KV, int D, ChunkMode M>
-__global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(const ChunkParams p) {
+__global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 : 0) chunk_simt_kernel(const ChunkParams p) {
     using C = Cfg<KV, D>;
     constexpr int DS = C::DS;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -182,14 +185,16 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
         for (int b = tid; b < p.B; b += nthr) bad |= !seq_ok(p, b);
         if (bad) atomicOr(p.status, TREESPEC_STATUS_BAD_LENGTH);
     }
-    if (tid == 0) {                                      // the last b whose blocks begin at or before unit
-        int lo = 0, hi = chunk_entries<M>(p);
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (block_base<M>(p, mid) <= unit) lo = mid;
-            else hi = mid;
+    if (warp == 0) {                                     // the last entry whose blocks begin at or before unit, 32 ways
+        int lo = 0, n = chunk_entries<M>(p);
+        while (n > 1) {
+            const int step = (n + 31) / 32, i = lane * step;
+            const unsigned le = __ballot_sync(0xffffffffu, i < n && block_base<M>(p, lo + min(i, n - 1)) <= unit) | 1u;
+            const int last = 31 - __clz(le);
+            lo += last * step;
+            n = min(step, n - last * step);
         }
-        seq_s = lo;
+        if (lane == 0) seq_s = lo;
     }
     __syncthreads();
     const int v = seq_s;
@@ -243,13 +248,15 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
 
     const int live_rows = min(rows, sq.live * p.G - r0);  // rows of a padded tree's other slots lie behind them
     const int* ptab = p.page_table + size_t(b) * p.max_pages;
-    auto issue = [&](int tile, int stage) {
+    // a tile's page ids, one load per warp: lane l has that of its tokens 16 l ..
+    auto fetch = [&](int tile) -> int {
+        const int at = t0 + tile * TT + kPage * lane;
+        return lane < TT / kPage && at < t1 ? __ldg(ptab + place(at) / kPage) : -1;
+    };
+    auto issue = [&](int tile, int stage, int pages) {
         const int base = t0 + tile * TT;
         unsigned char* Kd = kv + size_t(stage) * 2 * TT * C::ROWB;
         unsigned char* Vd = Kd + size_t(TT) * C::ROWB;
-        // the tile's page ids, one load per warp: lane l has that of tokens base + 16 l
-        const int at = base + kPage * lane;
-        const int pages = lane < TT / kPage && at < t1 ? __ldg(ptab + place(at) / kPage) : -1;
 #pragma unroll 2
         for (int e = tid; e < TT * C::VPR; e += nthr) {  // a warp takes part in a round as a whole
             const int tt = e / C::VPR, vi = e % C::VPR;
@@ -275,12 +282,12 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
             cp_async16(Vd + tt * C::ROWB + vi * 16, vs, bytes);
         }
         if constexpr (KV == kKvE4m3) {
-            for (int tt = tid; tt < TT; tt += nthr) {
+            for (int tt = tid; tt < TT; tt += nthr) {    // whole warps
                 const int pos = base + tt, tok = place(pos);
+                const int page = __shfl_sync(0xffffffffu, pages, tt / kPage);
                 size_t off = 0;
                 int bytes = 0;
                 if (pos < t1 && (M != kChunkWindow || tok >= low || tok < p.sinks)) {
-                    const int page = ptab[tok / kPage];
                     if (page >= 0 && page < p.num_pool_pages) {
                         off = (size_t(page) * p.Hkv + h) * kPage + tok % kPage;
                         bytes = 4;
@@ -293,7 +300,8 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
         asm volatile("cp.async.commit_group;\n" ::);
     };
 
-    issue(0, 0);                                           // the first tile is on its way while Q is read
+    issue(0, 0, fetch(0));                                 // the first tile is on its way while Q is read
+    int pages = fetch(1);                                  // and the next one's page ids
 #pragma unroll 4
     for (int e = tid; e < RW * 8 * D; e += nthr) {
         const int lr = e / D;
@@ -324,8 +332,12 @@ __global__ void __launch_bounds__(256, KV == kKvF32 ? 1 : 0) chunk_simt_kernel(c
     float* pt_w = Pt + warp * 256;
 
     for (int tile = 0; tile < ntiles; ++tile) {
-        if (tile + 1 < ntiles) issue(tile + 1, (tile + 1) & 1);
-        else asm volatile("cp.async.commit_group;\n" ::);
+        if (tile + 1 < ntiles) {
+            issue(tile + 1, (tile + 1) & 1, pages);
+            pages = fetch(tile + 2);
+        } else {
+            asm volatile("cp.async.commit_group;\n" ::);
+        }
         asm volatile("cp.async.wait_group 1;\n" ::);
         __syncthreads();
         if (has_rows) {
