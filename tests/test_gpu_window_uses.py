@@ -466,3 +466,80 @@ def test_serving_with_a_window_layer_and_a_layer_behind_a_shared_prompt(ts, cuda
         out, status = run_chunk_shared(ts, p, go, sl) if layer else run_chunk_window(ts, p, window, sinks)
         assert status == 0
         check_attention(out, *chunk64(p, *((1 << 30, 0) if layer else (window, sinks))), 400, D, "bf16", True)
+
+
+# ------------------------------------------------------------------------------ few rows to a sequence
+
+FEW = pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 128), (8, 2, 64), (32, 2, 128), (16, 1, 64)])
+
+
+@FEW
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_bad_pages_of_decoded_tokens(ts, cuda_device, hq, hkv, dim, e4m3):  # noqa: F811
+    """Each page of a step and of a tile of 64 tokens bad in turn, several at once, through a window and behind a shared
+    prefix: zeros in their place, and nothing else changes."""
+    p, go, sl = make_shared(cuda_device, [(192, [100, 30, 230])], [1, 1, 1], hq, hkv, dim, "bf16", e4m3, seed=dim + hq)
+    spots = [(0, 12), (0, 13), (0, 14), (0, 15), (1, 12), (1, 13), (2, 16), (2, 19), (2, 21), (2, 25)]   # own tokens
+    table = p.page_table.clone()
+    for b, i in spots:
+        page = int(table[b, i])
+        for pages, scales in ((p.k_pages, p.k_scales), (p.v_pages, p.v_scales)):
+            (pages.view(torch.uint8) if e4m3 else pages)[page] = 0
+            if scales is not None:
+                scales[page] = 1
+    calls = [lambda: run_chunk_window(ts, p, 230, 200), lambda: run_chunk_shared(ts, p, go, sl)]
+    want = [call() for call in calls]
+    assert all(status == 0 for _, status in want)
+    for n, (b, i) in enumerate(spots):
+        p.page_table[b, i] = (-1, p.k_pages.shape[0], -(1 << 31), (1 << 31) - 1)[n % 4]
+        if n % 3 == 0 or n + 1 == len(spots):
+            for call, (ref, _) in zip(calls, want):
+                got, status = call()
+                assert status == BAD_PAGE and torch.equal(got, ref)
+    p.page_table[2, 5] = -1                                    # a shared page, of one sequence: the group reads the first's
+    got, status = calls[1]()
+    assert status == BAD_PAGE and torch.equal(got, want[1][0])
+
+
+@FEW
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_a_prompt_among_decoded_tokens(ts, cuda_device, hq, hkv, dim, e4m3):  # noqa: F811
+    """The mean decides for units of few rows, and one sequence has many of them."""
+    G = hq // hkv
+    n = 60 + 12 * G
+    lens = [(37 * b) % 400 for b in range(n)]
+    new = [0 if G == 16 and b % 5 == 0 else 1 for b in range(n)]   # a mean of up to 16 rows
+    new[6], new[40] = 45, 0
+    assert sum(new) * G <= 16 * n
+    p = make(cuda_device, lens, new, hq, hkv, dim, "bf16", e4m3, seed=3 * dim + hq)
+    assert check_chunk_window(ts, p, 70, 3) == 0
+    p, go, sl = make_shared(cuda_device, [(128, lens[:50]), (0, lens[50:51]), (64, lens[51:])], new, hq, hkv, dim, "bf16", e4m3,
+                            seed=5 * dim + hq)
+    assert check_chunk_shared(ts, p, go, sl) == 0
+
+
+@types
+def test_the_same_call_gives_the_same_bits(ts, cuda_device, dtype, e4m3, kernel):  # noqa: F811
+    """Whatever ran in between and however the launches fell together."""
+    p, go, sl = make_shared(cuda_device, [(320, [(53 * b) % 300 for b in range(24)]), (640, [1, 200, 77])], [1, 2] * 13 + [1], 8, 2,
+                            128, dtype, e4m3, seed=41)
+    other = make(cuda_device, [700, 20], [3, 90], 8, 2, 128, dtype, e4m3, seed=43)
+    want = [run_chunk_shared(ts, p, go, sl, kernel)[0], run_chunk_window(ts, p, 200, 4, kernel)[0]]
+    for i in range(12):
+        if i % 3 == 2:
+            run_chunk_window(ts, other, 50, 1, kernel)
+        assert torch.equal(run_chunk_shared(ts, p, go, sl, kernel)[0], want[0])
+        assert torch.equal(run_chunk_window(ts, p, 200, 4, kernel)[0], want[1])
+
+
+@pytest.mark.parametrize("dtype,e4m3", [("f32", False), ("f32", True), ("bf16", False)])
+def test_more_entries_than_the_tensor_cores_take(ts, cuda_device, dtype, e4m3):  # noqa: F811
+    """1300 sequences, some without new tokens, in 400 groups, some of them empty or of one sequence."""
+    sizes = [(g * 7) % 5 for g in range(400)]
+    sizes[-1] += 1300 - sum(sizes) if sum(sizes) < 1300 else 0
+    groups = [(16 * (g % 9), [(11 * (g + k)) % 60 for k in range(n)]) for g, n in enumerate(sizes)]
+    B = sum(sizes)
+    new = [(b % 4) if b % 10 else 0 for b in range(B)]
+    p, go, sl = make_shared(cuda_device, groups, new, 4, 1, 64, dtype, e4m3, seed=47)
+    assert B > 700 and check_chunk_shared(ts, p, go, sl) == 0
+    assert check_chunk_window(ts, p, 21, 2) == 0
