@@ -34,7 +34,7 @@ namespace treespec {
 namespace {
 
 constexpr int kRows = 64;                // query rows per CTA, at most
-constexpr int kMaxSmem = 224 * 1024;     // dynamic shared memory a CTA may ask for, beside its static 1 KB
+constexpr int kMaxSmem = 220 * 1024;     // dynamic shared memory a CTA may ask for, beside its static 3 KB
 
 enum KvKind { kKvF32, kKvBf16, kKvE4m3 };
 
@@ -143,15 +143,16 @@ __host__ __device__ inline Shape shape_of(int rows) {
 // group's, whose blocks come before all sequences').
 template <ChunkMode M>
 __device__ __forceinline__ long long block_base(const ChunkParams& p, int v) {
-    const int RB = p.rows_block;
-    int b = v;
+    const int to = p.rows_block == 16 ? 4 : p.rows_block == 32 ? 5 : 6;   // a block's rows are 2^to: no 64-bit division
+    auto own = [&](int b) -> long long {
+        return p.offsets ? ((long long)max(0, p.offsets[b]) * p.G >> to) + b
+                         : (long long)b * ((p.N * p.G + p.rows_block - 1) >> to);
+    };
     if constexpr (M == kChunkShared) {
-        if (v < p.groups) return (long long)p.gtab[v].x * p.G / RB + v;
-        b = v - p.groups;
-        return (long long)p.T * p.G / RB + p.groups +
-               (p.offsets ? (long long)max(0, p.offsets[b]) * p.G / RB + b : (long long)b * ((p.N * p.G + RB - 1) / RB));
+        if (v < p.groups) return ((long long)p.gtab[v].x * p.G >> to) + v;
+        return ((long long)p.T * p.G >> to) + p.groups + own(v - p.groups);
     }
-    return p.offsets ? (long long)max(0, p.offsets[b]) * p.G / RB + b : (long long)b * ((p.N * p.G + RB - 1) / RB);
+    return own(v);
 }
 
 // Registers.  Without a window or shared prefixes: float32 K/V take up to 139 KB of shared memory, so one CTA
@@ -172,6 +173,7 @@ __global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 :
     float* Sc = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(Pt) + sh.pt_bytes);   // [stage][K, V][TT]
     __shared__ uint64_t anc_s[kRows][kAncWords];
     __shared__ unsigned long long at_s[kRows];           // element of q and out where a row begins
+    __shared__ int tok_s[kRows];                         // a row's token of the sequence's new ones, -1: none
     __shared__ int low_s[M == kChunkWindow ? kRows : 1];   // first token of a row's window
     __shared__ float fin_s[4][kRows];                    // weights of the token slices of a row in the result
     __shared__ int seq_s;
@@ -218,7 +220,11 @@ __global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 :
         const int which = M == kChunkShared && !group ? p.num_splits + split : split;
         return (size_t(which) * p.T + sq.row0 + row / p.G) * p.Hq + h * p.G + row % p.G;
     };
-    for (int lr = tid; lr < rows; lr += nthr) at_s[lr] = elem(lr);
+    for (int lr = tid; lr < kRows; lr += nthr) {
+        const int i = (r0 + lr) / p.G;
+        tok_s[lr] = lr < rows && i < sq.live ? i : -1;
+        if (lr < rows) at_s[lr] = elem(lr);
+    }
     __syncthreads();
     // last logical token any of the rows may see, and this split's share
     const int last_i = min((r0 + rows - 1) / p.G, sq.live - 1);
@@ -378,8 +384,8 @@ __global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 :
             unsigned seen_by = 0;                        // rows (of the warp's 8) that see this lane's token
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const int lr = rw * 8 + r, i = (r0 + lr) / p.G;
-                bool ok = pos < t1 && lr < rows && i < sq.live;
+                const int lr = rw * 8 + r, i = tok_s[lr];
+                bool ok = pos < t1 && i >= 0;
                 if (ok && j >= 0) ok = p.offsets ? j <= i : (anc_s[lr][j >> 6] >> (j & 63)) & 1ull;
                 // a tree's own tokens are in the window by their depth, which its sets say already
                 if constexpr (M == kChunkWindow)
