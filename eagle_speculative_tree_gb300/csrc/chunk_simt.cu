@@ -15,6 +15,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const ChunkParams p) {
     constexpr int DS = D / 32;
     const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
+    if constexpr (M == kChunkShared) grid_dep_wait();      // the attention kernel
     if (gw >= (long long)p.T * p.Hq) return;
     const int t = int(gw / p.Hq);
     int b;
@@ -157,12 +158,25 @@ __global__ void __launch_bounds__(256) group_merge_kernel(const ChunkParams p) {
     for (int e = 0; e < DS; ++e) store_out<uint16_t>(p.out, size_t(gw) * D + lane * DS + e, acc[e] * lsum);
 }
 
+template <class Kernel>
+cudaError_t launch_rows(Kernel kern, const ChunkParams& p, bool dependent, cudaStream_t s) {   // a warp per row
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(((long long)p.T * p.Hq + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <typename T, int D>
 cudaError_t launch_merge(const ChunkParams& p, ChunkMode mode, cudaStream_t s) {
-    const unsigned blocks = unsigned(((long long)p.T * p.Hq + 7) / 8);
-    if (mode == kChunkShared) chunk_merge_kernel<T, D, kChunkShared><<<blocks, 256, 0, s>>>(p);
-    else chunk_merge_kernel<T, D, kChunkPlain><<<blocks, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    if (mode == kChunkShared) return launch_rows(chunk_merge_kernel<T, D, kChunkShared>, p, true, s);
+    return launch_rows(chunk_merge_kernel<T, D, kChunkPlain>, p, false, s);
 }
 
 }  // namespace
@@ -175,17 +189,7 @@ int chunk_simt_min_rows(int D, int elem) {
 template cudaError_t launch_chunk_simt<kChunkPlain>(const ChunkParams& p, int dtype, int kv_dtype, cudaStream_t s);
 
 cudaError_t launch_group_merge(const ChunkParams& p, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(((long long)p.T * p.Hq + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, p.D == 64 ? group_merge_kernel<64> : group_merge_kernel<128>, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_rows(p.D == 64 ? group_merge_kernel<64> : group_merge_kernel<128>, p, true, s);
 }
 
 cudaError_t launch_chunk_merge(const ChunkParams& p, ChunkMode mode, int dtype, cudaStream_t s) {

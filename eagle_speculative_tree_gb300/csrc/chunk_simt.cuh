@@ -178,6 +178,10 @@ __global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 :
     __shared__ float fin_s[4][kRows];                    // weights of the token slices of a row in the result
     __shared__ int seq_s;
 
+    if constexpr (M == kChunkShared) {                   // the plan's groups; the merge may start where SMs are free
+        grid_dep_wait();
+        grid_dep_release();
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rw = warp % RW, ts = warp / RW;
     const int h = blockIdx.y, split = blockIdx.z;
@@ -507,8 +511,18 @@ cudaError_t launch_typed(const ChunkParams& p, cudaStream_t s) {
     static std::atomic<uint64_t> smem_set{0};
     cudaError_t e = allow_smem(kern, kMaxSmem, smem_set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(unsigned(units), unsigned(p.Hkv), unsigned(p.num_splits)), sh.nwarps * 32, sh.smem, s>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(units), unsigned(p.Hkv), unsigned(p.num_splits));
+    cfg.blockDim = dim3(unsigned(sh.nwarps * 32));
+    cfg.dynamicSmemBytes = sh.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = M == kChunkShared ? 1 : 0;            // behind the plan: the launch does not wait for its end
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
