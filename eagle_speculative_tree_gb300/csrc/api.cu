@@ -591,19 +591,30 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
     if (x.mode != kChunkWindow) return tokens;
     return std::min(tokens, (long long)x.window + x.sinks + 2 * kPage + std::max(kSharedTile, tree_nodes));
 }
-// With a window or shared prefixes, batches of few rows per sequence take the kernel made for them
-// (chunk_few.cuh), unless the call names the other; the lengths are on the device, so the mean counts.
-// Units of 16 rows read K and V again for every 16: decoded tokens of 4 and 8 heads take 171 and 45 us
+// With a window or shared prefixes, the kernel over units of 8 or 16 rows (chunk_few.cuh) is taken, unless the
+// call names the other, for batches of few rows per sequence; the lengths are on the device, so the mean counts.
+// Such units read K and V again for every 16 rows: decoded tokens of 4 and 8 heads take 171 and 45 us
 // (windows, bf16 and e4m3) against 217 and 91 in units of 256 rows, but 32 trees of 8 nodes x 4 heads over
 // 512 tokens 61 against 51, and 47 chunks of 8 .. 40 rows behind 3 prefixes 110 against 90 (bf16) and 120
 // against 107 (e4m3).
-ChunkPlan few_plan(ChunkPlan c, int kernel, const ChunkExtra& x, long long batch, long long rows, int G, int sms) {
-    if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain) return c;
+// It starts sooner, too, so it is also taken for small calls, up to a unit for 8 CTAs, or 4 where the
+// other has codes to widen through more stages (one tree of 16 nodes x 4 heads, 8 kv heads, over 512 tokens:
+// 25 us against 31, e4m3 26 and 36; 4 such trees 33 against 29, e4m3 35 and 33; one tree of 8
+// nodes, e4m3: 25 and 29; 4 trees of 8 nodes x 4 heads behind 2048 shared tokens, e4m3, one kv
+// head: 35 and 39, 8 kv heads: 44 and 39).
+ChunkPlan few_plan(ChunkPlan c, int kernel, int kv_dtype, const ChunkExtra& x, long long batch, long long rows, int G, int Hkv,
+                   int sms) {
+    if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain || G > 16) return c;
+    const bool window = x.mode == kChunkWindow;
     const long long mean = std::max<long long>((rows + batch - 1) / batch, G);
-    if (mean > 16) return c;
+    const int ctas = std::min(2 * sms, kChunkMaxCtas);
+    long long units = batch * ((mean + 15) / 16);
+    if (!window) units += x.groups * ((rows / x.groups + 15) / 16);
+    const bool small = Hkv * units <= ctas / (window && kv_dtype == TREESPEC_DTYPE_E4M3 ? 4 : 8);
+    if (mean > 16 && !small) return c;
     c.few_rows = mean <= 8 ? 8 : 16;
-    c.few_ctas = std::min(2 * sms, kChunkMaxCtas);
-    if (x.mode == kChunkWindow || rows <= 16) c.ctas = 0;   // else the groups' units are of 256 rows
+    c.few_ctas = ctas;
+    if (window || small || rows <= 16) c.ctas = 0;       // else the groups' units are of 256 rows
     return c;
 }
 ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
@@ -611,7 +622,7 @@ ChunkPlan plan_of(const treespec_chunk_shape& s, const ChunkExtra& x = {}) {
     const long long rows = (long long)s.num_tokens * G;
     return few_plan(chunk_plan(s.kernel, s.dtype, s.kv_dtype, s.batch + x.groups, rows, s.num_kv_heads, s.head_dim,
                                window_span((long long)s.max_pages_per_seq * kPage, x, 0), s.num_pool_pages, sms),
-                    s.kernel, x, s.batch, rows, G, sms);
+                    s.kernel, s.kv_dtype, x, s.batch, rows, G, s.num_kv_heads, sms);
 }
 ChunkLayout layout_of(const treespec_chunk_shape& s, const ChunkPlan& c, const ChunkExtra& x = {}) {
     return chunk_layout(c, s.num_tokens, s.num_q_heads, s.num_kv_heads, s.head_dim, 0, s.batch, x);
@@ -669,7 +680,7 @@ ChunkPlan plan_of(const treespec_attn_shape& s, int kv_dtype, const ChunkExtra& 
     const long long rows = (long long)s.batch * s.num_nodes * G;
     return few_plan(chunk_plan(s.kernel, s.dtype, kv_dtype, s.batch + x.groups, rows, s.num_kv_heads, s.head_dim,
                                window_span((long long)s.max_pages_per_seq * kPage, x, s.num_nodes), s.num_pool_pages, sms),
-                    s.kernel, x, s.batch, rows, G, sms);
+                    s.kernel, kv_dtype, x, s.batch, rows, G, s.num_kv_heads, sms);
 }
 ChunkLayout layout_of(const treespec_attn_shape& s, const ChunkPlan& c, const ChunkExtra& x) {
     const long long rows = (long long)s.batch * s.num_nodes;

@@ -525,7 +525,7 @@ int tree_kv_commit_e4m3(void *k_pages, void *v_pages, float *k_scales, float *v_
  * of the pools (the same, or TREESPEC_DTYPE_E4M3 with scales; else the scales are not used);
  * shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q), num_splits is not used.  AUTO takes, of bf16
  * queries, by their rows per sequence (tokens x query heads per kv head, the mean of the batch): up
- * to 16 a kernel bound by the reading of the cache, else TC_STREAM, units of 256 rows.
+ * to 16, and in small calls more, a kernel over units of 16 rows, else TC_STREAM, units of 256.
  * Of trees, all calls give a node the rows of its logical index in the pages (prefix_lens[b] + i).
  */
 
