@@ -21,6 +21,7 @@ namespace treespec {
 namespace {
 
 constexpr int kThreads = 1024;
+constexpr int kUnitThreads = kThreads / 2;                 // where units are listed, half of the threads for them
 static_assert(kChunkMaxBatch <= kThreads && kChunkMaxCtas <= kThreads, "a thread per entry and per range");
 
 struct GroupSmem {
@@ -238,94 +239,93 @@ __device__ __forceinline__ void lay_out(const ChunkParams& p, PlanSmem& all, con
         return make_int2(c[0], tiles <= tune.whole_tiles ? 1 : c[1] - c[0] + 1);
     };
 
-    // ---- the ranges, and behind them the groups' units of 256 rows for the merge: a thread per range or unit
+    // ---- the ranges, and at the same time the groups' units of 256 rows for the merge: a thread per range or unit
     const bool table = M == kChunkShared && !p.few_rows && is_group<M>(p, 0);
     const int nunits = table && total > 0 ? Hkv * sm.units[min(entries, p.groups)] : 0;
+    const bool unit_job = table && tid >= kUnitThreads;        // units; the other threads: ranges
+    int job = unit_job ? tid - kUnitThreads : tid;
 #pragma unroll 1
-    for (int pass = 0; pass < (table ? 2 : 1); ++pass)
+    for (int round = 0; round == 0 || round * kUnitThreads < nunits; ++round, job += kUnitThreads) {
+        const bool by_unit = unit_job || m, on = unit_job ? job < nunits : round == 0 && job < parts;
+        End e{0, 0, 0, 0};
+        int2 share = make_int2(0, 0);
+        int tiles = 0;
+        if (on) {
+            const int index = unit_job ? job : m ? job / m : 0;
+            const long long x = by_unit ? index : job * size_of + min((long long)job, rest);
+            int lo = 0, hi = entries;                  // the last entry that begins at or before x
 #pragma unroll 1
-        for (int job = tid; job < (pass ? nunits : kThreads); job += kThreads) {
-            const bool by_unit = pass || m, on = pass || job < parts;
-            End e{0, 0, 0, 0};
-            int2 share = make_int2(0, 0);
-            int tiles = 0;
-            if (on) {
-                const int index = pass ? job : m ? job / m : 0;
-                const long long x = by_unit ? index : job * size_of + min((long long)job, rest);
-                int lo = 0, hi = entries;                  // the last entry that begins at or before x
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if ((by_unit ? (long long)Hkv * sm.units[mid] : sm.start[mid]) <= x) lo = mid;
+                else hi = mid;
+            }
+            u = seq_units<M>(p, lo, sm.rows[lo], sm.base[lo]);
+            long long y = x - (by_unit ? (long long)Hkv * sm.units[lo] : sm.start[lo]);
+            const long long head = by_unit ? u.np : sm.head[lo];
+            e.b = lo;
+            e.h = int(div_pos(y, head));
+            y -= e.h * head;
+            long long at = 0;                          // of the unit, in its kv head
+            if (by_unit) {
+                e.pr = int(y);
+                if (!m && u.np > 1) at = unit_start<M>(&u, tune.kappa, e.pr);
+            } else if (u.np > 1) {
+                int end = u.np;                        // the last unit that begins at or before y
 #pragma unroll 1
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if ((by_unit ? (long long)Hkv * sm.units[mid] : sm.start[mid]) <= x) lo = mid;
-                    else hi = mid;
-                }
-                u = seq_units<M>(p, lo, sm.rows[lo], sm.base[lo]);
-                long long y = x - (by_unit ? (long long)Hkv * sm.units[lo] : sm.start[lo]);
-                const long long head = by_unit ? u.np : sm.head[lo];
-                e.b = lo;
-                e.h = int(div_pos(y, head));
-                y -= e.h * head;
-                long long at = 0;                          // of the unit, in its kv head
-                if (by_unit) {
-                    e.pr = int(y);
-                    if (!m && u.np > 1) at = unit_start<M>(&u, tune.kappa, e.pr);
-                } else if (u.np > 1) {
-                    int end = u.np;                        // the last unit that begins at or before y
-#pragma unroll 1
-                    while (end - e.pr > 1) {
-                        const int mid = (e.pr + end) >> 1;
-                        const long long z = unit_start<M>(&u, tune.kappa, mid);
-                        if (z <= y) {
-                            e.pr = mid;
-                            at = z;
-                        } else {
-                            end = mid;
-                        }
+                while (end - e.pr > 1) {
+                    const int mid = (e.pr + end) >> 1;
+                    const long long z = unit_start<M>(&u, tune.kappa, mid);
+                    if (z <= y) {
+                        e.pr = mid;
+                        at = z;
+                    } else {
+                        end = mid;
                     }
                 }
-                tiles = u.tiles(e.pr);
-                const int rows = min(u.tpu, (is_group<M>(p, lo) ? sm.rows[lo].n : u.live) - e.pr * u.tpu) * p.G;
-                share = share_of(sm.start[lo] + e.h * sm.head[lo] + at + tune.kappa, tiles, rows, index);
-                if (!by_unit) {
-                    e.j = int(max(0ll, y - at - tune.kappa));
-                    // Short units stay whole: the cut moves to the nearer end of one, and both neighbours see it there
-                    if (tiles <= tune.whole_tiles) e.j = 2 * e.j < tiles ? 0 : tiles;
-                }
             }
-            if (pass) {
-                const_cast<int2*>(p.units)[job] = share;
-                continue;
-            }
-            // one range ends where the next begins; of m CTAs for each unit, those beyond its pieces have nothing
-            auto cut_at = [&](int k) {
-                return k > share.y ? tiles : int(uint32_t(tiles) * uint32_t(k) / uint32_t(share.y));
-            };
-            int4 begin = make_int4(entries, 0, 0, 0);
-            if (on) begin = make_int4(e.b, e.h, e.pr, m ? cut_at(job % m) : e.j);
-            if (job < p.ctas) {
-                sm.ends[job] = begin;
-                sm.pieces[job] = share.y;
-            }
-            __syncthreads();
-            if (job < p.ctas) {
-                CtaPlan out{};
-                out.begin = begin;
-                if (!on) {
-                    out.begin.x = -1;
-                } else {
-                    const bool last = job + 1 >= parts;
-                    out.end = m ? make_int4(e.b, e.h, e.pr, cut_at(job % m + 1))
-                                : last ? make_int4(entries, 0, 0, 0) : sm.ends[job + 1];
-                    out.last_pieces = m ? share.y : last ? 0 : sm.pieces[job + 1];
-                    out.first_cta = share.x;
-                    out.first_pieces = share.y;
-                    const SeqRows& r = sm.rows[e.b];
-                    out.rows = make_int4(r.row0, r.n, r.live, r.S);
-                    out.base = sm.base[e.b];
-                }
-                const_cast<CtaPlan*>(p.plan)[job] = out;
+            tiles = u.tiles(e.pr);
+            const int rows = min(u.tpu, (is_group<M>(p, lo) ? sm.rows[lo].n : u.live) - e.pr * u.tpu) * p.G;
+            share = share_of(sm.start[lo] + e.h * sm.head[lo] + at + tune.kappa, tiles, rows, index);
+            if (!by_unit) {
+                e.j = int(max(0ll, y - at - tune.kappa));
+                // Short units stay whole: the cut moves to the nearer end of one, and both neighbours see it there
+                if (tiles <= tune.whole_tiles) e.j = 2 * e.j < tiles ? 0 : tiles;
             }
         }
+        if (unit_job && on) const_cast<int2*>(p.units)[job] = share;
+        if (round > 0) continue;
+        // one range ends where the next begins; of m CTAs for each unit, those beyond its pieces have nothing
+        auto cut_at = [&](int k) {
+            return k > share.y ? tiles : int(uint32_t(tiles) * uint32_t(k) / uint32_t(share.y));
+        };
+        int4 begin = make_int4(entries, 0, 0, 0);
+        if (on) begin = make_int4(e.b, e.h, e.pr, m ? cut_at(job % m) : e.j);
+        const bool range = !unit_job && job < p.ctas;
+        if (range) {
+            sm.ends[job] = begin;
+            sm.pieces[job] = share.y;
+        }
+        __syncthreads();
+        if (range) {
+            CtaPlan out{};
+            out.begin = begin;
+            if (!on) {
+                out.begin.x = -1;
+            } else {
+                const bool last = job + 1 >= parts;
+                out.end = m ? make_int4(e.b, e.h, e.pr, cut_at(job % m + 1))
+                            : last ? make_int4(entries, 0, 0, 0) : sm.ends[job + 1];
+                out.last_pieces = m ? share.y : last ? 0 : sm.pieces[job + 1];
+                out.first_cta = share.x;
+                out.first_pieces = share.y;
+                const SeqRows& r = sm.rows[e.b];
+                out.rows = make_int4(r.row0, r.n, r.live, r.S);
+                out.base = sm.base[e.b];
+            }
+            const_cast<CtaPlan*>(p.plan)[job] = out;
+        }
+    }
 }
 
 template <ChunkMode M>
@@ -396,7 +396,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 cudaError_t launch_chunk_plan(const PlanParams& p, ChunkMode mode, cudaStream_t s) {
     for (int i = 0; i < p.launches; ++i) {
         const ChunkParams& q = p.launch[i];
-        if ((mode == kChunkShared ? q.entries : q.B) > kChunkMaxBatch || q.ctas < 1 || q.ctas > kChunkMaxCtas)
+        if ((mode == kChunkShared ? q.entries : q.B) > kChunkMaxBatch || q.ctas < 1 ||
+            q.ctas > (mode == kChunkShared && !q.few_rows ? kUnitThreads : kChunkMaxCtas))
             return cudaErrorInvalidValue;
     }
     if (mode == kChunkShared && p.launch[0].groups > kMaxGroups) return cudaErrorInvalidValue;
