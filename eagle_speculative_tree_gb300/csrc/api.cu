@@ -23,6 +23,13 @@ int launch_failed(cudaError_t e) {
     return TREESPEC_ERR_LAUNCH;
 }
 
+// A number of a call's own, never 0: small numbers and their like, which memory that was used before may hold, are
+// spread over 64 bits.
+uint64_t next_epoch() {
+    static std::atomic<uint64_t> calls{0};
+    return (calls.fetch_add(1) + 1) * 0x9e3779b97f4a7c15ull;
+}
+
 constexpr int kDefaultSms = 152;
 constexpr int kMaxDevices = 64;
 
@@ -555,6 +562,7 @@ ChunkLayout chunk_layout(const ChunkPlan& c, long long T, int Hq, int Hkv, int D
         return at;
     };
     L.status = take(kWsAlign);
+    L.published = L.status + kWsAlign / 2;               // in a line of its own
     L.counters = take(size_t(c.ctas) * 8 * 4);
     L.few_counters = take(size_t(c.few_ctas) * 8 * 4);
     L.cleared = off;
@@ -734,7 +742,8 @@ int run_chunk(ChunkParams& p, const ChunkPlan& c, const ChunkLayout& lay, const 
         few.part_acc = reinterpret_cast<float*>(ws + lay.few_acc);
         if (shared && c.ctas) {                          // groups of many rows in a launch of their own
             p.entries = p.groups;
-            few.behind_groups = 1;
+            p.published = few.published = reinterpret_cast<uint64_t*>(ws + lay.published);
+            p.epoch = few.epoch = next_epoch();
             few.entry0 = p.groups;
             few.entries = p.B;
         }

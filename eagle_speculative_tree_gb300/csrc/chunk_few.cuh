@@ -53,6 +53,7 @@ constexpr int kStep = 32;                // tokens a warp takes at a time
 constexpr uint32_t kRegsCompute = 168, kRegsProduce = 88;
 constexpr int kWarpProduce = kWarps, kWarpWalk = kWarps + 2;   // the first of two that produce; the one that walks
 constexpr int kSegRing = 4;              // segments that the walking warp is ahead, at most
+constexpr int kNoPlan = -2;              // in place of a range's begin: the plan did not come
 
 template <int D, bool E4M3, int NR>
 struct CfgFew {
@@ -348,6 +349,16 @@ __device__ __forceinline__ bool produce(const ChunkParams& p, const CUtensorMap*
     return true;
 }
 
+// Whether the plan is there, waited for as all waits are.  By the time that this launch may start it has long been.
+__device__ __forceinline__ bool plan_published(const ChunkParams& p) {
+    if (load_acquire(p.published) == p.epoch) return true;
+    const uint64_t t0 = global_ns();
+    do {
+        if (load_acquire(p.published) == p.epoch) return true;
+    } while (global_ns() - t0 < p.wait_ns);
+    return false;
+}
+
 template <int D, bool E4M3, int NR, ChunkMode M>
 __global__ void __launch_bounds__(kFewThreads, 2)
     chunk_few_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -389,13 +400,24 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    // Behind the groups' launch, which begins to let this one start once the plan is there, the wait comes last: for
-    // what follows, the end of this launch stands for the end of that one
-    if (!p.behind_groups) grid_dep_wait();                 // the plan
+    // Behind the groups' launch, which lets this one start once the plan is there, the wait for that launch comes
+    // last: for what follows, the end of this launch stands for the end of that one.  A start that early carries no
+    // promise on what the plan and all that came before it have written, so this launch gets it from the plan itself:
+    // the plan's first block, which writes or has waited for everything that is read here, stores the call's epoch with
+    // release when it is done, the first warp reads it with acquire, and the barrier below hands that on to the others.
+    // (The call's last kernel takes the epoch away again, so a replayed graph does not find its own old one.)
+    const bool behind_groups = M == kChunkShared && p.published;
+    if (!behind_groups) grid_dep_wait();                   // the plan
     grid_dep_release();
     const int me = blockIdx.x;
-    if (tid < int(sizeof(CtaPlan) / 4))
-        reinterpret_cast<uint32_t*>(sm + C::kOffEnds)[tid] = reinterpret_cast<const uint32_t*>(p.plan + me)[tid];
+    if (warp == 0) {
+        static_assert(sizeof(CtaPlan) / 4 <= 32, "a word of the plan per lane");
+        const bool there = !behind_groups || __all_sync(0xffffffffu, plan_published(p));
+        if (!there && lane == 0) atomicOr(p.status, TREESPEC_STATUS_TIMEOUT);
+        if (lane < int(sizeof(CtaPlan) / 4))
+            reinterpret_cast<uint32_t*>(sm + C::kOffEnds)[lane] =
+                there ? reinterpret_cast<const uint32_t*>(p.plan + me)[lane] : uint32_t(kNoPlan);
+    }
     __syncthreads();
     const bool idle = plan.begin.x < 0;                    // nothing to compute
     // a wait of the whole warp: false for all of its lanes after a timeout of one, or when the CTA has been told to stop
@@ -420,11 +442,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     if (warp >= kWarps) {
         regs_lower<kRegsProduce>();
         if (warp > kWarpWalk) {
-            zero_rows<M, D>(p, lane, 32);
-            if (p.behind_groups) grid_dep_wait();
+            if (plan.begin.x != kNoPlan) zero_rows<M, D>(p, lane, 32);
+            if (behind_groups) grid_dep_wait();
             return;
         }
         if (idle) return;
+        if (behind_groups) fence_proxy_async_global();     // K and V come by TMA: what was acquired, for its proxy too
         if (warp == kWarpWalk) {
             // ------------------------------------------------------------ segments
             Walk<M> walk;

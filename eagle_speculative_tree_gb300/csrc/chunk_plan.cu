@@ -389,6 +389,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         tune.ctas = p.few_rows ? max(1, p.ctas - int((long long)p.ctas * for_groups / sms)) : max(1, for_groups);
     }
     lay_out<M>(p, sm, mine, tune, first);
+    // The second of two launches does not wait for this grid but for this store (chunk_few.cuh)
+    if (M == kChunkShared && first && p.published) {
+        __syncthreads();
+        if (threadIdx.x == 0) store_release(p.published, p.epoch);
+    }
 }
 
 }  // namespace

@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(256) group_merge_kernel(const ChunkParams p) {
     const long long gw = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     grid_dep_wait();                                       // the attention kernels
+    if (p.published && gw == 0 && lane == 0) *p.published = 0;   // read by them alone
     if (gw >= (long long)p.T * p.Hq) return;
     const int t = int(gw / p.Hq), hq = int(gw % p.Hq);
     int b;

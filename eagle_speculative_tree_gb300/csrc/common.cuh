@@ -35,6 +35,15 @@ __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a -
 __device__ __forceinline__ void grid_dep_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+__device__ __forceinline__ void store_release(uint64_t* at, uint64_t v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t load_acquire(const uint64_t* at) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+    return v;
+}
+
 // bf16 <-> f32 on raw bit patterns (bf16 is the high half of an f32).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -227,7 +236,7 @@ enum ChunkMode {
 };
 struct ChunkLayout {
     // [status, cleared): zeroed before every call
-    size_t status, counters, few_counters, cleared, anc, lens, nn, flags, depth, gtab, skip, group_units, units, plan, few_plan, ml,
+    size_t status, published, counters, few_counters, cleared, anc, lens, nn, flags, depth, gtab, skip, group_units, units, plan, few_plan, ml,
         acc, few_ml, few_acc, rows_ml, rows_acc, total;
 };
 // One CTA's range of KV tiles (chunk_plan.cu), as (entry, kv head, unit, tile) of its first tile and of the
@@ -261,7 +270,6 @@ struct ChunkParams {
     int num_splits, split_tokens, rows_block; // SIMT
     int ctas, tpq, inv_g;                     // persistent: CTAs; tokens per 128-row query tile, 128 / G; ceil(2^16 / G)
     int tpu;                                  //             tokens per unit
-    int behind_groups;                        // few rows: the launch before is the groups', not the plan
     int few_rows;                             // few rows: rows of a unit, 8 or 16; 0: units of 256
     float scale_log2;
     uint64_t wait_ns;
@@ -280,6 +288,8 @@ struct ChunkParams {
     const int32_t* group_units;               //               [groups] units before each group, one kv head
     float* rows_ml;                           //               persistent: the rows' two parts for the merge,
     float* rows_acc;                          //               [2][T][Hq][2] and [2][T][Hq][D]
+    uint64_t* published;                      //               two launches: holds `epoch` from the end of the plan to the
+    uint64_t epoch;                           //               merge; else NULL
 };
 // Groups of sequences (kChunkShared) as the caller gives them.
 struct GroupParams {
