@@ -424,7 +424,8 @@ struct Spoil {
     uint32_t hidden;       // of V as the MMA reads it, in tokens that it does not see
     bool key;              // a NaN in K of a token that it sees
 };
-// Adds tokens from .. to - 1 of the segment's sequence, by one warp; pages outside the pool hold zeros.
+// Adds tokens from .. to - 1 of the segment's sequence, by one warp; pages outside the pool hold zeros, and so do those
+// of which no row of the unit sees a token.
 template <int D, bool E4M3, ChunkMode M>
 __device__ __forceinline__ void look(const ChunkParams& p, const Seg<M>& s, const Sight<M>& v, int from, int to, Spoil& f) {
     constexpr int DS = D / 32;
@@ -435,6 +436,8 @@ __device__ __forceinline__ void look(const ChunkParams& p, const Seg<M>& s, cons
     const int* ptab = p.page_table + size_t(s.sequence()) * p.max_pages;
     for (int q0 = from & ~(kPage - 1); q0 < to; q0 += kPage) {
         q0 = s.over_gap(q0);
+        if constexpr (M == kChunkWindow)                   // as the producers: zeros to the MMA, and not ours to read
+            if (q0 + kPage <= s.low && q0 >= p.sinks) continue;
         const int page = __ldg(ptab + q0 / kPage);
         if (page < 0 || page >= p.num_pool_pages) continue;
 #pragma unroll 8
