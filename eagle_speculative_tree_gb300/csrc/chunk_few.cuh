@@ -657,7 +657,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
                         for (int h = 0; h < NR; ++h)
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) x[u][h][2 * i + b] *= ks * sc[h][b];
+                            for (int b = 0; b < 2; ++b) {  // in this order: ks sc may pass the range where the score does not
+                                float& y = x[u][h][2 * i + b];
+                                y = y * sc[h][b] * ks;
+                            }
                     }
             }
             __syncwarp();
