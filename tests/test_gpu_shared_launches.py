@@ -1,11 +1,12 @@
-"""Shared prefixes where the groups' rows and the sequences' own are two launches side by side."""
+"""Shared prefixes where the groups' rows and the sequences' own are two launches side by side, and trees of few rows in
+every form that AUTO takes of them."""
 import numpy as np
 import pytest
 import torch
 
 from chunk_util import check_attention
-from test_gpu_window import ints, run_chunk_shared, ts  # noqa: F401
-from window_util import chunk64, make_shared
+from test_gpu_window import ints, run_chunk_shared, run_tree_shared, shared_tree_problem, ts  # noqa: F401
+from window_util import chunk64, make_shared, tree64
 
 pytestmark = pytest.mark.gpu
 pools = pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
@@ -77,3 +78,88 @@ def test_each_of_many_calls_finds_its_own_plan(ts, cuda_device, e4m3, graph):  #
             if turn == 0 and i < 3:
                 p.prefix = p.prefix_lens.tolist()
                 check_attention(want[rows], *chunk64(p), max(p.prefix) + 3, 128, "bf16", True)
+
+
+# ------------------------------------------------------------------------------ trees of few rows
+
+def inner(offsets, lens):
+    """The groups between the first and the last, whose sequences then share nothing."""
+    return offsets[1:-1].contiguous(), lens[1:-1].contiguous()
+
+
+# trees behind shared prefixes in units of 8 or 16 rows: groups, nodes, N, hq, hkv, dim, whether the first and last group are
+# left out, kernels of a call: the prologue, the plan, the attention (twice where the groups' rows are a launch of their own)
+# and the merge
+FEW_TREES = [
+    ([(130, [5, 0])], [4, 2], 4, 8, 2, 128, False, 4),
+    ([(64, [1, 70, 0])], [2, 1, 2], 2, 8, 2, 64, False, 4),
+    ([(300, [0, 9])], [1, 1], 1, 32, 2, 128, False, 4),
+    ([(40, [30, 0]), (700, list(range(0, 300, 20))), (257, list(range(0, 900, 60))), (128, [0] * 5), (90, [8, 9, 60])],
+     [1, 4, 3, 2, 4] * 8, 4, 32, 8, 128, True, 5),
+    ([(40, [30, 0]), (700, list(range(0, 300, 20))), (257, list(range(0, 900, 60))), (128, [0] * 5), (90, [8, 9, 60])],
+     [1, 2, 2] * 13 + [1], 2, 16, 4, 64, True, 5),
+    ([(64, [0] * 7), (1999, [3 * b for b in range(20)]), (0, [5])], [3, 4, 1, 2] * 7, 4, 16, 8, 128, False, 5),
+    ([(70, [9]), (1000, [7 * b for b in range(38)]), (66, [3])], [1] * 40, 1, 64, 4, 64, True, 5),
+]
+
+
+@pools
+@pytest.mark.parametrize("case", FEW_TREES, ids=lambda c: f"{len(c[0])}g-{len(c[1])}x{c[2]}x{c[3]}-d{c[5]}-{c[7]}k")
+def test_trees_of_few_rows_behind_shared_prefixes(ts, cuda_device, case, e4m3):  # noqa: F811
+    """Against the definition, with padding rows whose queries are NaN, and to the bit whatever ran in between."""
+    groups, sizes, N, hq, hkv, dim, cut, kernels = case
+    p, q, parents, go, sl = shared_tree_problem(cuda_device, groups, sizes, N, hq, hkv, dim, "bf16", e4m3, sum(sizes))
+    assert len(sizes) == go[-1].item()
+    if cut:
+        go, sl = inner(go, sl)
+    prob = ts.attn_problem(q, p.k_pages, p.page_table)
+    kv = ts.DTYPE_E4M3 if e4m3 else ts.DTYPE_BF16
+    own = torch.empty(ts.attn_shared_workspace_bytes(prob, kv, sl.shape[0]), dtype=torch.uint8, device=cuda_device)
+    out, count = launches(ts, lambda: ts.tree_attn_verify_shared(q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, parents,
+                                                                 go, sl, workspace=own, **p.scales()))
+    assert ts.read_status(own) == 0 and count == kernels
+    ref, spread, reach = tree64(p, q, parents.cpu().numpy())
+    check_attention(out, ref, spread, reach, max(S + n for S, n in zip(p.prefix, p.new)), dim, "bf16", True)
+    other, go2, sl2 = two_launch_chunks(cuda_device, e4m3, 53)
+    for turn in range(6):
+        if turn % 2:
+            run_chunk_shared(ts, other, go2, sl2)
+        again, status = run_tree_shared(ts, p, q, parents, go, sl)
+        assert status == 0 and torch.equal(again, out)
+
+
+@pools
+def test_trees_of_few_rows_replay_from_a_graph(ts, cuda_device, e4m3):  # noqa: F811
+    """Two launches over trees: lengths, trees and shares change between the replays."""
+    groups, sizes, N, hq, hkv, dim = FEW_TREES[3][:6]
+    p, q, parents, go, sl = shared_tree_problem(cuda_device, groups, sizes, N, hq, hkv, dim, "bf16", e4m3, 55)
+    prob = ts.attn_problem(q, p.k_pages, p.page_table)
+    kv = ts.DTYPE_E4M3 if e4m3 else ts.DTYPE_BF16
+    ws = torch.empty(ts.attn_shared_workspace_bytes(prob, kv, sl.shape[0]), dtype=torch.uint8, device=cuda_device)
+    out = torch.empty_like(q)
+
+    def call():
+        ts.tree_attn_verify_shared(q, p.k_pages, p.v_pages, p.page_table, p.prefix_lens, parents, go, sl, out, workspace=ws,
+                                   **p.scales())
+
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    lens, nodes = sl.tolist(), list(sizes)
+    for turn in range(4):
+        q.normal_()
+        sl.copy_(ints([max(0, x - 64 * turn) for x in lens], cuda_device))
+        sizes = [max(1, n - (b + turn) % 2) for b, n in enumerate(nodes)]
+        rows = [[-1] + [max(0, i - 1 - turn % 2) for i in range(1, n)] + [-2] * (N - n) for n in sizes]
+        parents.copy_(ints(rows, cuda_device))
+        p.new = sizes
+        out.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert ts.read_status(ws) == 0
+        assert torch.equal(got, run_tree_shared(ts, p, q, parents, go, sl)[0])
+        ref, spread, reach = tree64(p, q, parents.cpu().numpy())
+        check_attention(got, ref, spread, reach, max(S + n for S, n in zip(p.prefix, p.new)), dim, "bf16", True)
