@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from chunk_util import check_attention
-from test_gpu_window import ints, run_chunk_shared, run_tree_shared, shared_tree_problem, ts  # noqa: F401
+from test_gpu_window import (TIMEOUT, ints, run_chunk_shared, run_chunk_window, run_tree_shared, shared_tree_problem,  # noqa: F401
+                             ts)
 from window_util import chunk64, make_shared, tree64
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +164,44 @@ def test_trees_of_few_rows_replay_from_a_graph(ts, cuda_device, e4m3):  # noqa: 
         assert torch.equal(got, run_tree_shared(ts, p, q, parents, go, sl)[0])
         ref, spread, reach = tree64(p, q, parents.cpu().numpy())
         check_attention(got, ref, spread, reach, max(S + n for S, n in zip(p.prefix, p.new)), dim, "bf16", True)
+
+
+# ------------------------------------------------------------------------------ limits
+
+@pools
+@pytest.mark.parametrize("kind", ["chunks", "trees"])
+def test_waits_that_run_out_in_two_launches_leave_the_next_call_right(ts, cuda_device, kind, e4m3):  # noqa: F811
+    if kind == "chunks":
+        p, go, sl = two_launch_chunks(cuda_device, e4m3, 57)
+        call = lambda: run_chunk_shared(ts, p, go, sl)  # noqa: E731
+    else:
+        p, q, parents, go, sl = shared_tree_problem(cuda_device, *FEW_TREES[3][:6], "bf16", e4m3, 57)
+        call = lambda: run_tree_shared(ts, p, q, parents, go, sl)  # noqa: E731
+    want, status = call()
+    assert status == 0
+    for limit in (1, 500, 1500, 3000, 8000, 25000):
+        ts.set_wait_limit_ns(limit)
+        try:
+            got, status = call()
+        finally:
+            ts.set_wait_limit_ns(0)
+        assert status in (0, TIMEOUT) and (limit > 1 or status == TIMEOUT)
+        if status == 0:
+            assert torch.equal(got, want)
+        got, status = call()
+        assert status == 0 and torch.equal(got, want)
+
+
+@pools
+@pytest.mark.parametrize("sequences,kernel", [(40, 0), (3, 0), (40, 5), (40, 1)], ids=["two", "one", "units", "simt"])
+def test_a_batch_without_new_tokens_writes_nothing(ts, cuda_device, sequences, kernel, e4m3):  # noqa: F811
+    """Rows that no sequence owns, as in a captured call whose sequences have all ended; then one sequence has a token."""
+    p, go, sl = make_shared(cuda_device, [(100, [b for b in range(sequences)])], [1] * sequences, 32, 8, 128, "bf16", e4m3, seed=59)
+    p.chunk_offsets.zero_()
+    for out, status in (run_chunk_shared(ts, p, go, sl, kernel), run_chunk_window(ts, p, 50, 2, kernel)):
+        assert status == 0 and (out == 3).all()
+    p.chunk_offsets[2:] = 1
+    p.new = [int(b == 1) for b in range(sequences)]
+    for (out, status), window in ((run_chunk_shared(ts, p, go, sl, kernel), (1 << 30, 0)), (run_chunk_window(ts, p, 50, 2, kernel), (50, 2))):
+        assert status == 0 and (out[1:] == 3).all()
+        check_attention(out[:1], *chunk64(p, *window), 200, 128, "bf16", kernel != 1)
