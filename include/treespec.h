@@ -524,13 +524,16 @@ int tree_kv_commit_e4m3(void *k_pages, void *v_pages, float *k_scales, float *v_
  * tree_attn_verify_e4m3.  Of the tree calls, shape->dtype is that of q and out and kv_dtype that
  * of the pools (the same, or TREESPEC_DTYPE_E4M3 with scales; else the scales are not used);
  * shape->kernel is AUTO, SIMT or TC_STREAM (bf16 q), num_splits is not used.  AUTO takes, of bf16
- * queries, by their rows per sequence (tokens x query heads per kv head, the mean of the batch): up
- * to 16, and in small calls more, a kernel over units of 16 rows, else TC_STREAM, units of 256.
+ * queries, by the mean rows per sequence (num_tokens / batch, or num_nodes, x query heads per kv
+ * head): up to 16, and in small calls more, a kernel over units of 8 or 16 rows, else TC_STREAM,
+ * units of 256, which it also takes with more than 16 query heads per kv head.  The host knows the
+ * shape alone, so a captured graph keeps its choice whatever its lengths become.  Batches of more
+ * than 1024 sequences (and groups) run on CUDA cores, as SIMT and float32 queries do.
  * Of trees, all calls give a node the rows of its logical index in the pages (prefix_lens[b] + i).
  */
 
 /* Workspace bytes of the two window calls (0 if the arguments are invalid): on tensor cores about
- * tree_chunk_attn's, or an eighth of it for batches of few rows. */
+ * tree_chunk_attn's 40 MB in units of 256 rows, an eighth of it in units of 8 or 16. */
 size_t treespec_chunk_window_workspace_bytes(const treespec_chunk_shape *shape, int32_t window, int32_t sinks);
 size_t treespec_attn_window_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t window,
                                             int32_t sinks);
@@ -560,7 +563,9 @@ int tree_attn_verify_window(const void *q, const void *k_pages, const void *v_pa
                             size_t workspace_bytes, treespec_stream_t stream);
 
 /* Workspace bytes of the two calls over shared prefixes (0 if the arguments are invalid): on tensor cores
- * tree_chunk_attn's, some 5 MB and two float32 states of every row: 8 (D + 2) bytes a token and query head. */
+ * two float32 states of every row, 8 (D + 2) bytes a token and query head, and those of the window calls:
+ * 40 MB in units of 256 rows, 5 MB in small calls of units of 8 or 16, both where the groups' rows are in
+ * units of 256 and the sequences' own in small ones. */
 size_t treespec_chunk_shared_workspace_bytes(const treespec_chunk_shape *shape, int32_t num_groups);
 size_t treespec_attn_shared_workspace_bytes(const treespec_attn_shape *shape, int32_t kv_dtype, int32_t num_groups);
 
@@ -578,8 +583,8 @@ size_t treespec_attn_shared_workspace_bytes(const treespec_attn_shape *shape, in
  *   shared_lens   [num_groups]      int32 device, 0 <= shared_lens[g] <= the prefix length of
  *                                   every sequence of the group that has new tokens
  * Shared lengths that do not hold to that, and group offsets out of order or range, set BAD_LENGTH
- * and the group (all groups, in case of offsets) is computed as if it shared nothing; so it is,
- * without a status, where chunk_offsets are out of order.
+ * and the group (all groups, in case of offsets) is computed as if it shared nothing.  So are all
+ * groups where chunk_offsets are out of order or range, which sets BAD_LENGTH as in tree_chunk_attn.
  * 1 <= num_groups <= 1024 (TREESPEC_KERNEL_TC_STREAM: batch + num_groups <= 1024).
  * A tree's padding rows are zeros; what their q holds does not matter.
  */
