@@ -601,15 +601,16 @@ long long window_span(long long tokens, const ChunkExtra& x, int tree_nodes) {
 }
 // With a window or shared prefixes, the kernel over units of 8 or 16 rows (chunk_few.cuh) is taken, unless the
 // call names the other, for batches of few rows per sequence; the lengths are on the device, so the mean counts.
+// (Rows that a batch has room for and does not use count too, and so do those of a prompt among decoded tokens.)
 // Such units read K and V again for every 16 rows: decoded tokens of 4 and 8 heads take 171 and 45 us
-// (windows, bf16 and e4m3) against 217 and 91 in units of 256 rows, but 32 trees of 8 nodes x 4 heads over
-// 512 tokens 61 against 51, and 47 chunks of 8 .. 40 rows behind 3 prefixes 110 against 90 (bf16) and 120
-// against 107 (e4m3).
+// (windows, bf16 and e4m3) against 214 and 91 in units of 256 rows, but 32 trees of 8 nodes x 4 heads over
+// 512 tokens 61 against 51, and 47 chunks of 8 .. 40 rows behind 3 prefixes 110 against 90 (bf16) and 124
+// against 104 (e4m3).
 // It starts sooner, too, so it is also taken for small calls, up to a unit for 8 CTAs, or 4 where the
 // other has codes to widen through more stages (one tree of 16 nodes x 4 heads, 8 kv heads, over 512 tokens:
-// 25 us against 31, e4m3 26 and 36; 4 such trees 33 against 29, e4m3 35 and 33; one tree of 8
-// nodes, e4m3: 25 and 29; 4 trees of 8 nodes x 4 heads behind 2048 shared tokens, e4m3, one kv
-// head: 35 and 39, 8 kv heads: 44 and 39).
+// 25 us against 33, e4m3 25 and 35; 4 such trees 34 against 30, e4m3 35 and 33; one tree of 8
+// nodes, e4m3: 26 and 29; 4 trees of 8 nodes x 4 heads behind 2048 shared tokens, e4m3, one kv
+// head: 35 and 39, 8 kv heads: 41 and 38).
 ChunkPlan few_plan(ChunkPlan c, int kernel, int kv_dtype, const ChunkExtra& x, long long batch, long long rows, int G, int Hkv,
                    int sms) {
     if (c.kernel != TREESPEC_KERNEL_TC_STREAM || kernel != TREESPEC_KERNEL_AUTO || x.mode == kChunkPlain || G > 16) return c;

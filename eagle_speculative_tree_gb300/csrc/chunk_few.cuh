@@ -9,12 +9,12 @@
 // no step waits for another warp's.  A warp holds 8 NR rows of Q and O in registers (NR = 1 or 2), and
 // a step is 32 tokens in 16 x 8 x 16 matrix instructions with the rows across: S^T = K Q^T (16 tokens x
 // 8 rows) and O^T += V^T P^T (16 head elements x 8 rows), so eight rows waste nothing; with the rows
-// along the other side of 16, window decode (below) took 190 us for 185.  A lane reads 16 bytes of K at
+// along the other side of 16, window decode (below) took 3% longer.  A lane reads 16 bytes of K at
 // a time, which permutes the head elements (Q's alike); V^T is transposed on the way from shared memory
 // (ldmatrix), P^T by movmatrix.
 //
 // A CTA is four such warps, two that fill the K and V rings by TMA and one that walks along the CTA's
-// range and hands its segments on, ahead of the others (185 us without it, 175 with); two CTAs to an SM,
+// range and hands its segments on, ahead of the others (without it window decode took 6% longer); two CTAs to an SM,
 // so that one computes while the other joins.  The warps take the steps of the range in turn.  Units,
 // pieces and segments are those of chunk_units.cuh, one range per CTA laid out by chunk_plan.cu; at the
 // end of a unit (or piece) the warps' states are joined through shared memory, and the pieces of a cut
@@ -29,6 +29,10 @@
 // holds Q's 8 bits from the row's largest element down to 2^-28 of it, and what is smaller is off by
 // 2^-39 of that element.  V's codes are widened to bf16 (exact), as P times V's scale is bf16, whose
 // range it needs.
+//
+// P (over e4m3 times V's scale) is rounded to bf16 for the product with V, by at most 2^-8 of each weight;
+// the sum that divides it, O and the running maxima stay in 32 bits.  With both the weights and the result rounded, a
+// bf16 result is off by 0.0023 of its norm, by 0.0017 with the result alone; P in two halves would double P V.
 //
 // A value that a row may not see must not reach it, and P V multiplies it by zero.  V of tokens that no
 // row of the unit sees is overwritten with zeros before use; a step that only some rows see whole is
@@ -263,9 +267,9 @@ __device__ __forceinline__ int tile_pages(const ChunkParams& p, const Seg<M>& s,
 // chain of a wait, two votes, an arrival and the issue of the copies, 0.5 us or more however little it
 // copies.  With two stages to a computing warp (kPairs) it therefore takes the whole KV tile, K and V of
 // two steps, and the producers take every second tile of the CTA; as one warp for K and one for V, a step at a
-// time, the computing warps waited for them (window decode e4m3: 59 us so, 49 this way).  With one
+// time, the computing warps waited for them (window decode e4m3 took a fifth longer).  With one
 // stage to a warp, V of a step would hold up K of the next, so there they are one for K and one
-// for V (window decode: 223 us in tiles, 174 this way).
+// for V (in tiles, window decode took 28% longer).
 //
 // Lanes 4 i .. 4 i + 3 own page i of the iteration, the first of them its TMA copy and each a quarter of
 // its scales, which come by plain asynchronous copies: a bulk copy of 64 bytes takes as long to issue as

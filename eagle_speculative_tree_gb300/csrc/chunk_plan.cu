@@ -354,8 +354,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         // Two launches, the groups' on units of 256 rows with an SM for each CTA and the sequences' with
         // two CTAs to an SM, run at the same time: each gets SMs by its tiles, a tile of 256 rows
         // counted 2.3 times (64 sequences of one token, 20 .. 600 tokens of their own behind 8192
-        // shared ones: 65 us, e4m3 66; 69 and 73 counted 1.4 times, 71 and 66 counted 3.4; 89 one
-        // launch after the other).
+        // shared ones: 59 us, e4m3 62; 63 and 69 counted 1.4 times, 61 and 58 counted 3.4; one launch
+        // after the other took an eighth longer).
         const int g0 = a.launch[1].groups, tpu = a.launch[1].tpu, few_tpu = a.launch[0].tpu;
         float load[2] = {0.f, 0.f};
         if (int(threadIdx.x) < p.B && mine.S >= 0) {

@@ -18,7 +18,7 @@
 // new tokens of a group's sequences, which are packed) run over the shared tokens; the
 // sequences' own blocks begin behind these.  Both leave partial states for the merge.
 // Small calls are bound by one CTA's run (5 float32 chunks of up to 130 tokens x 4 heads of 64 through windows
-// of 100: 19 us of a call of 23; 4 chunks behind 800 shared tokens: 18 of 30, the plan 4, the
+// of 100: 19 us of a call of 23; 4 chunks behind 800 shared tokens: 18 of 27, the plan 4, the
 // merge 4), large ones by float32 arithmetic on CUDA cores.
 //
 // Layout of a CTA: RW row-warps (8 rows each) x TS token slices (32 tokens each); QK^T has
@@ -158,8 +158,8 @@ __device__ __forceinline__ long long block_base(const ChunkParams& p, int v) {
 // Registers.  Without a window or shared prefixes: float32 K/V take up to 139 KB of shared memory, so one CTA
 // fits an SM; told so, the compiler uses the registers there are (5 short chunks of 64-element heads:
 // 26.7 us, 29 with 128 registers and spills).  With them: 128, for two CTAs to an SM where they fit, as a row
-// block's run is short and mostly latency (50 chunks of up to 3 tokens x 32 kv heads over e4m3: 126 us, 201
-// with one; float32, 2 chunks of up to 300 tokens x 32 / 8 heads: 534 and 619; a few small batches 2 to 4% slower).
+// block's run is short and mostly latency (float32, chunks of 300 and 245 tokens x 32 / 8 heads over 1137 and 761:
+// 521 us, 656 with one; small calls take as long either way).
 template <typename T, KvKind KV, int D, ChunkMode M>
 __global__ void __launch_bounds__(256, M != kChunkPlain ? 2 : KV == kKvF32 ? 1 : 0) chunk_simt_kernel(const ChunkParams p) {
     using C = Cfg<KV, D>;

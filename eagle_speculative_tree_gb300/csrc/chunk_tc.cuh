@@ -27,6 +27,9 @@
 // Rows are spread over the four warps of a tile (row r in lane r / 4 of warp r % 4), so that
 // the few rows of a decoded token share the epilogue's work.
 //
+// P is one operand of a bf16 product, so it is rounded to bf16, over e4m3 times V's scale: at most 2^-8 of each weight.
+// The sum that divides it, O, the running maxima and the parts stay in 32 bits.
+//
 // A value that a row may not see must not reach it.  S is masked by selection, but P V
 // multiplies a masked token's V by zero, and 0 x NaN is NaN.  A row whose O comes out
 // non-finite, and does not see what makes it so, is therefore recomputed from the visible tokens
@@ -38,15 +41,15 @@
 // rows sees, those from the first token of its first row's window on.  Tiles are numbered without
 // the gap, which depends on the unit alone, so the cut, the pieces and the joins are as above;
 // pages that no row of the unit sees count as zeros.  32 trees of 40 .. 64 nodes x 8 heads over windows
-// of 4096: 284 us, 4 prompts of 900 .. 5000 tokens through windows of 1024: 207 us; bound as the plain
+// of 4096: 283 us, 4 prompts of 900 .. 5000 tokens through windows of 1024: 208 us; bound as the plain
 // form is, by the chain of a tile (about 1900 clocks for two query tiles, of which the matrix
 // instructions alone would take 1260 at the measured rate), and by 8 unit changes per CTA of the prompts.
 // Shared prefixes (kChunkShared): the list of units begins with those of the groups.  A group's
 // units are 2 floor(128 / G) consecutive rows' tokens of its packed rows, whichever sequences they
 // belong to, over the shared tokens, which all of them see whole; a sequence's own units begin
 // behind these.  Both leave (m, l, O) of each row for the merge (chunk_simt.cu), which also joins
-// the pieces of a group's unit: 256 rows joined here, by the last CTA of a unit, took 84 us of a
-// launch that takes 39 without (64 decoded tokens behind 8192 shared ones).  32 trees of 9 .. 16
+// the pieces of a group's unit: with 256 rows joined here, by the last CTA of a unit, a launch took more
+// than twice as long (64 decoded tokens behind 8192 shared ones).  32 trees of 9 .. 16
 // nodes x 4 heads behind 16384 shared tokens: 168 us; the same tokens read by every sequence for
 // itself would be 2.1 GB more.
 // In both the ranges are laid out ahead by chunk_plan.cu.
@@ -134,9 +137,9 @@ __device__ __forceinline__ Row row_of(const ChunkParams& p, const Seg<M>& s, int
 // Stores N 16-byte units of each lane's row, those with `ok`.  A store of 32 lanes to as many rows takes the
 // memory pipe 32 turns, some 4000 (bf16) or 8000 clocks for the 256 rows of a unit; so where more than 8 rows
 // are there, four lanes first exchange their units (kExchange), and a store writes 64 bytes of 8 rows: 4 prompts
-// through a window 208 us, 216 without; 32 trees 286 and 293; 6 prompts without a window 362 and 378.  Over
-// 8-bit pools (prompts through a window 383, 378 without; 47 short chunks behind 3 prefixes 115 and 108) and
-// for the parts of shared prefixes (the same chunks in bf16: 96 and 93) the exchange costs more than it gives.
+// through a window 208 us, 216 without; 32 trees 283 and 290; 6 prompts without a window 364 and 380.  Over
+// 8-bit pools (prompts through a window 383, 376 without; 47 short chunks behind 3 prefixes 112 and 104) and
+// for the parts of shared prefixes (the same chunks in bf16: 93 and 90) the exchange costs more than it gives.
 template <int N, bool kExchange>
 __device__ __forceinline__ void store_row(void* row, bool ok, uint32_t (&w)[4 * N]) {
     const int lane = threadIdx.x & 31;

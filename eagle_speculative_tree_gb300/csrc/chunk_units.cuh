@@ -22,13 +22,13 @@ struct TuneUnits {                   // units of 256 rows (chunk_tc.cuh)
     // heads: 33 and 25).
     static constexpr int kMinTiles = 4, kMinTilesManyRows = 9;
     // where the ranges are planned ahead (chunk_plan.cu), a CTA starts sooner and shorter pieces pay (8 nodes
-    // x 4 heads over 2048 e4m3 tokens, 512 of them in the window: 31.0 us in pieces of 2 tiles, 32.8 of 4)
+    // x 4 heads over 2048 e4m3 tokens, 512 of them in the window: 29.1 us in pieces of 2 tiles, 31.1 of 4)
     static constexpr int kPlanMinTiles = 2;
     // There, too, the fixed cost counts in each type's tiles, 0.8 us of bf16 and 1.3 of e4m3 (4 prompts
-    // through a window and 32 trees behind a shared prefix, bf16: 217 and 171 us, and 219 and 176 with 7;
-    // 4 prompts and 47 short chunks behind 3 prefixes, e4m3: 379 and 108 us, and 395 and 110 with 7); but
-    // the groups of decoded tokens are cut into pieces whose stores count for more (64 sequences, e4m3:
-    // 66 us, and 69 with 7).
+    // through a window and 32 trees behind a shared prefix, bf16: 208 and 168 us, and 212 and 174 with 7;
+    // 4 prompts and 47 short chunks behind 3 prefixes, e4m3: 376 and 104 us, and 393 and 106 with 7); but
+    // the groups of decoded tokens are cut into pieces whose stores count for more (64 sequences, bf16 and
+    // e4m3: 59 and 62 us, and 65 and 66 with 7).
     static constexpr int kPlanKappa = 10, kPlanKappaCodes = 5;
     static constexpr int kWholeTiles = 4;
 };
